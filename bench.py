@@ -201,8 +201,8 @@ def load_peaks():
     return dict(FALLBACK_PEAKS), "fallback"
 
 
-KERNEL_SOURCES = ("tc_gemm.cu", "tc_gemm_common.cuh", "ptx.cuh", "act.cuh", "tpmlp_internal.h",
-                  "tpmlp_api.cu")
+KERNEL_SOURCES = ("tc_gemm.cu", "tc_gemm_body.cuh", "tc_gemm_common.cuh", "ckpt8.cuh", "ptx.cuh", "act.cuh",
+                  "tpmlp_internal.h", "tpmlp_api.cu")
 
 
 def kernel_sources_sha256() -> str:

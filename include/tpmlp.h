@@ -105,7 +105,8 @@ TPMLP_API tpmlp_status tpmlp_plan_create(const tpmlp_desc* desc, tpmlp_plan** ou
 TPMLP_API void tpmlp_plan_destroy(tpmlp_plan* plan);
 
 /* Bytes of device workspace every call needs.  fp32 plans: a 256-byte block
- * holding the device status word.  bf16 plans: that block, then the ticket
+ * holding the device status word (and, once a norm of the heads is set,
+ * tpmlp_attn_plan_set_qk_norm_rope, the partial sums of its gains' gradients).  bf16 plans: that block, then the ticket
  * counters and fp32 partial accumulators of the stream-K schedules (16 KB +
  * 160 x 256 KB, about 42 MB; see tpmlp_plan_set_stream_k).  The caller allocates it once,
  * zero-filled, and passes it to every call of this plan; calls that share it
@@ -317,6 +318,122 @@ TPMLP_API tpmlp_status tpmlp_attn_out_backward(const tpmlp_plan* plan, const voi
 TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const void* X, const void* const* Wqkv,
                                                const void* const* dQKV, void* dX, void* const* dWqkv,
                                                void* workspace, tpmlp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norm of the query and key heads with the position rotation, between the QKV
+ * projection and the attention core, and back.
+ *
+ * Every head x (head_dim elements of Q_i or K_i, one token at position p):
+ *   r = (mean(x^2) + eps)^(-1/2)          (norm = 0: r = 1)
+ *   u = g x r                             (g: gq for queries, gk for keys; NULL: ones)
+ *   pair j < rotary_dim / 2, phi = p f_j: a' = u_a cos phi - u_b sin phi
+ *                                         b' = u_b cos phi + u_a sin phi
+ * and the elements from rotary_dim on are u.  The partners (a, b) of pair j are
+ * the elements (j, j + rotary_dim / 2) (TPMLP_ROPE_HALVES) or (2j, 2j + 1)
+ * (TPMLP_ROPE_PAIRS); f_j = base^(-2j / rotary_dim), or inv_freq[j].  All in
+ * fp32, rounded once to the plan's dtype.  The angle is p f_j taken modulo a
+ * turn exactly, with f_j to 53 bits, for any 64-bit position, negative ones
+ * included; its error in turns is at most |p f_j| 2^-53 + 2^-25.
+ * Backward, from dy: w = dy rotated back, n = x r, s = w g:
+ *   dx = r (s - n mean(s n)),   dg = sum over tokens, shards and heads of w n
+ * (norm = 0: dx = w).  x is the QKV buffer as the projection wrote it: keep it.
+ * Rows with a NaN or an infinity spoil their own head and the gain's gradient
+ * only.
+ *
+ * tpmlp_attn_plan_set_qk_norm_rope describes the heads (copied into the plan,
+ * inv_freq included; may not run while another call uses the plan).  Every
+ * dq_i and dkv_i must be a multiple of head_dim, an even number up to 256;
+ * rotary_dim is even, 0 (norm only) to head_dim.  With an fp32 plan and
+ * norm = 1 tpmlp_workspace_size grows: query it after this call.  Errors:
+ * TPMLP_ERR_INVALID_ARG (NULL, an MLP plan, unknown layout, norm not 0 or 1,
+ * eps, base or inv_freq not usable), TPMLP_ERR_SHAPE, TPMLP_ERR_UNSUPPORTED
+ * (head_dim above 256).
+ *
+ * Forward: QK[i] = [Q_i | K_i] normed and rotated, dense [T x (dq_i + dkv_i)];
+ * or in place, QK[i] == QKV[i]: then the query and key columns of the
+ * [T x n_i] buffer are overwritten and its value columns left as they are
+ * (the backward pass then lacks its input: for inference).  positions: T
+ * 64-bit integers (device), NULL for 0 .. T - 1.  One launch.
+ * Backward: dQK[i] = the core's [dQ_i | dK_i], dense [T x (dq_i + dkv_i)];
+ * dQKV[i] [T x n_i] as tpmlp_attn_qkv_backward takes it.  dV (optional): t
+ * dense [T x dkv_i] arrays, copied into the value columns; NULL leaves those
+ * columns as they are.  dQK[i] == dQKV[i] is allowed: the query and key
+ * columns of the [T x n_i] buffer are then read and overwritten.  dgq, dgk
+ * [head_dim] (optional) in the plan's dtype.  One launch, and a second one when
+ * a gain's gradient is asked for, which is also when workspace is needed (the
+ * plan's, zero-filled or used).  Other overlaps of inputs and outputs are
+ * refused (TPMLP_ERR_INVALID_ARG).  With T = 0 the gradients of the gains are
+ * zero-filled.                                                               */
+typedef enum { TPMLP_ROPE_HALVES = 0, TPMLP_ROPE_PAIRS = 1 } tpmlp_rope_layout;
+typedef struct {
+  int32_t head_dim;
+  int32_t rotary_dim;
+  tpmlp_rope_layout layout;
+  int32_t norm;            /* 1: RMS norm, 0: rotation only (no gains then) */
+  float eps;               /* > 0 with norm = 1 */
+  double base;             /* > 0; read if inv_freq is NULL */
+  const double* inv_freq;  /* rotary_dim / 2 radians per position (host memory, copied), or NULL */
+} tpmlp_qk_desc;
+TPMLP_API tpmlp_status tpmlp_attn_plan_set_qk_norm_rope(tpmlp_plan* plan, const tpmlp_qk_desc* desc);
+TPMLP_API tpmlp_status tpmlp_attn_qk_norm_rope_forward(const tpmlp_plan* plan, const void* const* QKV,
+                                                       const int64_t* positions, const void* gq, const void* gk,
+                                                       void* const* QK, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void* const* QKV,
+                                                        const int64_t* positions, const void* gq, const void* gk,
+                                                        const void* const* dQK, const void* const* dV,
+                                                        void* const* dQKV, void* dgq, void* dgk, void* workspace,
+                                                        tpmlp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits.
+ *
+ * A checkpoint holds a [rows x cols] tensor in 1.0625 bytes an element: groups
+ * of 16 columns of a row, an e4m3 code an element and a power of two 2^e a
+ * group.  With m the group's largest magnitude, e is the smallest with
+ * m <= 448 * 2^e, within [-117, 120]; a code is the e4m3 number nearest to
+ * x 2^-e (ties to even; at most 240 with e = 120, so that no finite number
+ * comes back as an infinity).  An element is off by at most 2^-4 of its value,
+ * or 2^(e - 10) if that is more.  A group that holds a NaN or an infinity comes
+ * back as NaN throughout.  Every kept value is a bf16 number, so unpacking is
+ * exact in both dtypes, and packing what was unpacked gives the same codes'
+ * values again.
+ * Storage (tpmlp_ckpt8_size bytes, 16-byte aligned): blocks of 32 rows x 16
+ * columns, 512 bytes each (a row's 16 codes after the other's), the blocks of
+ * 32 rows side by side, G = ceil(cols / 16) of them; after the last block one
+ * byte e + 127 per group (255: NaN), 32 per block in the blocks' order.  Bytes
+ * that stand for rows past the last are neither written nor read; columns past
+ * the last within a group are kept as 0.
+ *
+ * tpmlp_ckpt8_size: 0 for sizes below 0 or above 2^31 - 1.
+ * tpmlp_ckpt8_pack / _unpack: any tensor kept between two passes (a layer's
+ * input, the attention core's output, QKV).  src / dst: row stride ld >= cols
+ * elements; cols and ld multiples of 8 (bf16) / 4 (fp32).  src or dst must not
+ * overlap ckpt.  One launch each, none for rows = 0.
+ *
+ * tpmlp_forward_ckpt8: tpmlp_forward with checkpoints in saved's place: ckpt
+ * are t (GeLU: A_i) or 2t (SwiGLU: G_0.., U_0..) buffers of
+ * tpmlp_ckpt8_size(T, d_i) bytes, written by the column GEMM's epilogue from
+ * its fp32 accumulators.  H (so Y) is that of tpmlp_forward; it is scratch
+ * after the call.
+ * tpmlp_backward_ckpt8: tpmlp_backward_recompute on the kept values: act' and
+ * the recomputed H are taken of them, so that dact, dX, dW1, dW2 and the bias
+ * gradients are those of the kept pre-activations.  H is scratch (not read).
+ * Both take the plans, layouts and errors of those calls, and as many
+ * launches; the plan's token stripes are not used.                           */
+TPMLP_API size_t tpmlp_ckpt8_size(int64_t rows, int64_t cols);
+TPMLP_API tpmlp_status tpmlp_ckpt8_pack(tpmlp_dtype dtype, int64_t rows, int64_t cols, const void* src, int64_t ld,
+                                        void* ckpt, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_ckpt8_unpack(tpmlp_dtype dtype, int64_t rows, int64_t cols, const void* ckpt, void* dst,
+                                          int64_t ld, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_forward_ckpt8(const tpmlp_plan* plan, const void* X, const void* const* W1,
+                                           const void* const* W3, const void* const* W2, const void* const* b1,
+                                           const void* const* b3, const void* b2, void* Y, void* const* ckpt,
+                                           void* const* H, void* workspace, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* X, const void* const* W1,
+                                            const void* const* W3, const void* const* W2, const void* const* ckpt,
+                                            void* const* H, const void* dY, void* const* dact, void* dX,
+                                            void* const* dW1, void* const* dW3, void* const* dW2, void* const* db1,
+                                            void* const* db3, void* db2, void* workspace, tpmlp_stream_t stream);
 
 /* Watchdog controls, for testing the failure path without faulting a GPU.
  * Neither may run while another call uses the plan.

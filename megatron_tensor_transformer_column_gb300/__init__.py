@@ -15,6 +15,7 @@ output projections (``tpmlp_attn_*``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -33,11 +34,15 @@ __all__ = [
     "tpmlp_attn_out_backward", "tpmlp_attn_qkv_backward", "ShardedAttentionProj",
     "tpmlp_plan_set_sequence_stripes", "tpmlp_forward_sp", "tpmlp_backward_sp", "tpmlp_last_split_tiles",
     "LAUNCH_FWD_COLUMN", "LAUNCH_FWD_ROW", "LAUNCH_BWD_DGRAD", "LAUNCH_BWD_FSUM", "tpmlp_eval_activation",
-    "ACT_EVAL",
+    "ACT_EVAL", "tpmlp_attn_plan_set_qk_norm_rope", "tpmlp_attn_qk_norm_rope_forward",
+    "tpmlp_attn_qk_norm_rope_backward", "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack",
+    "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8", "ckpt8_pack", "ckpt8_unpack", "TPMLPCheckpointFunction",
+    "ROPE_LAYOUT",
 ]
 
 ACT = {"gelu": 0, "swiglu": 1}
 DTYPE = {"bf16": 0, "fp32": 1}
+ROPE_LAYOUT = {"halves": 0, "pairs": 1}
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_INVALID_ARG", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_ALIGNMENT",
           4: "TPMLP_ERR_UNSUPPORTED", 5: "TPMLP_ERR_CUDA", 6: "TPMLP_ERR_DEVICE_TIMEOUT",
           7: "TPMLP_ERR_NOT_IMPLEMENTED"}
@@ -51,6 +56,8 @@ EXPORTED_SYMBOLS = (
     "tpmlp_backward_recompute", "tpmlp_attn_plan_create", "tpmlp_attn_qkv_forward", "tpmlp_attn_out_forward",
     "tpmlp_attn_out_backward", "tpmlp_attn_qkv_backward", "tpmlp_plan_set_sequence_stripes", "tpmlp_forward_sp",
     "tpmlp_backward_sp", "tpmlp_plan_set_stream_k", "tpmlp_last_split_tiles", "tpmlp_eval_activation",
+    "tpmlp_attn_plan_set_qk_norm_rope", "tpmlp_attn_qk_norm_rope_forward", "tpmlp_attn_qk_norm_rope_backward",
+    "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack", "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8",
 )
 
 # forms of tpmlp_eval_activation
@@ -82,6 +89,12 @@ class _AttnDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int64), ("t", ctypes.c_int32),
                 ("dq_i", ctypes.POINTER(ctypes.c_int64)), ("dkv_i", ctypes.POINTER(ctypes.c_int64)),
                 ("dtype", ctypes.c_int)]
+
+
+class _QkDesc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("base", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
 
 
 _lib = None
@@ -164,6 +177,23 @@ def load():
         lib.tpmlp_last_split_tiles.restype = i32
         lib.tpmlp_eval_activation.argtypes = [i32, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
         lib.tpmlp_eval_activation.restype = st
+        i64 = ctypes.c_int64
+        lib.tpmlp_attn_plan_set_qk_norm_rope.argtypes = [vp, ctypes.POINTER(_QkDesc)]
+        lib.tpmlp_attn_plan_set_qk_norm_rope.restype = st
+        lib.tpmlp_attn_qk_norm_rope_forward.argtypes = [vp, pp, vp, vp, vp, pp, vp]
+        lib.tpmlp_attn_qk_norm_rope_forward.restype = st
+        lib.tpmlp_attn_qk_norm_rope_backward.argtypes = [vp, pp, vp, vp, vp, pp, pp, pp, vp, vp, vp, vp]
+        lib.tpmlp_attn_qk_norm_rope_backward.restype = st
+        lib.tpmlp_ckpt8_size.argtypes = [i64, i64]
+        lib.tpmlp_ckpt8_size.restype = ctypes.c_size_t
+        lib.tpmlp_ckpt8_pack.argtypes = [i32, i64, i64, vp, i64, vp, vp]
+        lib.tpmlp_ckpt8_pack.restype = st
+        lib.tpmlp_ckpt8_unpack.argtypes = [i32, i64, i64, vp, vp, i64, vp]
+        lib.tpmlp_ckpt8_unpack.restype = st
+        lib.tpmlp_forward_ckpt8.argtypes = lib.tpmlp_forward.argtypes
+        lib.tpmlp_forward_ckpt8.restype = st
+        lib.tpmlp_backward_ckpt8.argtypes = lib.tpmlp_backward_recompute.argtypes
+        lib.tpmlp_backward_ckpt8.restype = st
         _lib = lib
         return lib
 
@@ -188,6 +218,13 @@ def _arr(xs) -> Optional[ctypes.Array]:
     if xs is None:
         return None
     return (ctypes.c_void_p * len(xs))(*[_addr(x) for x in xs])
+
+
+def _positions(plan, x) -> Optional[int]:
+    if hasattr(x, "data_ptr"):
+        if str(x.dtype) != "torch.int64" or x.numel() != plan.T:
+            raise ValueError(f"positions must be {plan.T} int64 numbers, got {x.numel()} of {x.dtype}")
+    return _addr(x)
 
 
 def _stream(stream) -> Optional[int]:
@@ -290,6 +327,67 @@ def tpmlp_attn_out_backward(plan, WO, O, dZ, dO, dWO, workspace, stream=None):
 def tpmlp_attn_qkv_backward(plan, X, Wqkv, dQKV, dX, dWqkv, workspace, stream=None):
     _ok(load().tpmlp_attn_qkv_backward(plan.handle, _addr(X), _arr(Wqkv), _arr(dQKV), _addr(dX), _arr(dWqkv),
                                        _addr(workspace), _stream(stream)), "tpmlp_attn_qkv_backward")
+
+
+def tpmlp_attn_plan_set_qk_norm_rope(plan, head_dim, rotary_dim=None, layout="halves", norm=True, eps=1e-6,
+                                     base=10000.0, inv_freq=None):
+    """Describe the plan's heads for tpmlp_attn_qk_norm_rope_*: head_dim elements, the first rotary_dim (None: all)
+    of them rotated; inv_freq: rotary_dim / 2 radians per position (None: base ** (-2 j / rotary_dim))."""
+    rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    freq = None
+    if inv_freq is not None:
+        if len(inv_freq) != int(rotary_dim) // 2:
+            raise ValueError(f"inv_freq must have rotary_dim / 2 = {int(rotary_dim) // 2} entries, got {len(inv_freq)}")
+        freq = (ctypes.c_double * max(1, len(inv_freq)))(*[float(f) for f in inv_freq])
+    desc = _QkDesc(int(head_dim), int(rotary_dim), ROPE_LAYOUT[layout] if isinstance(layout, str) else int(layout),
+                   int(norm), float(eps), float(base),
+                   ctypes.cast(freq, ctypes.POINTER(ctypes.c_double)) if freq is not None else None)
+    _ok(load().tpmlp_attn_plan_set_qk_norm_rope(plan.handle, ctypes.byref(desc)), "tpmlp_attn_plan_set_qk_norm_rope")
+    plan.head_dim, plan.qk_norm = int(head_dim), bool(norm)
+
+
+def tpmlp_attn_qk_norm_rope_forward(plan, QKV, positions, gq, gk, QK, stream=None):
+    _ok(load().tpmlp_attn_qk_norm_rope_forward(plan.handle, _arr(QKV), _positions(plan, positions), _addr(gq),
+                                               _addr(gk), _arr(QK), _stream(stream)),
+        "tpmlp_attn_qk_norm_rope_forward")
+
+
+def tpmlp_attn_qk_norm_rope_backward(plan, QKV, positions, gq, gk, dQK, dV, dQKV, dgq, dgk, workspace, stream=None):
+    if hasattr(workspace, "numel") and workspace.numel() * workspace.element_size() < tpmlp_workspace_size(plan):
+        raise ValueError("workspace is smaller than tpmlp_workspace_size(plan)")
+    _ok(load().tpmlp_attn_qk_norm_rope_backward(plan.handle, _arr(QKV), _positions(plan, positions), _addr(gq),
+                                                _addr(gk), _arr(dQK), _arr(dV), _arr(dQKV), _addr(dgq), _addr(dgk),
+                                                _addr(workspace), _stream(stream)),
+        "tpmlp_attn_qk_norm_rope_backward")
+
+
+def tpmlp_ckpt8_size(rows: int, cols: int) -> int:
+    """Bytes of the 8-bit checkpoint of a [rows x cols] tensor."""
+    return int(load().tpmlp_ckpt8_size(int(rows), int(cols)))
+
+
+def tpmlp_ckpt8_pack(dtype, rows, cols, src, ld, ckpt, stream=None):
+    _ok(load().tpmlp_ckpt8_pack(DTYPE[dtype] if isinstance(dtype, str) else int(dtype), int(rows), int(cols),
+                                _addr(src), int(ld), _addr(ckpt), _stream(stream)), "tpmlp_ckpt8_pack")
+
+
+def tpmlp_ckpt8_unpack(dtype, rows, cols, ckpt, dst, ld, stream=None):
+    _ok(load().tpmlp_ckpt8_unpack(DTYPE[dtype] if isinstance(dtype, str) else int(dtype), int(rows), int(cols),
+                                  _addr(ckpt), _addr(dst), int(ld), _stream(stream)), "tpmlp_ckpt8_unpack")
+
+
+def tpmlp_forward_ckpt8(plan, X, W1, W3, W2, b1, b3, b2, Y, ckpt, H, workspace, stream=None):
+    _ok(load().tpmlp_forward_ckpt8(plan.handle, _addr(X), _arr(W1), _arr(W3), _arr(W2), _arr(b1), _arr(b3), _addr(b2),
+                                   _addr(Y), _arr(ckpt), _arr(H), _addr(workspace), _stream(stream)),
+        "tpmlp_forward_ckpt8")
+
+
+def tpmlp_backward_ckpt8(plan, X, W1, W3, W2, ckpt, H, dY, dact, dX, dW1, dW3, dW2, db1, db3, db2, workspace,
+                         stream=None):
+    _ok(load().tpmlp_backward_ckpt8(plan.handle, _addr(X), _arr(W1), _arr(W3), _arr(W2), _arr(ckpt), _arr(H),
+                                    _addr(dY), _arr(dact), _addr(dX), _arr(dW1), _arr(dW3), _arr(dW2), _arr(db1),
+                                    _arr(db3), _addr(db2), _addr(workspace), _stream(stream)),
+        "tpmlp_backward_ckpt8")
 
 
 def tpmlp_plan_set_sequence_stripes(plan: Plan, stripe_rows: Sequence[int]):
@@ -431,6 +529,85 @@ def tpmlp_last_split_tiles(launch_kind: int) -> List[tuple]:
 
 # ---------------------------------------------------------------- convenience layer
 
+def _tdtype(dtype: str):
+    import torch
+    return {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+
+
+def _check(name: str, x, shape, dtype, device):
+    """One tensor argument of the classes below: shape, dtype and device (contiguity is checked with its address)."""
+    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or x.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} of {dtype} on {device}, got {tuple(x.shape)} of {x.dtype} "
+                         f"on {x.device}")
+
+
+def _check_list(name: str, xs, shapes, dtype, device):
+    if len(xs) != len(shapes):
+        raise ValueError(f"{name}: expected {len(shapes)} tensors, got {len(xs)}")
+    for i, (x, s) in enumerate(zip(xs, shapes)):
+        _check(f"{name}[{i}]", x, s, dtype, device)
+
+
+def _device(device):
+    import torch
+    d = torch.device(device or "cuda")
+    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The call's device and stream as the current ones, so that what it allocates belongs to that stream.
+    stream: None (the device's current one), a torch stream or a raw handle (0: the default stream)."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            yield
+
+
+def ckpt8_pack(x, out=None, stream=None):
+    """The 8-bit checkpoint (a uint8 tensor of tpmlp_ckpt8_size bytes) of a 2-D bf16 or fp32 CUDA tensor, whose rows
+    may be further apart than they are long (a column slice)."""
+    import torch
+    names = {torch.bfloat16: "bf16", torch.float32: "fp32"}
+    if x.dim() != 2 or x.dtype not in names or not x.is_cuda:
+        raise ValueError("expected a 2-D bf16 or fp32 CUDA tensor")
+    rows, cols = x.shape
+    if x.numel() and cols > 1 and x.stride(1) != 1:
+        raise ValueError("the rows must be contiguous")
+    ld = x.stride(0) if rows > 1 else cols
+    n = tpmlp_ckpt8_size(rows, cols)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty(n, dtype=torch.uint8, device=x.device)
+        _check("out", out, (n,), torch.uint8, x.device)
+        tpmlp_ckpt8_pack(names[x.dtype], rows, cols, (x.data_ptr() or None) if x.numel() else None, ld, out)
+    return out
+
+
+def ckpt8_unpack(ckpt, rows: int, cols: int, dtype: str = "bf16", out=None, stream=None):
+    """The [rows x cols] tensor that a checkpoint stands for; out: a tensor to write it to (rows may lie apart)."""
+    import torch
+    td = _tdtype(dtype)
+    _check("ckpt", ckpt, (tpmlp_ckpt8_size(rows, cols),), torch.uint8, ckpt.device)
+    if not ckpt.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    with _on(ckpt.device, stream):
+        if out is None:
+            out = torch.empty(rows, cols, dtype=td, device=ckpt.device)
+        _check("out", out, (rows, cols), td, ckpt.device)
+        if out.numel() and cols > 1 and out.stride(1) != 1:
+            raise ValueError("the rows must be contiguous")
+        ld = out.stride(0) if rows > 1 else cols
+        tpmlp_ckpt8_unpack(dtype, rows, cols, ckpt, (out.data_ptr() or None) if out.numel() else None, ld)
+    return out
+
+
 class ShardedMLP:
     """Plan + workspace + output allocation for one problem shape.
 
@@ -504,6 +681,66 @@ class ShardedMLP:
            stream)
         return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "dact": dact, "db1": db1, "db3": db3, "db2": db2}
 
+    # ---- 8-bit activation checkpoints: what backward needs of the pre-activations in 1.0625 bytes each
+    def _weight_shapes(self):
+        p = self.plan
+        return [(p.d, w) for w in p.d_i], [(w, p.d) for w in p.d_i]
+
+    def _check_mlp(self, X, W1_i, W2_i, W3_i, more=()):
+        p, dev = self.plan, _device(self.device)
+        col, row = self._weight_shapes()
+        _check("X", X, (p.T, p.d), self.tdtype, dev)
+        _check_list("W1_i", W1_i, col, self.tdtype, dev)
+        _check_list("W2_i", W2_i, row, self.tdtype, dev)
+        if self.swiglu:
+            _check_list("W3_i", W3_i if W3_i is not None else (), col, self.tdtype, dev)
+        for name, x, shape in more:
+            if x is not None:
+                _check(name, x, shape, self.tdtype, dev)
+        return dev
+
+    def _check_biases(self, dev, b1_i, b3_i):
+        for name, b in (("b1_i", b1_i), ("b3_i", b3_i if self.swiglu else None)):
+            if b is not None:
+                _check_list(name, b, [(w,) for w in self.plan.d_i], self.tdtype, dev)
+
+    def ckpt8_sizes(self):
+        """Bytes of each checkpoint: one per shard (A_i), SwiGLU two (G_i, then U_i)."""
+        return [tpmlp_ckpt8_size(self.plan.T, w) for w in self.plan.d_i * (2 if self.swiglu else 1)]
+
+    def forward_ckpt8(self, X, W1_i, W2_i, W3_i=None, stream=None, b1_i=None, b3_i=None, b2=None, out=None):
+        """forward with the pre-activations kept as 8-bit checkpoints.  Returns (Y, ckpt); out: those two, to write
+        to.  H is scratch of the call."""
+        import torch
+        p = self.plan
+        dev = self._check_mlp(X, W1_i, W2_i, W3_i, [("b2", b2, (p.d,))])
+        self._check_biases(dev, b1_i, b3_i)
+        with _on(dev, stream):
+            if out is None:
+                out = (self._empty(p.T, p.d),
+                       [torch.empty(n, dtype=torch.uint8, device=dev) for n in self.ckpt8_sizes()])
+            Y, ckpt = out
+            _check("Y", Y, (p.T, p.d), self.tdtype, dev)
+            _check_list("ckpt", ckpt, [(n,) for n in self.ckpt8_sizes()], torch.uint8, dev)
+            H = [self._empty(p.T, w) for w in p.d_i]
+            tpmlp_forward_ckpt8(p, X, W1_i, W3_i if self.swiglu else None, W2_i, b1_i, b3_i if self.swiglu else None,
+                                b2, Y, ckpt, H, self.workspace)
+        return Y, ckpt
+
+    def backward_ckpt8(self, X, W1_i, W2_i, ckpt, dY, W3_i=None, stream=None, bias_grads=False, out=None):
+        """Gradients as backward gives them (without "dact"), from the checkpoints that forward_ckpt8 wrote."""
+        import torch
+        p = self.plan
+        dev = self._check_mlp(X, W1_i, W2_i, W3_i, [("dY", dY, (p.T, p.d))])
+        _check_list("ckpt", ckpt, [(n,) for n in self.ckpt8_sizes()], torch.uint8, dev)
+        with _on(dev, stream):
+            dact, dX, dW1, dW3, dW2 = out if out is not None else self.alloc_backward()
+            db1, db3, db2 = self.alloc_bias_grads() if bias_grads else (None, None, None)
+            H = [self._empty(p.T, w) for w in p.d_i]
+            tpmlp_backward_ckpt8(p, X, W1_i, W3_i if self.swiglu else None, W2_i, ckpt, H, dY, dact, dX, dW1, dW3,
+                                 dW2, db1, db3, db2, self.workspace)
+        return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "db1": db1, "db3": db3, "db2": db2}
+
     def check(self, stream=None):
         tpmlp_check(self.plan, self.workspace, stream)
 
@@ -576,6 +813,72 @@ class ShardedAttentionProj:
         tpmlp_attn_qkv_backward(p, X, Wqkv_i, dQKV_i, dX, dWqkv, self.workspace, stream)
         return dX, dWqkv
 
+    # ---- norm of the query and key heads with the position rotation
+    def set_qk_norm_rope(self, head_dim, rotary_dim=None, layout="halves", norm=True, eps=1e-6, base=10000.0,
+                         inv_freq=None):
+        import torch
+        tpmlp_attn_plan_set_qk_norm_rope(self.plan, head_dim, rotary_dim, layout, norm, eps, base, inv_freq)
+        n = tpmlp_workspace_size(self.plan)
+        if n > self.workspace.numel():
+            self.workspace = torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    def _check_qk(self, QKV_i, positions, gq, gk):
+        p, dev = self.plan, _device(self.device)
+        if not hasattr(p, "head_dim"):
+            raise ValueError("the heads are not described (set_qk_norm_rope)")
+        _check_list("QKV_i", QKV_i, [(p.T, n) for n in p.d_i], self.tdtype, dev)
+        for name, g in (("gq", gq), ("gk", gk)):
+            if g is not None:
+                _check(name, g, (p.head_dim,), self.tdtype, dev)
+        if positions is not None and positions.device != dev:
+            raise ValueError(f"positions: expected on {dev}, got on {positions.device}")
+        return dev
+
+    def qk_norm_rope_forward(self, QKV_i, positions=None, gq=None, gk=None, out=None, stream=None):
+        """The normed and rotated heads [Q_i | K_i] of each shard.  out: [T, dq_i + dkv_i] tensors, or QKV_i itself
+        (in place: the value columns stay as they are)."""
+        import torch
+        p = self.plan
+        dev = self._check_qk(QKV_i, positions, gq, gk)
+        with _on(dev, stream):
+            if out is None:
+                out = [self._empty(p.T, q + k) for q, k in zip(p.dq_i, p.dkv_i)]
+            self._check_in_place("out", out, QKV_i, dev)
+            tpmlp_attn_qk_norm_rope_forward(p, QKV_i, positions, gq, gk, out)
+        return out
+
+    def _check_in_place(self, name, xs, fused, dev):
+        p = self.plan
+        if len(xs) != p.t:
+            raise ValueError(f"{name}: expected {p.t} tensors, got {len(xs)}")
+        for i, (x, f) in enumerate(zip(xs, fused)):
+            same = p.T and x.data_ptr() == f.data_ptr()
+            _check(f"{name}[{i}]", x, (p.T, p.d_i[i] if same else p.dq_i[i] + p.dkv_i[i]), self.tdtype, dev)
+
+    def qk_norm_rope_backward(self, QKV_i, dQK_i, positions=None, gq=None, gk=None, dV_i=None, out=None, stream=None,
+                              gain_grads=None):
+        """(dQKV_i, dgq, dgk) from the core's [dQ_i | dK_i] and, optionally, dV_i [T, dkv_i].  out: the dQKV_i to
+        write to; their value columns stay as they are without dV_i.  dQK_i may be those tensors themselves.
+        gain_grads: whether to compute dgq and dgk (None: if a gain is given)."""
+        import torch
+        p = self.plan
+        dev = self._check_qk(QKV_i, positions, gq, gk)
+        if dV_i is not None:
+            _check_list("dV_i", dV_i, [(p.T, k) for k in p.dkv_i], self.tdtype, dev)
+        elif out is None:
+            raise ValueError("dV_i, or dQKV_i that hold dV already (out), must be given")
+        if gain_grads is None:
+            gain_grads = gq is not None or gk is not None
+        with _on(dev, stream):
+            if out is None:
+                out = [self._empty(p.T, n) for n in p.d_i]
+            _check_list("out", out, [(p.T, n) for n in p.d_i], self.tdtype, dev)
+            self._check_in_place("dQK_i", dQK_i, out, dev)
+            dgq, dgk = (self._empty(p.head_dim), self._empty(p.head_dim)) if gain_grads else (None, None)
+            tpmlp_attn_qk_norm_rope_backward(p, QKV_i, positions, gq, gk, dQK_i, dV_i, out, dgq, dgk,
+                                             self.workspace)
+        return out, dgq, dgk
+
     def check(self, stream=None):
         tpmlp_check(self.plan, self.workspace, stream)
 
@@ -616,13 +919,48 @@ def _make_function():
     return TPMLPFunction
 
 
+def _make_checkpoint_function():
+    import torch
+
+    class TPMLPCheckpointFunction(torch.autograd.Function):
+        """TPMLPFunction with the pre-activations kept as 8-bit checkpoints between the passes: it saves X, the
+        weights and 1.0625 bytes per pre-activation."""
+
+        @staticmethod
+        def forward(ctx, mlp: ShardedMLP, X, *weights):
+            t = mlp.plan.t
+            X = X.contiguous()
+            W3_i = list(weights[2 * t:3 * t]) if mlp.swiglu else None
+            Y, ckpt = mlp.forward_ckpt8(X, list(weights[:t]), list(weights[t:2 * t]), W3_i)
+            ctx.mlp, ctx.nw = mlp, len(weights)
+            ctx.save_for_backward(X, *weights, *ckpt)
+            return Y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dY):
+            mlp, nw = ctx.mlp, ctx.nw
+            t = mlp.plan.t
+            X, *rest = ctx.saved_tensors
+            weights, ckpt = rest[:nw], rest[nw:]
+            W3_i = weights[2 * t:] if mlp.swiglu else None
+            g = mlp.backward_ckpt8(X, weights[:t], weights[t:2 * t], ckpt, dY.contiguous(), W3_i)
+            return (None, g["dX"], *g["dW1"], *g["dW2"], *(g["dW3"] if mlp.swiglu else []))
+
+    return TPMLPCheckpointFunction
+
+
 class _LazyFunction:
-    _fn = None
+    """An autograd function that is made, and torch imported, on its first use."""
+
+    def __init__(self, make=_make_function):
+        self._make, self._fn = make, None
 
     def __getattr__(self, name):
-        if _LazyFunction._fn is None:
-            _LazyFunction._fn = _make_function()
-        return getattr(_LazyFunction._fn, name)
+        if self._fn is None:
+            self._fn = self._make()
+        return getattr(self._fn, name)
 
 
 TPMLPFunction = _LazyFunction()
+TPMLPCheckpointFunction = _LazyFunction(_make_checkpoint_function)

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtpmlp.so")
-SOURCES = ["tpmlp_api.cu", "tc_gemm.cu", "simt_gemm.cu", "colsum.cu", "act_eval.cu"]
+SOURCES = ["tpmlp_api.cu", "tc_gemm.cu", "tc_gemm_ckpt8.cu", "simt_gemm.cu", "qk_norm_rope.cu", "ckpt8.cu", "colsum.cu",
+           "act_eval.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "act.cuh"
+#include "ckpt8.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
@@ -39,6 +40,84 @@ __device__ __forceinline__ float load_a(const GemmParams& p, const Seg& S, int m
 __device__ __forceinline__ float load_b(const GemmParams& p, const void* b, int64_t ldb, bool striped, int major,
                                         int64_t k, int64_t n) {
   return major == MAJOR_MN ? load_elem(p, b, ldb, striped, k, n) : load_elem(p, b, ldb, striped, n, k);
+}
+
+// A value of one lane of a row of 32 columns to and from an 8-bit checkpoint:
+// the 16 lanes of a group find its largest magnitude by shuffles.
+__device__ __forceinline__ int64_t ckpt8_block(const Prob& P, int64_t row, int64_t col) {
+  return (row / ck::kRows) * ck::groups(P.N) + col / ck::kGroup;
+}
+
+__device__ __forceinline__ void store_ckpt8(void* ckpt, const Prob& P, int64_t row, int64_t col, bool row_ok, float v) {
+  uint32_t m = __float_as_uint(col < P.N ? v : 0.0f) & 0x7fffffffu;
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const uint32_t b = ck::scale_byte(m);
+  const int64_t k = col % ck::kGroup;
+  if (!row_ok || col - k >= P.N) return;
+  const float w[4] = {col < P.N ? v : 0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t blk = ckpt8_block(P, row, col);
+  uint8_t* base = static_cast<uint8_t*>(ckpt);
+  base[blk * ck::kBlockBytes + (row % ck::kRows) * ck::kGroup + k] =
+      static_cast<uint8_t>(ck::encode4(w, ck::inv_scale(b), b == ck::kTopScale));
+  if (k == 0) base[ck::scale_offset(P.M, P.N) + blk * ck::kRows + row % ck::kRows] = static_cast<uint8_t>(b);
+}
+
+__device__ __forceinline__ float load_ckpt8(const void* ckpt, const Prob& P, int64_t row, int64_t col) {
+  const int64_t blk = ckpt8_block(P, row, col);
+  const uint8_t* base = static_cast<const uint8_t*>(ckpt);
+  float x0, x1;
+  ck::decode2(base[blk * ck::kBlockBytes + (row % ck::kRows) * ck::kGroup + col % ck::kGroup],
+              ck::scale(base[ck::scale_offset(P.M, P.N) + blk * ck::kRows + row % ck::kRows]), x0, x1);
+  return x0;
+}
+
+// The activation epilogues with 8-bit checkpoints: rows row0 .. row0 + 3 of
+// this thread's column.  Every lane takes part (the groups' shuffles).
+__device__ __forceinline__ void ckpt8_epilogue(const Prob& P, int64_t row0, int64_t n0, const float (&acc)[4],
+                                               const float (&acc2)[4]) {
+  const int64_t col = n0 + (threadIdx.x & 31);
+  const bool in = col < P.N;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + i;
+    const bool row_ok = row < P.M;  // the same for the whole warp
+    const int64_t o = row * P.ldo + col;
+    float v = acc[i];
+    switch (P.epi) {
+      case EPI_GELU_FWD:
+        if (P.aux0 && in) v += static_cast<const float*>(P.aux0)[col];
+        store_ckpt8(P.out0, P, row, col, row_ok, v);
+        if (row_ok && in) static_cast<float*>(P.out1)[o] = act::gelu(v);
+        break;
+      case EPI_SWIGLU_FWD: {
+        float u = acc2[i];
+        if (P.aux0 && in) v += static_cast<const float*>(P.aux0)[col];
+        if (P.aux1 && in) u += static_cast<const float*>(P.aux1)[col];
+        store_ckpt8(P.out0, P, row, col, row_ok, v);
+        store_ckpt8(P.out1, P, row, col, row_ok, u);
+        if (row_ok && in) static_cast<float*>(P.out2)[o] = u * act::swish(v);
+        break;
+      }
+      case EPI_GELU_BWD:
+        if (row_ok && in) {
+          const float a = load_ckpt8(P.aux0, P, row, col);
+          static_cast<float*>(P.out0)[o] = v * act::gelu_grad(a);
+          static_cast<float*>(P.out1)[o] = act::gelu(a);
+        }
+        break;
+      case EPI_SWIGLU_BWD:
+        if (row_ok && in) {
+          float dg, du;
+          const float gg = load_ckpt8(P.aux0, P, row, col), uu = load_ckpt8(P.aux1, P, row, col);
+          act::swiglu_grads(v, gg, uu, dg, du);
+          static_cast<float*>(P.out0)[o] = dg;
+          static_cast<float*>(P.out1)[o] = du;
+          static_cast<float*>(P.out2)[o] = uu * act::swish(gg);
+        }
+        break;
+      default:
+        break;
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) tpmlp_fp32_simt_gemm(const __grid_constant__ GemmParams p) {
@@ -99,6 +178,10 @@ __global__ void __launch_bounds__(kThreads) tpmlp_fp32_simt_gemm(const __grid_co
   }
 
   const int64_t col = n0 + tx;
+  if (p.ckpt8) {
+    ckpt8_epilogue(P, m0 + 4 * ty, n0, acc, acc2);
+    return;
+  }
   if (col >= P.N) return;
   for (int i = 0; i < 4; ++i) {
     const int64_t row = m0 + 4 * ty + i;

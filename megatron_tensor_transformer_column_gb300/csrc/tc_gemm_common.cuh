@@ -1,5 +1,5 @@
 // tc_gemm_common.cuh -- device building blocks of the persistent 2-SM
-// tcgen05 GEMM (tc_gemm.cu): tile geometry, bounded waits, the per-pair load
+// tcgen05 GEMM (tc_gemm_body.cuh): tile geometry, bounded waits, the per-pair load
 // shape, the straight-line MMA issue of a stage and the fused epilogue of a
 // 32-column chunk.
 #pragma once
@@ -9,6 +9,7 @@
 #include <climits>
 
 #include "act.cuh"
+#include "ckpt8.cuh"
 #include "ptx.cuh"
 #include "tpmlp_internal.h"
 
@@ -395,10 +396,53 @@ __device__ __forceinline__ void add_bias(const void* bias, int col, int nvalid, 
   for (int j = 0; j < N; ++j) v[j] += b[j];
 }
 
+// This thread's row of a chunk (columns x .. x + N - 1 of row grow, nvalid of
+// them inside the tensor) to an 8-bit checkpoint of the problem's output and
+// back.  x is a multiple of 16 and a warp's rows are one block of 32, so each
+// group's 16 bytes a lane are 512 contiguous bytes a warp: plain stores, no
+// staging.
+template <int N>
+__device__ __forceinline__ void store_ckpt8(void* ckpt, const Prob& P, int64_t grow, int x, int nvalid,
+                                            const float (&v)[N]) {
+  const int64_t blk = (grow >> 5) * ck::groups(P.N) + x / ck::kGroup;
+  uint8_t* codes = static_cast<uint8_t*>(ckpt) + blk * ck::kBlockBytes + (grow & 31) * ck::kGroup;
+  uint8_t* scales = static_cast<uint8_t*>(ckpt) + ck::scale_offset(P.M, P.N) + blk * ck::kRows + (grow & 31);
+#pragma unroll
+  for (int g = 0; g < N / ck::kGroup; ++g) {
+    if (ck::kGroup * g >= nvalid) break;
+    float w[ck::kGroup];
+#pragma unroll
+    for (int k = 0; k < ck::kGroup; ++k) w[k] = ck::kGroup * g + k < nvalid ? v[ck::kGroup * g + k] : 0.0f;
+    uint32_t byte;
+    const uint4 c = ck::encode_row(w, byte);
+    *reinterpret_cast<uint4*>(codes + g * ck::kBlockBytes) = c;
+    scales[g * ck::kRows] = static_cast<uint8_t>(byte);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void load_ckpt8(const void* ckpt, const Prob& P, int64_t grow, int x, int nvalid,
+                                           float (&v)[N]) {
+  const int64_t blk = (grow >> 5) * ck::groups(P.N) + x / ck::kGroup;
+  const uint8_t* codes = static_cast<const uint8_t*>(ckpt) + blk * ck::kBlockBytes + (grow & 31) * ck::kGroup;
+  const uint8_t* scales = static_cast<const uint8_t*>(ckpt) + ck::scale_offset(P.M, P.N) + blk * ck::kRows + (grow & 31);
+#pragma unroll
+  for (int g = 0; g < N / ck::kGroup; ++g) {
+    uint4 c = make_uint4(0, 0, 0, 0);
+    uint32_t byte = 127;
+    if (ck::kGroup * g < nvalid) {
+      c = __ldg(reinterpret_cast<const uint4*>(codes + g * ck::kBlockBytes));
+      byte = __ldg(scales + g * ck::kRows);
+    }
+    ck::decode_row(c, byte, v + ck::kGroup * g);
+  }
+}
+
 // Epilogue of one N-column chunk (columns x .. x+N-1 of rows y .. y+31, this
 // thread's row grow) of a single accumulator.  Every lane takes part (the
 // stores are per warp); inputs are read only for valid rows and columns.
-template <int N>
+// kCk8: the pre-activations are 8-bit checkpoints and H is recomputed.
+template <int N, bool kCk8>
 __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& P, EpiStore& es, int64_t grow,
                                                bool row_ok, int x, int y, int nvalid, const uint32_t (&r)[N],
                                                int lane) {
@@ -413,6 +457,12 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
       break;
     case EPI_GELU_FWD: {
       add_bias<N>(P.aux0, x, nvalid, acc);
+      if constexpr (kCk8) {
+        if (row_ok) store_ckpt8<N>(P.out0, P, grow, x, nvalid, acc);
+        act::x2::gelu_xn(acc);
+        store_block<N>(es, p, P, 1, x, y, nvalid, acc, lane);
+        break;
+      }
       if (N == 16 && !P.out_striped) {  // A and H behind one fence
         float h[N];
 #pragma unroll
@@ -427,6 +477,14 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
       break;
     }
     case EPI_GELU_BWD: {
+      if constexpr (kCk8) {
+        float a[N], h[N];
+        load_ckpt8<N>(P.aux0, P, grow, x, nload, a);
+        act::x2::gelu_bwd_xn<true>(acc, a, h);
+        store_block<N>(es, p, P, 1, x, y, nvalid, h, lane);
+        store_block<N>(es, p, P, 0, x, y, nvalid, a, lane);
+        break;
+      }
       if (N == 32 && !P.out1 && y < es.rows) {  // A staged through the output block, dA written over it
         const uint32_t b = es.buf + es.next * epi_block_bytes<N>();
         if (lane == 0) ptx::bulk_wait_group_read<1>();  // the store that last used block b has read it
@@ -459,6 +517,16 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
       break;
     }
     case EPI_SWIGLU_BWD: {
+      if constexpr (kCk8) {
+        float g[N], u[N], h[N];
+        load_ckpt8<N>(P.aux0, P, grow, x, nload, g);
+        load_ckpt8<N>(P.aux1, P, grow, x, nload, u);
+        act::x2::swiglu_bwd_xn<true>(acc, g, u, h);
+        store_block<N>(es, p, P, 2, x, y, nvalid, h, lane);
+        store_block<N>(es, p, P, 0, x, y, nvalid, g, lane);
+        store_block<N>(es, p, P, 1, x, y, nvalid, u, lane);
+        break;
+      }
       if (N == 32 && !P.out2 && y < es.rows) {  // G and U staged through both blocks, dG and dU written over them
         if (lane == 0) ptx::bulk_wait_group_read<0>();
         __syncwarp();

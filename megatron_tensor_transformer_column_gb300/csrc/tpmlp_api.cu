@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -15,6 +16,7 @@
 #include <new>
 #include <vector>
 
+#include "ckpt8.cuh"
 #include "tpmlp.h"
 #include "tpmlp_internal.h"
 
@@ -36,6 +38,11 @@ struct tpmlp_plan {
   int32_t stall_injection;
   int32_t stream_k;  // TPMLP_STREAM_K_OFF / _AUTO / _ALWAYS
   std::vector<int64_t> stripe_rows;  // sequence-parallel token stripes (empty: not set)
+  // Norm and rotation of the query and key heads (attention; head_dim 0: not set)
+  int32_t head_dim = 0, rotary_dim = 0, qk_norm = 0;
+  bool rope_pairs = false;
+  float qk_eps = 0.0f;
+  std::vector<uint64_t> rope_freq;  // rotary_dim / 2 turns per position, 2^64 = one turn
 };
 
 namespace {
@@ -703,6 +710,12 @@ void plan_stream_k(GemmParams& p, int pairs, int mode, int long_from, std::vecto
   sk.epoch = e;
 }
 
+// Whether output k of problem P is an 8-bit checkpoint (written by plain
+// stores): the pre-activations of the forward epilogues.
+bool ckpt8_out(const GemmParams& p, const Prob& P, int k) {
+  return p.ckpt8 && ((P.epi == EPI_GELU_FWD && k == 0) || (P.epi == EPI_SWIGLU_FWD && k < 2));
+}
+
 // sk_workspace: the workspace holds the stream-K flags and partial slots
 // (tpmlp_workspace_size bytes); false for the library's status-only scratch.
 tpmlp_status launch(Builder& B, int tag, const DeviceInfo& di, const tpmlp_plan* plan, void* workspace,
@@ -735,7 +748,7 @@ tpmlp_status launch(Builder& B, int tag, const DeviceInfo& di, const tpmlp_plan*
       Prob& P = p.probs[i];
       void* outs[3] = {P.out0, P.out1, P.out2};
       for (int k = 0; k < 3; ++k)
-        if (outs[k]) P.out_map[k] = B.map(outs[k], P.M, P.N, out_box, P.ldo);
+        if (outs[k] && !ckpt8_out(p, P, k)) P.out_map[k] = B.map(outs[k], P.M, P.N, out_box, P.ldo);
     }
   }
   if (B.table_error) return TPMLP_ERR_UNSUPPORTED;  // message set by Builder::table_full
@@ -867,11 +880,13 @@ bool balance_long(const tpmlp_plan* pl, int64_t long_bytes) {
 
 tpmlp_status fwd_column(const tpmlp_plan* pl, const DeviceInfo& di, const void* X, const void* const* W1,
                         const void* const* W3, const void* const* b1, const void* const* b3, void* const* saved,
-                        void* const* H, void* ws, cudaStream_t st, const void* const* X_stripes = nullptr) {
+                        void* const* H, void* ws, cudaStream_t st, const void* const* X_stripes = nullptr,
+                        bool ckpt8 = false) {
   if (pl->T == 0) return TPMLP_OK;
   const bool tc = pl->dtype == TPMLP_BF16;
   const bool sw = swiglu(pl);
   Builder B(scratch_params(), tc);
+  B.p->ckpt8 = ckpt8;  // saved: 8-bit checkpoints
   if (X_stripes) {  // all-gather of the X stripes: every shard reads all of them
     B.set_stripes(pl, X_stripes, pl->d, nullptr, 0);
     X = kStripedIn;
@@ -911,11 +926,12 @@ tpmlp_status fwd_row(const tpmlp_plan* pl, const DeviceInfo& di, const void* con
 }
 
 // With recompute, H is an output: the dgrad epilogue writes H_i = act(saved_i)
-// and dW2 moves to the f-sum launch (bwd_fsum's dW2 problems).
+// and dW2 moves to the f-sum launch (bwd_fsum's dW2 problems).  ckpt8 (with
+// recompute): saved are 8-bit checkpoints.
 tpmlp_status bwd_dgrad(const tpmlp_plan* pl, const DeviceInfo& di, const void* const* W2,
                        const void* const* saved, const void* const* H, const void* dY, void* const* dact,
                        void* const* dW2, void* db2, void* ws, cudaStream_t st, bool recompute = false,
-                       const void* const* dY_stripes = nullptr) {
+                       const void* const* dY_stripes = nullptr, bool ckpt8 = false) {
   const bool sw = swiglu(pl);
   if (pl->T == 0) {
     const size_t es = pl->dtype == TPMLP_BF16 ? 2 : 4;
@@ -930,6 +946,7 @@ tpmlp_status bwd_dgrad(const tpmlp_plan* pl, const DeviceInfo& di, const void* c
     return TPMLP_OK;
   }
   Builder B(scratch_params(), pl->dtype == TPMLP_BF16);
+  B.p->ckpt8 = ckpt8;
   const void* dY_dense = dY;
   if (dY_stripes) {  // all-gather of the dY stripes (backward of the reduce-scatter)
     B.set_stripes(pl, dY_stripes, pl->d, nullptr, 0);
@@ -1206,6 +1223,65 @@ tpmlp_status attn_qkv_bwd(const tpmlp_plan* pl, const DeviceInfo& di, const void
   return launch(B, TAG_ATTN_QKV_BWD, di, pl, ws, st);
 }
 
+// ------------------------------------------------------------------ norm and rotation of the heads
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+tpmlp_status check_overlap(const char* na, int i, const void* a, int64_t bytes_a, const char* nb, int j, const void* b,
+                           int64_t bytes_b) {
+  if (!overlap(a, bytes_a, b, bytes_b)) return TPMLP_OK;
+  return fail(TPMLP_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", na, i, nb, j);
+}
+
+// The checks both passes share, before any device query.
+tpmlp_status qk_checks(const tpmlp_plan* pl, const void* const* QKV, const int64_t* positions, const void* gq,
+                       const void* gk) {
+  g_last_error[0] = 0;
+  if (!pl) return fail(TPMLP_ERR_INVALID_ARG, "plan is NULL");
+  TPMLP_TRY(check_kind(pl, PLAN_ATTN));
+  if (!pl->head_dim)
+    return fail(TPMLP_ERR_INVALID_ARG, "the heads are not described (tpmlp_attn_plan_set_qk_norm_rope)");
+  TPMLP_TRY(check_array("QKV", QKV, pl->t, pl->T == 0));
+  if (reinterpret_cast<uintptr_t>(positions) & 7u)
+    return fail(TPMLP_ERR_ALIGNMENT, "positions (%p) is not 8-byte aligned", static_cast<const void*>(positions));
+  TPMLP_TRY(check_ptr("gq", gq, true));
+  TPMLP_TRY(check_ptr("gk", gk, true));
+  if (!pl->qk_norm && (gq || gk)) return fail(TPMLP_ERR_INVALID_ARG, "gains without a norm (the plan rotates only)");
+  return TPMLP_OK;
+}
+
+int64_t esize(const tpmlp_plan* pl) { return pl->dtype == TPMLP_BF16 ? 2 : 4; }
+
+QkParams qk_params(const tpmlp_plan* pl, const int64_t* positions, const void* gq, const void* gk) {
+  QkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.T = pl->T;
+  p.t = pl->t;
+  p.D = pl->head_dim;
+  p.R = pl->rotary_dim;
+  p.norm = pl->qk_norm;
+  p.eps = pl->qk_eps;
+  p.pos = positions;
+  p.gain[0] = gq;
+  p.gain[1] = gk;
+  std::copy(pl->rope_freq.begin(), pl->rope_freq.end(), p.freq);
+  for (int i = 0; i < pl->t; ++i) {
+    QkShard& S = p.shards[i];
+    S.ldx = pl->d_i[i];
+    S.col[0] = 0;
+    S.col[1] = static_cast<int32_t>(pl->dq_i[i]);
+    S.vcol = static_cast<int32_t>(pl->dq_i[i] + pl->dkv_i[i]);
+    S.dkv = static_cast<int32_t>(pl->dkv_i[i]);
+    p.heads[0] += static_cast<int32_t>(pl->dq_i[i] / p.D);
+    p.heads[1] += static_cast<int32_t>(pl->dkv_i[i] / p.D);
+    p.head_end[0][i] = p.heads[0];
+    p.head_end[1][i] = p.heads[1];
+  }
+  return p;
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ library-owned scratch
@@ -1312,7 +1388,8 @@ tpmlp_status tpmlp_plan_set_stall_injection(tpmlp_plan* plan, int enable) {
 
 size_t tpmlp_workspace_size(const tpmlp_plan* plan) {
   if (!plan) return 0;
-  return plan->dtype == TPMLP_BF16 ? kSkWorkspaceBytes : kStatusBytes;
+  if (plan->dtype == TPMLP_BF16) return kSkWorkspaceBytes;
+  return kStatusBytes + (plan->qk_norm ? kQkMaxCtas * plan->head_dim * sizeof(float) : 0);
 }
 
 tpmlp_status tpmlp_plan_set_stream_k(tpmlp_plan* plan, int mode) {
@@ -1625,6 +1702,253 @@ tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const void* X, cons
   TPMLP_TRY(check_array("dQKV", dQKV, plan->t, tz));
   TPMLP_TRY(check_array("dWqkv", dWqkv, plan->t, false));
   return attn_qkv_bwd(plan, di, X, Wqkv, dQKV, dX, dWqkv, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tpmlp_status tpmlp_attn_plan_set_qk_norm_rope(tpmlp_plan* plan, const tpmlp_qk_desc* desc) {
+  g_last_error[0] = 0;
+  if (!plan || !desc) return fail(TPMLP_ERR_INVALID_ARG, "plan or desc is NULL");
+  TPMLP_TRY(check_kind(plan, PLAN_ATTN));
+  const int32_t D = desc->head_dim, R = desc->rotary_dim;
+  if (desc->layout != TPMLP_ROPE_HALVES && desc->layout != TPMLP_ROPE_PAIRS)
+    return fail(TPMLP_ERR_INVALID_ARG, "unknown rotation layout %d", static_cast<int>(desc->layout));
+  if (desc->norm != 0 && desc->norm != 1) return fail(TPMLP_ERR_INVALID_ARG, "norm = %d is not 0 or 1", desc->norm);
+  if (D < 2 || D % 2) return fail(TPMLP_ERR_SHAPE, "head_dim = %d is not an even number from 2 on", D);
+  if (R < 0 || R > D || R % 2) return fail(TPMLP_ERR_SHAPE, "rotary_dim = %d is not an even number in [0, %d]", R, D);
+  if (D > kMaxHeadDim) return fail(TPMLP_ERR_UNSUPPORTED, "head_dim = %d is above %d", D, kMaxHeadDim);
+  for (int i = 0; i < plan->t; ++i)
+    if (plan->dq_i[i] % D || plan->dkv_i[i] % D)
+      return fail(TPMLP_ERR_SHAPE, "shard %d: dq_i = %lld and dkv_i = %lld must be multiples of head_dim = %d", i,
+                  static_cast<long long>(plan->dq_i[i]), static_cast<long long>(plan->dkv_i[i]), D);
+  if (desc->norm && !(desc->eps > 0.0f && std::isfinite(desc->eps)))
+    return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive number", static_cast<double>(desc->eps));
+  if (R && !desc->inv_freq && !(desc->base > 0.0 && std::isfinite(desc->base)))
+    return fail(TPMLP_ERR_INVALID_ARG, "base = %g is not a positive number", desc->base);
+  uint64_t freq[kMaxHeadDim / 2];
+  for (int j = 0; j < R / 2; ++j) {
+    const double f = desc->inv_freq ? desc->inv_freq[j] : std::pow(desc->base, -2.0 * j / R);
+    if (!std::isfinite(f)) return fail(TPMLP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", j);
+    // The fraction of a turn per position; whole turns do not count.
+    const double turns = f / 6.283185307179586476925286766559;
+    double frac = turns - std::floor(turns);
+    if (!(frac < 1.0)) frac = 0.0;  // a tiny negative frequency, rounded up to a whole turn
+    freq[j] = static_cast<uint64_t>(std::ldexp(frac, 64));
+  }
+  try {
+    plan->rope_freq.assign(freq, freq + R / 2);
+  } catch (const std::bad_alloc&) {
+    return fail(TPMLP_ERR_INVALID_ARG, "out of host memory");
+  }
+  plan->head_dim = D;
+  plan->rotary_dim = R;
+  plan->rope_pairs = desc->layout == TPMLP_ROPE_PAIRS;
+  plan->qk_norm = desc->norm;
+  plan->qk_eps = desc->norm ? desc->eps : 0.0f;
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_attn_qk_norm_rope_forward(const tpmlp_plan* plan, const void* const* QKV, const int64_t* positions,
+                                             const void* gq, const void* gk, void* const* QK,
+                                             tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(qk_checks(plan, QKV, positions, gq, gk));
+  TPMLP_TRY(check_array("QK", QK, plan->t, plan->T == 0));
+  if (plan->T == 0) return TPMLP_OK;
+  QkParams p = qk_params(plan, positions, gq, gk);
+  const int64_t es = esize(plan);
+  for (int i = 0; i < plan->t; ++i) {
+    const bool in_place = QK[i] == QKV[i];
+    const int64_t ldo = in_place ? plan->d_i[i] : plan->dq_i[i] + plan->dkv_i[i];
+    for (int j = 0; j < plan->t; ++j) {
+      if (!(in_place && j == i))
+        TPMLP_TRY(check_overlap("QK", i, QK[i], plan->T * ldo * es, "QKV", j, QKV[j], plan->T * plan->d_i[j] * es));
+    }
+    p.shards[i].x = QKV[i];
+    p.shards[i].out = QK[i];
+    p.shards[i].ldo = ldo;
+  }
+  DeviceInfo di;
+  TPMLP_TRY(device_info(&di));
+  cudaError_t e = launch_qk_norm_rope(p, plan->dtype == TPMLP_BF16, plan->rope_pairs, false, di.sms,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  ++g_last_launches;
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void* const* QKV,
+                                              const int64_t* positions, const void* gq, const void* gk,
+                                              const void* const* dQK, const void* const* dV, void* const* dQKV,
+                                              void* dgq, void* dgk, void* workspace, tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(qk_checks(plan, QKV, positions, gq, gk));
+  const bool tz = plan->T == 0;
+  TPMLP_TRY(check_array("dQK", dQK, plan->t, tz));
+  if (dV) TPMLP_TRY(check_array("dV", dV, plan->t, tz));
+  TPMLP_TRY(check_array("dQKV", dQKV, plan->t, tz));
+  TPMLP_TRY(check_ptr("dgq", dgq, true));
+  TPMLP_TRY(check_ptr("dgk", dgk, true));
+  const bool gains = dgq || dgk;
+  if (gains && !plan->qk_norm)
+    return fail(TPMLP_ERR_INVALID_ARG, "gain gradients without a norm (the plan rotates only)");
+  TPMLP_TRY(check_ptr("workspace", workspace, !gains));
+  const int64_t es = esize(plan);
+  DeviceInfo di;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (tz) {
+    if (!gains) return TPMLP_OK;
+    TPMLP_TRY(device_info(&di));
+    for (void* dg : {dgq, dgk})
+      if (dg) {
+        cudaError_t e = cudaMemsetAsync(dg, 0, static_cast<size_t>(plan->head_dim * es), st);
+        if (e != cudaSuccess) return cuda_fail(e);
+      }
+    return TPMLP_OK;
+  }
+  QkParams p = qk_params(plan, positions, gq, gk);
+  for (int i = 0; i < plan->t; ++i) {
+    const int64_t n = plan->T * plan->d_i[i] * es;
+    const bool in_place = dQK[i] == dQKV[i];
+    for (int j = 0; j < plan->t; ++j) {
+      const int64_t qk = plan->T * (plan->dq_i[j] + plan->dkv_i[j]) * es, v = plan->T * plan->dkv_i[j] * es;
+      TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "QKV", j, QKV[j], plan->T * plan->d_i[j] * es));
+      if (!(in_place && j == i)) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dQK", j, dQK[j], qk));
+      if (dV) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dV", j, dV[j], v));
+    }
+    QkShard& S = p.shards[i];
+    S.x = QKV[i];
+    S.dy = dQK[i];
+    S.dv = dV ? dV[i] : nullptr;
+    S.out = dQKV[i];
+    S.lddy = in_place ? plan->d_i[i] : plan->dq_i[i] + plan->dkv_i[i];
+    S.ldo = plan->d_i[i];
+    if (dV) p.values += plan->dkv_i[i];
+  }
+  if (gains)
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                         (plan->dtype == TPMLP_BF16 ? kSkSlotsOffset : kStatusBytes));
+  TPMLP_TRY(device_info(&di));
+  const bool bf16 = plan->dtype == TPMLP_BF16;
+  cudaError_t e = launch_qk_norm_rope(p, bf16, plan->rope_pairs, true, di.sms, st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  ++g_last_launches;
+  if (gains) {
+    e = launch_qk_gain_grad(p, bf16, dgq, dgk, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+    ++g_last_launches;
+  }
+  return TPMLP_OK;
+}
+
+size_t tpmlp_ckpt8_size(int64_t rows, int64_t cols) {
+  const int64_t kMax32 = (int64_t(1) << 31) - 1;
+  if (rows < 0 || cols < 0 || rows > kMax32 || cols > kMax32) return 0;
+  return static_cast<size_t>(ck::bytes(rows, cols));
+}
+
+tpmlp_status ckpt8_checks(tpmlp_dtype dtype, int64_t rows, int64_t cols, const char* name, const void* x, int64_t ld,
+                          const void* ckpt) {
+  g_last_error[0] = 0;
+  if (dtype != TPMLP_BF16 && dtype != TPMLP_FP32)
+    return fail(TPMLP_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dtype));
+  const int64_t mult = dtype == TPMLP_BF16 ? 8 : 4, es = dtype == TPMLP_BF16 ? 2 : 4;
+  const int64_t kMax32 = (int64_t(1) << 31) - 1;
+  if (rows < 0 || cols < 1 || ld < cols)
+    return fail(TPMLP_ERR_SHAPE, "need rows >= 0, cols >= 1, ld >= cols (got rows=%lld cols=%lld ld=%lld)",
+                static_cast<long long>(rows), static_cast<long long>(cols), static_cast<long long>(ld));
+  if (cols % mult || ld % mult)
+    return fail(TPMLP_ERR_ALIGNMENT, "cols = %lld and ld = %lld must be multiples of %lld",
+                static_cast<long long>(cols), static_cast<long long>(ld), static_cast<long long>(mult));
+  if (rows > kMax32 || ld > kMax32) return fail(TPMLP_ERR_UNSUPPORTED, "rows, cols and ld must each be below 2^31");
+  TPMLP_TRY(check_ptr(name, x, rows == 0));
+  TPMLP_TRY(check_ptr("ckpt", ckpt, rows == 0));
+  if (rows && overlap(x, ((rows - 1) * ld + cols) * es, ckpt, ck::bytes(rows, cols)))
+    return fail(TPMLP_ERR_INVALID_ARG, "%s overlaps ckpt", name);
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_ckpt8_pack(tpmlp_dtype dtype, int64_t rows, int64_t cols, const void* src, int64_t ld, void* ckpt,
+                              tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(ckpt8_checks(dtype, rows, cols, "src", src, ld, ckpt));
+  if (rows == 0) return TPMLP_OK;
+  DeviceInfo di;
+  TPMLP_TRY(device_info(&di));
+  cudaError_t e = launch_ckpt8_pack(dtype == TPMLP_BF16, rows, cols, src, ld, ckpt,
+                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  ++g_last_launches;
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_ckpt8_unpack(tpmlp_dtype dtype, int64_t rows, int64_t cols, const void* ckpt, void* dst, int64_t ld,
+                                tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(ckpt8_checks(dtype, rows, cols, "dst", dst, ld, ckpt));
+  if (rows == 0) return TPMLP_OK;
+  DeviceInfo di;
+  TPMLP_TRY(device_info(&di));
+  cudaError_t e = launch_ckpt8_unpack(dtype == TPMLP_BF16, rows, cols, ckpt, dst, ld,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  ++g_last_launches;
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_forward_ckpt8(const tpmlp_plan* plan, const void* X, const void* const* W1, const void* const* W3,
+                                 const void* const* W2, const void* const* b1, const void* const* b3, const void* b2,
+                                 void* Y, void* const* ckpt, void* const* H, void* workspace, tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  DeviceInfo di;
+  TPMLP_TRY(common_checks(plan, workspace, &di));
+  const bool tz = plan->T == 0;
+  TPMLP_TRY(check_ptr("X", X, tz)); TPMLP_TRY(check_ptr("Y", Y, tz));
+  TPMLP_TRY(check_array("W1", W1, plan->t, false));
+  if (swiglu(plan)) TPMLP_TRY(check_array("W3", W3, plan->t, false));
+  TPMLP_TRY(check_array("W2", W2, plan->t, false));
+  TPMLP_TRY(check_array("ckpt", ckpt, nsaved(plan), tz));
+  TPMLP_TRY(check_array("H", H, plan->t, tz));
+  TPMLP_TRY(check_bias("b1", b1, plan->t));
+  if (swiglu(plan)) TPMLP_TRY(check_bias("b3", b3, plan->t));
+  TPMLP_TRY(check_ptr("b2", b2, true));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TPMLP_TRY(fwd_column(plan, di, X, W1, W3, b1, swiglu(plan) ? b3 : nullptr, ckpt, H, workspace, st, nullptr,
+                       /*ckpt8=*/true));
+  return fwd_row(plan, di, W2, b2, Y, H, workspace, st);
+}
+
+tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* X, const void* const* W1, const void* const* W3,
+                                  const void* const* W2, const void* const* ckpt, void* const* H, const void* dY,
+                                  void* const* dact, void* dX, void* const* dW1, void* const* dW3, void* const* dW2,
+                                  void* const* db1, void* const* db3, void* db2, void* workspace,
+                                  tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  DeviceInfo di;
+  TPMLP_TRY(common_checks(plan, workspace, &di));
+  const bool tz = plan->T == 0;
+  TPMLP_TRY(check_ptr("X", X, tz)); TPMLP_TRY(check_ptr("dY", dY, tz)); TPMLP_TRY(check_ptr("dX", dX, tz));
+  TPMLP_TRY(check_array("W1", W1, plan->t, false));
+  TPMLP_TRY(check_array("W2", W2, plan->t, false));
+  if (swiglu(plan)) {
+    TPMLP_TRY(check_array("W3", W3, plan->t, false));
+    TPMLP_TRY(check_array("dW3", dW3, plan->t, false));
+  }
+  TPMLP_TRY(check_array("ckpt", ckpt, nsaved(plan), tz));
+  TPMLP_TRY(check_array("H", H, plan->t, tz));
+  TPMLP_TRY(check_array("dact", dact, nsaved(plan), tz));
+  TPMLP_TRY(check_array("dW1", dW1, plan->t, false));
+  TPMLP_TRY(check_array("dW2", dW2, plan->t, false));
+  TPMLP_TRY(check_bias("db1", db1, plan->t));
+  if (swiglu(plan)) TPMLP_TRY(check_bias("db3", db3, plan->t));
+  TPMLP_TRY(check_ptr("db2", db2, true));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  void* const* db3_ = swiglu(plan) ? db3 : nullptr;
+  if (tz) {  // zero-filled gradients as in tpmlp_backward
+    TPMLP_TRY(bwd_dgrad(plan, di, W2, ckpt, H, dY, dact, dW2, db2, workspace, st));
+    return bwd_fsum(plan, di, X, W1, W3, dact, dX, dW1, dW3, db1, db3_, workspace, st);
+  }
+  TPMLP_TRY(bwd_dgrad(plan, di, W2, ckpt, H, dY, dact, dW2, db2, workspace, st, /*recompute=*/true, nullptr,
+                      /*ckpt8=*/true));
+  return bwd_fsum(plan, di, X, W1, W3, dact, dX, dW1, dW3, db1, db3_, workspace, st, H, dY, dW2);
 }
 
 tpmlp_status tpmlp_plan_set_sequence_stripes(tpmlp_plan* plan, int32_t nstripes, const int64_t* stripe_rows) {

@@ -242,6 +242,7 @@ struct GemmParams {
   int32_t tile_m;
   int32_t* status;          // device status word (workspace)
   uint64_t timeout_ns;      // bound on every wait inside the kernel
+  int32_t ckpt8;            // out0 / out1 of the activation forward epilogues and aux0 / aux1 of the backward ones are 8-bit checkpoints
   int32_t stall_injection;  // test hook: 1, producers load nothing; 2, stream-K parts but a tile's first run late
 };
 
@@ -274,6 +275,40 @@ int colsum_strip_cols(bool bf16, int lane_threads);
 ColsumShape colsum_shape(const ColsumJob* jobs, int num_jobs, bool bf16, int sms);
 cudaError_t launch_colsum(const ColsumParams& p, bool bf16, ColsumShape shape, cudaStream_t stream);
 
+// Norm of the query and key heads with the position rotation
+// (qk_norm_rope.cu).  Kind 0: queries, 1: keys, 2: the copy of dV.
+constexpr int kMaxHeadDim = 256;
+constexpr int kQkMaxCtas = 4096;  // bound of a launch's CTAs: rows of its partial gain gradients
+struct QkShard {
+  const void* x;   // [T x ldx]: q | k | v before the norm
+  const void* dy;  // [T x lddy]: gradient of the rotated q | k (backward)
+  const void* dv;  // [T x dkv] (backward, optional)
+  void* out;       // [T x ldo]: rotated q | k, or dq | dk | dv
+  int64_t ldx, lddy, ldo;
+  int32_t col[2];  // first query and key column (of x, dy and out alike)
+  int32_t vcol, dkv;
+};
+struct QkParams {
+  QkShard shards[kMaxShards];
+  int32_t head_end[2][kMaxShards];    // heads of the kind in shards 0 .. i
+  uint64_t freq[kMaxHeadDim / 2];     // turns per position, as a fraction of 2^64
+  const int64_t* pos;                 // [T], or null: 0, 1, 2, ...
+  const void* gain[2];                // [D], or null: ones
+  float* partial;                     // [CTAs x D] sums of the gain's gradient (backward), or null
+  int64_t T, values;                  // tokens; value columns to copy
+  int32_t t, D, R, norm;
+  float eps;
+  int32_t lanes, heads[2], parts[2], cta_end[3];  // set by the launcher, but heads
+};
+cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, int sms, cudaStream_t stream);
+cudaError_t launch_qk_gain_grad(const QkParams& p, bool bf16, void* dgq, void* dgk, cudaStream_t stream);
+
+// 8-bit checkpoints (ckpt8.cuh has the format).
+cudaError_t launch_ckpt8_pack(bool bf16, int64_t rows, int64_t cols, const void* src, int64_t ld, void* ckpt,
+                              cudaStream_t stream);
+cudaError_t launch_ckpt8_unpack(bool bf16, int64_t rows, int64_t cols, const void* ckpt, void* dst, int64_t ld,
+                                cudaStream_t stream);
+
 // Kernel parameters live in the 32 KB parameter space (__grid_constant__).
 static_assert(sizeof(GemmParams) <= 32000, "kernel parameter block too large");
 
@@ -305,6 +340,9 @@ constexpr int kShortKBlocks = 8;  // K <= 1024
 // (Prob::k_rev).
 constexpr int kRevKBlocks = 48;  // K > 6016
 int tc_epi_warps_for(const GemmParams& p, int kernel_tag);
+// The kernels of the launches with 8-bit checkpoints (column and dgrad).
+using TcKernelFn = void (*)(GemmParams);
+TcKernelFn tc_ckpt8_kernel(int tag, bool stream_k, int epi_warps);
 cudaError_t launch_simt_gemm(const GemmParams& p, cudaStream_t stream);
 // The epilogues' activation forms on plain arrays (tpmlp_eval_activation).
 cudaError_t launch_act_eval(int fn, const float* x, const float* y, const float* dh, float* o0, float* o1,
