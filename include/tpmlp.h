@@ -337,13 +337,14 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * Backward, from dy: w = dy rotated back, n = x r, s = w g:
  *   dx = r (s - n mean(s n)),   dg = sum over tokens, shards and heads of w n
  * (norm = 0: dx = w).  x is the QKV buffer as the projection wrote it: keep it.
- * Rows with a NaN or an infinity spoil their own head and the gain's gradient
- * only.
+ * A head with a NaN or an infinity spoils itself and the gain's gradient only;
+ * so does one whose sum of squares passes the fp32 range (elements above about
+ * 10^18).
  *
  * tpmlp_attn_plan_set_qk_norm_rope describes the heads (copied into the plan,
  * inv_freq included; may not run while another call uses the plan).  Every
- * dq_i and dkv_i must be a multiple of head_dim, an even number up to 256;
- * rotary_dim is even, 0 (norm only) to head_dim.  With an fp32 plan and
+ * dq_i and dkv_i must be a multiple of head_dim, an even number up to 256, with
+ * at most 4096 query heads and 4096 key heads over all shards; rotary_dim is even, 0 (norm only) to head_dim.  With an fp32 plan and
  * norm = 1 tpmlp_workspace_size grows: query it after this call.  Errors:
  * TPMLP_ERR_INVALID_ARG (NULL, an MLP plan, unknown layout, norm not 0 or 1,
  * eps, base or inv_freq not usable), TPMLP_ERR_SHAPE, TPMLP_ERR_UNSUPPORTED

@@ -215,8 +215,8 @@ def _addr(x) -> Optional[int]:
 
 
 def _arr(xs) -> Optional[ctypes.Array]:
-    if xs is None:
-        return None
+    if xs is None or isinstance(xs, ctypes.Array):
+        return xs
     return (ctypes.c_void_p * len(xs))(*[_addr(x) for x in xs])
 
 
@@ -534,59 +534,72 @@ def _tdtype(dtype: str):
     return {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
 
 
-def _check(name: str, x, shape, dtype, device):
-    """One tensor argument of the classes below: shape, dtype and device (contiguity is checked with its address)."""
-    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or x.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} of {dtype} on {device}, got {tuple(x.shape)} of {x.dtype} "
-                         f"on {x.device}")
+def _ptr(name: str, x, shape, dtype, device) -> int:
+    """The address of a tensor argument of the classes below, which has to be a dense tensor of this shape, type
+    and device."""
+    if x.shape != shape or x.dtype != dtype or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} tensor of {dtype} on {device}, got "
+                         f"{tuple(x.shape)} of {x.dtype} on {x.device}, strides {x.stride()}")
+    return x.data_ptr()
 
 
-def _check_list(name: str, xs, shapes, dtype, device):
-    if len(xs) != len(shapes):
-        raise ValueError(f"{name}: expected {len(shapes)} tensors, got {len(xs)}")
-    for i, (x, s) in enumerate(zip(xs, shapes)):
-        _check(f"{name}[{i}]", x, s, dtype, device)
+def _ptrs(name: str, xs, shapes, dtype, device):
+    if xs is None or len(xs) != len(shapes):
+        raise ValueError(f"{name}: expected {len(shapes)} tensors, got {0 if xs is None else len(xs)}")
+    return (ctypes.c_void_p * len(shapes))(*[_ptr(name, x, s, dtype, device) for x, s in zip(xs, shapes)])
 
 
-def _device(device):
-    import torch
-    d = torch.device(device or "cuda")
-    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
-
-
-@contextlib.contextmanager
 def _on(device, stream):
-    """The call's device and stream as the current ones, so that what it allocates belongs to that stream.
-    stream: None (the device's current one), a torch stream or a raw handle (0: the default stream)."""
+    """A context with the call's device and stream as the current ones, so that what the call allocates belongs to
+    that stream.  stream: None (the device's current one), a torch stream or a raw handle (0: the default stream)."""
     import torch
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-            return
-        if not hasattr(stream, "cuda_stream"):
-            handle = int(stream)
-            stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-        with torch.cuda.stream(stream):
-            yield
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _pieces(nbytes, device):
+    """One uninitialised buffer cut into pieces of these sizes (multiples of 256 bytes apart): (buffer, addresses)."""
+    import torch
+    at, total = [], 0
+    for n in nbytes:
+        at.append(total)
+        total += (n + 255) // 256 * 256
+    buf = torch.empty(total, dtype=torch.uint8, device=device)
+    base = buf.data_ptr()
+    return buf, [base + a for a in at]
+
+
+def _rows_apart(name, x):
+    """(address, row stride) of a 2-D tensor whose rows are contiguous but may lie apart."""
+    if not x.numel():
+        return None, x.shape[1]
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: the rows must be contiguous, got strides {x.stride()}")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
 def ckpt8_pack(x, out=None, stream=None):
     """The 8-bit checkpoint (a uint8 tensor of tpmlp_ckpt8_size bytes) of a 2-D bf16 or fp32 CUDA tensor, whose rows
     may be further apart than they are long (a column slice)."""
     import torch
-    names = {torch.bfloat16: "bf16", torch.float32: "fp32"}
-    if x.dim() != 2 or x.dtype not in names or not x.is_cuda:
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32) or not x.is_cuda:
         raise ValueError("expected a 2-D bf16 or fp32 CUDA tensor")
     rows, cols = x.shape
-    if x.numel() and cols > 1 and x.stride(1) != 1:
-        raise ValueError("the rows must be contiguous")
-    ld = x.stride(0) if rows > 1 else cols
+    src, ld = _rows_apart("x", x)
     n = tpmlp_ckpt8_size(rows, cols)
     with _on(x.device, stream):
         if out is None:
             out = torch.empty(n, dtype=torch.uint8, device=x.device)
-        _check("out", out, (n,), torch.uint8, x.device)
-        tpmlp_ckpt8_pack(names[x.dtype], rows, cols, (x.data_ptr() or None) if x.numel() else None, ld, out)
+        tpmlp_ckpt8_pack("bf16" if x.dtype == torch.bfloat16 else "fp32", rows, cols, src, ld,
+                         _ptr("out", out, (n,), torch.uint8, x.device))
     return out
 
 
@@ -594,17 +607,17 @@ def ckpt8_unpack(ckpt, rows: int, cols: int, dtype: str = "bf16", out=None, stre
     """The [rows x cols] tensor that a checkpoint stands for; out: a tensor to write it to (rows may lie apart)."""
     import torch
     td = _tdtype(dtype)
-    _check("ckpt", ckpt, (tpmlp_ckpt8_size(rows, cols),), torch.uint8, ckpt.device)
     if not ckpt.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
+    src = _ptr("ckpt", ckpt, (tpmlp_ckpt8_size(rows, cols),), torch.uint8, ckpt.device)
     with _on(ckpt.device, stream):
         if out is None:
             out = torch.empty(rows, cols, dtype=td, device=ckpt.device)
-        _check("out", out, (rows, cols), td, ckpt.device)
-        if out.numel() and cols > 1 and out.stride(1) != 1:
-            raise ValueError("the rows must be contiguous")
-        ld = out.stride(0) if rows > 1 else cols
-        tpmlp_ckpt8_unpack(dtype, rows, cols, ckpt, (out.data_ptr() or None) if out.numel() else None, ld)
+        elif out.shape != (rows, cols) or out.dtype != td or out.device != ckpt.device:
+            raise ValueError(f"out: expected {(rows, cols)} of {td} on {ckpt.device}, got {tuple(out.shape)} of "
+                             f"{out.dtype} on {out.device}")
+        dst, ld = _rows_apart("out", out)
+        tpmlp_ckpt8_unpack(dtype, rows, cols, src, dst, ld)
     return out
 
 
@@ -682,63 +695,58 @@ class ShardedMLP:
         return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "dact": dact, "db1": db1, "db3": db3, "db2": db2}
 
     # ---- 8-bit activation checkpoints: what backward needs of the pre-activations in 1.0625 bytes each
-    def _weight_shapes(self):
-        p = self.plan
-        return [(p.d, w) for w in p.d_i], [(w, p.d) for w in p.d_i]
-
-    def _check_mlp(self, X, W1_i, W2_i, W3_i, more=()):
-        p, dev = self.plan, _device(self.device)
-        col, row = self._weight_shapes()
-        _check("X", X, (p.T, p.d), self.tdtype, dev)
-        _check_list("W1_i", W1_i, col, self.tdtype, dev)
-        _check_list("W2_i", W2_i, row, self.tdtype, dev)
-        if self.swiglu:
-            _check_list("W3_i", W3_i if W3_i is not None else (), col, self.tdtype, dev)
-        for name, x, shape in more:
-            if x is not None:
-                _check(name, x, shape, self.tdtype, dev)
-        return dev
-
-    def _check_biases(self, dev, b1_i, b3_i):
-        for name, b in (("b1_i", b1_i), ("b3_i", b3_i if self.swiglu else None)):
-            if b is not None:
-                _check_list(name, b, [(w,) for w in self.plan.d_i], self.tdtype, dev)
-
     def ckpt8_sizes(self):
         """Bytes of each checkpoint: one per shard (A_i), SwiGLU two (G_i, then U_i)."""
-        return [tpmlp_ckpt8_size(self.plan.T, w) for w in self.plan.d_i * (2 if self.swiglu else 1)]
+        return [tpmlp_ckpt8_size(self.plan.T, w) for w in self.plan.d_i] * (2 if self.swiglu else 1)
+
+    def _ckpt8_args(self, X, W1_i, W2_i, W3_i):
+        """Checked addresses of the inputs that both passes share, and the shapes they are checked by."""
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        col, row = [(p.d, w) for w in p.d_i], [(w, p.d) for w in p.d_i]
+        return (_ptr("X", X, (p.T, p.d), td, dev), _ptrs("W1_i", W1_i, col, td, dev),
+                _ptrs("W3_i", W3_i, col, td, dev) if self.swiglu else None, _ptrs("W2_i", W2_i, row, td, dev), col, row)
 
     def forward_ckpt8(self, X, W1_i, W2_i, W3_i=None, stream=None, b1_i=None, b3_i=None, b2=None, out=None):
         """forward with the pre-activations kept as 8-bit checkpoints.  Returns (Y, ckpt); out: those two, to write
         to.  H is scratch of the call."""
         import torch
-        p = self.plan
-        dev = self._check_mlp(X, W1_i, W2_i, W3_i, [("b2", b2, (p.d,))])
-        self._check_biases(dev, b1_i, b3_i)
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        x, w1, w3, w2, _, _ = self._ckpt8_args(X, W1_i, W2_i, W3_i)
+        wide = [(w,) for w in p.d_i]
+        b1 = _ptrs("b1_i", b1_i, wide, td, dev) if b1_i is not None else None
+        b3 = _ptrs("b3_i", b3_i, wide, td, dev) if b3_i is not None and self.swiglu else None
+        b2 = _ptr("b2", b2, (p.d,), td, dev) if b2 is not None else None
+        sizes = self.ckpt8_sizes()
         with _on(dev, stream):
             if out is None:
-                out = (self._empty(p.T, p.d),
-                       [torch.empty(n, dtype=torch.uint8, device=dev) for n in self.ckpt8_sizes()])
+                out = X.new_empty((p.T, p.d)), [torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes]
             Y, ckpt = out
-            _check("Y", Y, (p.T, p.d), self.tdtype, dev)
-            _check_list("ckpt", ckpt, [(n,) for n in self.ckpt8_sizes()], torch.uint8, dev)
-            H = [self._empty(p.T, w) for w in p.d_i]
-            tpmlp_forward_ckpt8(p, X, W1_i, W3_i if self.swiglu else None, W2_i, b1_i, b3_i if self.swiglu else None,
-                                b2, Y, ckpt, H, self.workspace)
+            scratch, H = _pieces([p.T * w * X.element_size() for w in p.d_i], dev)
+            tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, _ptr("Y", Y, (p.T, p.d), td, dev),
+                                _ptrs("ckpt", ckpt, [(n,) for n in sizes], torch.uint8, dev), H, self.workspace)
         return Y, ckpt
 
     def backward_ckpt8(self, X, W1_i, W2_i, ckpt, dY, W3_i=None, stream=None, bias_grads=False, out=None):
-        """Gradients as backward gives them (without "dact"), from the checkpoints that forward_ckpt8 wrote."""
+        """Gradients as backward gives them (without "dact"), from the checkpoints that forward_ckpt8 wrote.  out:
+        (dX, dW1, dW3, dW2) to write to (dW3: None for GeLU)."""
         import torch
-        p = self.plan
-        dev = self._check_mlp(X, W1_i, W2_i, W3_i, [("dY", dY, (p.T, p.d))])
-        _check_list("ckpt", ckpt, [(n,) for n in self.ckpt8_sizes()], torch.uint8, dev)
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        x, w1, w3, w2, col, row = self._ckpt8_args(X, W1_i, W2_i, W3_i)
+        dy = _ptr("dY", dY, (p.T, p.d), td, dev)
+        c = _ptrs("ckpt", ckpt, [(n,) for n in self.ckpt8_sizes()], torch.uint8, dev)
+        es = X.element_size()
         with _on(dev, stream):
-            dact, dX, dW1, dW3, dW2 = out if out is not None else self.alloc_backward()
+            if out is None:
+                out = (X.new_empty((p.T, p.d)), [X.new_empty(s) for s in col],
+                       [X.new_empty(s) for s in col] if self.swiglu else None, [X.new_empty(s) for s in row])
+            dX, dW1, dW3, dW2 = out
             db1, db3, db2 = self.alloc_bias_grads() if bias_grads else (None, None, None)
-            H = [self._empty(p.T, w) for w in p.d_i]
-            tpmlp_backward_ckpt8(p, X, W1_i, W3_i if self.swiglu else None, W2_i, ckpt, H, dY, dact, dX, dW1, dW3,
-                                 dW2, db1, db3, db2, self.workspace)
+            wide = [p.T * w * es for w in p.d_i]
+            scratch, at = _pieces(wide * (3 if self.swiglu else 2), dev)  # H_i, then dact
+            tpmlp_backward_ckpt8(p, x, w1, w3, w2, c, at[:p.t], dy, at[p.t:], _ptr("dX", dX, (p.T, p.d), td, dev),
+                                 _ptrs("dW1", dW1, col, td, dev),
+                                 _ptrs("dW3", dW3, col, td, dev) if self.swiglu else None,
+                                 _ptrs("dW2", dW2, row, td, dev), db1, db3, db2, self.workspace)
         return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "db1": db1, "db3": db3, "db2": db2}
 
     def check(self, stream=None):
@@ -822,61 +830,57 @@ class ShardedAttentionProj:
         if n > self.workspace.numel():
             self.workspace = torch.zeros(n, dtype=torch.uint8, device=self.device)
 
-    def _check_qk(self, QKV_i, positions, gq, gk):
-        p, dev = self.plan, _device(self.device)
-        if not hasattr(p, "head_dim"):
+    def _qk_args(self, QKV_i, positions, gq, gk):
+        """Checked addresses of the inputs that both passes share."""
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        D = getattr(p, "head_dim", 0)
+        if not D:
             raise ValueError("the heads are not described (set_qk_norm_rope)")
-        _check_list("QKV_i", QKV_i, [(p.T, n) for n in p.d_i], self.tdtype, dev)
-        for name, g in (("gq", gq), ("gk", gk)):
-            if g is not None:
-                _check(name, g, (p.head_dim,), self.tdtype, dev)
-        if positions is not None and positions.device != dev:
-            raise ValueError(f"positions: expected on {dev}, got on {positions.device}")
-        return dev
+        import torch
+        return (_ptrs("QKV_i", QKV_i, [(p.T, n) for n in p.d_i], td, dev),
+                _ptr("positions", positions, (p.T,), torch.int64, dev) if positions is not None else None,
+                _ptr("gq", gq, (D,), td, dev) if gq is not None else None,
+                _ptr("gk", gk, (D,), td, dev) if gk is not None else None)
+
+    def _in_place_or_dense(self, name, xs, fused):
+        """[T, dq_i + dkv_i] tensors, or the [T, n_i] ones at the addresses `fused`."""
+        p = self.plan
+        if len(xs) != p.t:
+            raise ValueError(f"{name}: expected {p.t} tensors, got {len(xs)}")
+        shapes = [(p.T, n if p.T and x.data_ptr() == f else q + k)
+                  for x, f, n, q, k in zip(xs, fused, p.d_i, p.dq_i, p.dkv_i)]
+        return _ptrs(name, xs, shapes, self.tdtype, self.workspace.device)
 
     def qk_norm_rope_forward(self, QKV_i, positions=None, gq=None, gk=None, out=None, stream=None):
         """The normed and rotated heads [Q_i | K_i] of each shard.  out: [T, dq_i + dkv_i] tensors, or QKV_i itself
         (in place: the value columns stay as they are)."""
-        import torch
         p = self.plan
-        dev = self._check_qk(QKV_i, positions, gq, gk)
-        with _on(dev, stream):
+        qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk)
+        with _on(self.workspace.device, stream):
             if out is None:
-                out = [self._empty(p.T, q + k) for q, k in zip(p.dq_i, p.dkv_i)]
-            self._check_in_place("out", out, QKV_i, dev)
-            tpmlp_attn_qk_norm_rope_forward(p, QKV_i, positions, gq, gk, out)
+                out = [x.new_empty((p.T, q_ + k_)) for x, q_, k_ in zip(QKV_i, p.dq_i, p.dkv_i)]
+            tpmlp_attn_qk_norm_rope_forward(p, qkv, pos, q, k, self._in_place_or_dense("out", out, qkv))
         return out
-
-    def _check_in_place(self, name, xs, fused, dev):
-        p = self.plan
-        if len(xs) != p.t:
-            raise ValueError(f"{name}: expected {p.t} tensors, got {len(xs)}")
-        for i, (x, f) in enumerate(zip(xs, fused)):
-            same = p.T and x.data_ptr() == f.data_ptr()
-            _check(f"{name}[{i}]", x, (p.T, p.d_i[i] if same else p.dq_i[i] + p.dkv_i[i]), self.tdtype, dev)
 
     def qk_norm_rope_backward(self, QKV_i, dQK_i, positions=None, gq=None, gk=None, dV_i=None, out=None, stream=None,
                               gain_grads=None):
         """(dQKV_i, dgq, dgk) from the core's [dQ_i | dK_i] and, optionally, dV_i [T, dkv_i].  out: the dQKV_i to
         write to; their value columns stay as they are without dV_i.  dQK_i may be those tensors themselves.
         gain_grads: whether to compute dgq and dgk (None: if a gain is given)."""
-        import torch
-        p = self.plan
-        dev = self._check_qk(QKV_i, positions, gq, gk)
-        if dV_i is not None:
-            _check_list("dV_i", dV_i, [(p.T, k) for k in p.dkv_i], self.tdtype, dev)
-        elif out is None:
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk)
+        dv = _ptrs("dV_i", dV_i, [(p.T, w) for w in p.dkv_i], td, dev) if dV_i is not None else None
+        if dV_i is None and out is None:
             raise ValueError("dV_i, or dQKV_i that hold dV already (out), must be given")
         if gain_grads is None:
             gain_grads = gq is not None or gk is not None
         with _on(dev, stream):
             if out is None:
-                out = [self._empty(p.T, n) for n in p.d_i]
-            _check_list("out", out, [(p.T, n) for n in p.d_i], self.tdtype, dev)
-            self._check_in_place("dQK_i", dQK_i, out, dev)
+                out = [x.new_empty(x.shape) for x in QKV_i]
+            dqkv = _ptrs("out", out, [(p.T, n) for n in p.d_i], td, dev)
             dgq, dgk = (self._empty(p.head_dim), self._empty(p.head_dim)) if gain_grads else (None, None)
-            tpmlp_attn_qk_norm_rope_backward(p, QKV_i, positions, gq, gk, dQK_i, dV_i, out, dgq, dgk,
-                                             self.workspace)
+            tpmlp_attn_qk_norm_rope_backward(p, qkv, pos, q, k, self._in_place_or_dense("dQK_i", dQK_i, dqkv), dv,
+                                             dqkv, dgq, dgk, self.workspace)
         return out, dgq, dgk
 
     def check(self, stream=None):

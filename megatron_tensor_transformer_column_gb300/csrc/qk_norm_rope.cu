@@ -19,20 +19,26 @@
 //
 // Layout of the work.  HBM-bound: a head is read and written once.  A lane
 // holds a unit: V pairs, i.e. two vectors of V elements, both partners of each
-// pair, so that the rotation needs no exchange; L lanes (a power of two)
-// share a head and add its sum of squares by shuffles; a warp takes 32 / L
-// heads at a time, all heads of one kind (queries or keys) of one token, one
-// after another, with that token's sines and cosines in registers.  CTAs belong
-// to one kind, so that the gains (and, backward, the lane's sums of the gain's
-// gradient) stay in registers for the whole launch; the host deals the CTAs
-// to the kinds in proportion to their bytes.  With few tokens the heads of a
-// token are split over several warps.
+// pair, so that the rotation needs no exchange.  n lanes share a head and add
+// its sums by shuffles; a warp takes 32 / n heads at a time (a round), all
+// heads of one kind (queries or keys) of one token, round after round, with
+// that token's sines and cosines in registers: they are computed once per
+// token by all lanes, a pair each, and read back from shared memory.  Each
+// lane's vectors of the next kStages - 1 rounds, of the next tokens too, are
+// on their way into shared memory (16-byte asynchronous copies, a queue of
+// its own per lane, so that nothing waits but the lane): bytes in flight
+// without registers.  CTAs belong to one kind, so that the gains (and,
+// backward, the lane's sums of the gain's gradient) stay with the CTA for the
+// whole launch; the host deals the CTAs to the kinds by their work.  With few
+// tokens the heads of a token are split over several warps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
 
+#include "act.cuh"
+#include "ptx.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
@@ -40,6 +46,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxSmem = 227 * 1024;    // dynamic shared memory of a CTA
+constexpr int kSmemPerSm = 228 * 1024;  // of an SM, 1 KB of it taken by each CTA
 
 // V elements of the storage type at p, as floats.
 template <typename E, int V>
@@ -100,14 +108,89 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[V]) {
   }
 }
 
-// A unit of V pairs between its two stored vectors and the partners (a, b).
-// Halves: vector 0 holds the a's, vector 1 the b's.  Pairs: the 2V elements
-// are a0 b0 a1 b1 ...
-template <typename E, int V, bool kPairs>
-__device__ __forceinline__ void load_unit(const E* row, int o1, int o2, float (&a)[V], float (&b)[V]) {
-  float v1[V], v2[V];
-  load_vec<E, V>(row + o1, v1);
-  load_vec<E, V>(row + o2, v2);
+constexpr int kStages = 4;  // rounds of a lane's queue: one being worked on, three on their way
+
+// Element-wise operations on V floats, two at a time where V is even.
+template <int V>
+__device__ __forceinline__ void mul_v(const float (&a)[V], const float (&b)[V], float (&o)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+      act::x2::upk(act::x2::mul2(act::x2::pk(a[k], a[k + 1]), act::x2::pk(b[k], b[k + 1])), o[k], o[k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = a[k] * b[k];
+  }
+}
+template <int V>
+__device__ __forceinline__ void scale_v(const float (&a)[V], float s, float (&o)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+      act::x2::upk(act::x2::mul2(act::x2::pk(a[k], a[k + 1]), act::x2::splat(s)), o[k], o[k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = a[k] * s;
+  }
+}
+// o = a b + c
+template <int V>
+__device__ __forceinline__ void fma_v(const float (&a)[V], const float (&b)[V], const float (&c)[V], float (&o)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+      act::x2::upk(act::x2::fma2(act::x2::pk(a[k], a[k + 1]), act::x2::pk(b[k], b[k + 1]), act::x2::pk(c[k], c[k + 1])),
+                   o[k], o[k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = fmaf(a[k], b[k], c[k]);
+  }
+}
+// The sum of a b, two running sums where V is even.
+template <int V>
+__device__ __forceinline__ float dot_v(const float (&a)[V], const float (&b)[V], const float (&c)[V],
+                                       const float (&d)[V]) {
+  if constexpr (V % 2 == 0) {
+    uint64_t s = 0;
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      s = act::x2::fma2(act::x2::pk(a[k], a[k + 1]), act::x2::pk(b[k], b[k + 1]), s);
+      s = act::x2::fma2(act::x2::pk(c[k], c[k + 1]), act::x2::pk(d[k], d[k + 1]), s);
+    }
+    float s0, s1;
+    act::x2::upk(s, s0, s1);
+    return s0 + s1;
+  } else {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) s = fmaf(a[k], b[k], fmaf(c[k], d[k], s));
+    return s;
+  }
+}
+
+// V floats from shared memory.
+template <int V>
+__device__ __forceinline__ void read_v(const float* p, float (&o)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + k);
+      o[k] = q.x;
+      o[k + 1] = q.y;
+      o[k + 2] = q.z;
+      o[k + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = p[k];
+  }
+}
+
+// The partners (a, b) of a unit's V pairs between the registers and its two
+// stored vectors v1, v2.  Halves: v1 holds the a's, v2 the b's.  Pairs: the 2V
+// elements are a0 b0 a1 b1 ...
+template <int V, bool kPairs>
+__device__ __forceinline__ void to_partners(const float (&v1)[V], const float (&v2)[V], float (&a)[V], float (&b)[V]) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     if (kPairs && V > 1) {
@@ -118,6 +201,14 @@ __device__ __forceinline__ void load_unit(const E* row, int o1, int o2, float (&
       b[k] = v2[k];
     }
   }
+}
+
+template <typename E, int V, bool kPairs>
+__device__ __forceinline__ void load_unit(const E* p1, const E* p2, float (&a)[V], float (&b)[V]) {
+  float v1[V], v2[V];
+  load_vec<E, V>(p1, v1);
+  load_vec<E, V>(p2, v2);
+  to_partners<V, kPairs>(v1, v2, a, b);
 }
 
 template <typename E, int V, bool kPairs>
@@ -137,174 +228,378 @@ __device__ __forceinline__ void store_unit(E* row, int o1, int o2, const float (
   store_vec<E, V>(row + o2, v2);
 }
 
-// Where unit u of a head lies, and its first pair (-1: not rotated).  Halves:
-// the units of the rotated part, then the rest cut into neighbouring vectors.
+// Where unit u of a head lies; its pairs are V u .. V u + V - 1, those from
+// R / 2 on being no pairs but elements that are not rotated.  Halves: the units
+// of the rotated part, then the rest cut into neighbouring vectors.
 template <int V, bool kPairs>
-__device__ __forceinline__ void unit_at(int u, int R, int& o1, int& o2, int& j0) {
-  if (kPairs) {
-    o1 = 2 * V * u;
-    o2 = o1 + V;
-    j0 = V * u;
-    return;
-  }
-  const int ru = R / (2 * V);
+__device__ __forceinline__ void unit_at(int u, int R, int& o1, int& o2) {
+  const int ru = kPairs ? 0 : R / (2 * V);
   if (u < ru) {
     o1 = V * u;
     o2 = R / 2 + V * u;
-    j0 = V * u;
   } else {
-    o1 = R + 2 * V * (u - ru);
+    o1 = (kPairs ? 0 : R) + 2 * V * (u - ru);
     o2 = o1 + V;
-    j0 = R;  // past the last pair
   }
 }
 
-// The shard and the position in it of a kind's head h, counted over shards.
-__device__ __forceinline__ int shard_of_head(const QkParams& p, int kind, int h, int from) {
-  while (h >= p.head_end[kind][from]) ++from;
-  return from;
+// The sum over the n lanes of a group, to all of them (the same bits).
+__device__ __forceinline__ float group_sum(float s, int n, int li, int leader) {
+  if ((n & (n - 1)) == 0) {
+    for (int o = n >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+  int o = 16;
+  while (o >= n) o >>= 1;
+  for (; o > 0; o >>= 1) {
+    const float t = __shfl_down_sync(0xffffffffu, s, o);
+    if (li + o < n) s += t;
+  }
+  return __shfl_sync(0xffffffffu, s, leader);
 }
 
-// One kind's heads of a warp's tokens: this warp is w of nw of that kind,
-// part w % parts of the heads of tokens w / parts, + nw / parts, ...
-template <typename E, int V, int NU, bool kPairs, bool kBwd>
-__device__ __forceinline__ void qk_walk(const QkParams& p, int kind, int w, int nw, float (&dga)[NU][V],
-                                        float (&dgb)[NU][V]) {
-  const int lane = threadIdx.x & 31;
-  const int L = p.lanes;
-  const int G = 32 / L;  // heads of a warp at a time
-  const int grp = lane / L, li = lane % L;
-  const int units = p.D / (2 * V);
-  const int parts = p.parts[kind];
-  const int heads = p.heads[kind];
-  const float inv_d = 1.0f / static_cast<float>(p.D);
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (B == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-  int o1[NU], o2[NU];
-  bool on[NU];
-  float ga[NU][V], gb[NU][V];
-  uint64_t F[NU][V];
+// Shared memory of a CTA (bytes from the start of the dynamic part): the
+// kind's heads, the frequencies, the gains by unit, each warp's cosines and
+// sines, each warp's queue.
+struct Head {
+  int32_t shard, col;
+};
+template <int V>
+constexpr bool kQueue = V > 1;  // single elements are loaded when they are needed
+template <typename E, int V, bool kBwd>
+constexpr int queue_bytes() { return kQueue<V> ? kStages * (kBwd ? 4 : 2) * 32 * V * int(sizeof(E)) : 0; }
+__host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
+struct Place {
+  int freq, gain, angle, queue, total;
+};
+__host__ __device__ inline Place place(int heads, int D, int queue) {
+  Place p;
+  p.freq = round16(heads * int(sizeof(Head)));
+  p.gain = p.freq + round16(D / 2 * 8);
+  p.angle = p.gain + round16(D * 4);
+  p.queue = p.angle + kWarps * round16(D * 4);
+  p.total = p.queue + kWarps * queue;
+  return p;
+}
+
+// A position in a warp's sequence of (token, round).
+struct Cursor {
+  int64_t tok;
+  int h0;
+};
+__device__ __forceinline__ void cursor_next(Cursor& c, const QkParams& p, int first, int step, int heads, int rows) {
+  c.h0 += step;
+  if (c.h0 >= heads) {
+    c.h0 = first;
+    c.tok += rows;
+  }
+}
+
+template <typename E, int V, int NU, bool kPairs, bool kBwd>
+__device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int nw, uint8_t* smem) {
+  constexpr int kVecBytes = V * int(sizeof(E));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = p.lanes, G = p.groups;  // lanes of a head, heads of a round
+  const int grp = lane / n, li = lane - grp * n, leader = grp * n;
+  const int units = p.D / (2 * V), heads = p.heads[kind], parts = p.parts[kind];
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  const Place at = place(max(p.heads[0], p.heads[1]), p.D, queue_bytes<E, V, kBwd>());
+  Head* head = reinterpret_cast<Head*>(smem);
+  uint64_t* freq = reinterpret_cast<uint64_t*>(smem + at.freq);
+  float* gains = reinterpret_cast<float*>(smem + at.gain);  // by unit: V a's, V b's
+  float* cosines = reinterpret_cast<float*>(smem + at.angle + warp * round16(p.D * 4));
+  float* sines = cosines + p.D / 2;
+
+  // The CTA's tables.
+  for (int h = threadIdx.x; h < heads; h += kThreads) {
+    int s = 0;
+    while (h >= p.head_end[kind][s]) ++s;
+    head[h] = Head{s, p.shards[s].col[kind] + (h - (s ? p.head_end[kind][s - 1] : 0)) * p.D};
+  }
+  for (int j = threadIdx.x; j < p.R / 2; j += kThreads) freq[j] = p.freq[j];
   const E* g = static_cast<const E*>(p.gain[kind]);
+  for (int u = threadIdx.x; u < units; u += kThreads) {
+    int o1, o2;
+    unit_at<V, kPairs>(u, p.R, o1, o2);
+    float a[V], b[V];
 #pragma unroll
-  for (int n = 0; n < NU; ++n) {
-    const int u = li + n * L;
-    on[n] = u < units;
-    int j0;
-    unit_at<V, kPairs>(on[n] ? u : 0, p.R, o1[n], o2[n], j0);
+    for (int k = 0; k < V; ++k) a[k] = b[k] = 1.0f;
+    if (g) load_unit<E, V, kPairs>(g + o1, g + o2, a, b);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      ga[n][k] = gb[n][k] = 1.0f;
-      F[n][k] = 2 * (j0 + k) < p.R ? p.freq[j0 + k] : 0;  // 0: the rotation by no angle
+      gains[2 * V * u + k] = a[k];
+      gains[2 * V * u + V + k] = b[k];
     }
-    if (g && on[n]) load_unit<E, V, kPairs>(g, o1[n], o2[n], ga[n], gb[n]);
   }
+  for (int j = p.R / 2 + lane; j < p.D / 2; j += 32) {  // not rotated
+    cosines[j] = 1.0f;
+    sines[j] = 0.0f;
+  }
+  __syncthreads();
+
+  int o1[NU], o2[NU], un[NU];
+  bool on[NU];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int u = li + i * n;
+    on[i] = grp < G && u < units;
+    un[i] = on[i] ? u : 0;
+    unit_at<V, kPairs>(un[i], p.R, o1[i], o2[i]);
+  }
+  float dga[NU][V], dgb[NU][V];
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) dga[i][k] = dgb[i][k] = 0.0f;
 
   const int rows = nw / parts;  // tokens at a time; warps left over have none
-  for (int64_t tok = w < rows * parts ? w / parts : p.T; tok < p.T; tok += rows) {
-    const uint64_t pos = p.pos ? static_cast<uint64_t>(p.pos[tok]) : static_cast<uint64_t>(tok);
-    float cs[NU][V], sn[NU][V];
-#pragma unroll
-    for (int n = 0; n < NU; ++n)
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int32_t turn = static_cast<int32_t>((pos * F[n][k]) >> 32);  // in 2^-32 turns
-        sincospif(static_cast<float>(turn) * 0x1p-31f, &sn[n][k], &cs[n][k]);
-      }
-    int sh = 0;
-    for (int h0 = (w % parts) * G; h0 < heads; h0 += parts * G) {
-      const int h = h0 + grp;
-      const bool ok = h < heads;
-      sh = shard_of_head(p, kind, ok ? h : heads - 1, sh);
-      const QkShard& S = p.shards[sh];
-      const int col = S.col[kind] + ((ok ? h : heads - 1) - (sh ? p.head_end[kind][sh - 1] : 0)) * p.D;
-      const E* x = static_cast<const E*>(S.x) + tok * S.ldx + col;
-      float a[NU][V], b[NU][V], ya[NU][V], yb[NU][V];
-      float ss = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NU; ++n) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) a[n][k] = b[n][k] = ya[n][k] = yb[n][k] = 0.0f;
-        if (ok && on[n]) {
-          load_unit<E, V, kPairs>(x, o1[n], o2[n], a[n], b[n]);
-          if (kBwd)
-            load_unit<E, V, kPairs>(static_cast<const E*>(S.dy) + tok * S.lddy + col, o1[n], o2[n], ya[n], yb[n]);
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) ss = fmaf(a[n][k], a[n][k], fmaf(b[n][k], b[n][k], ss));
-      }
-      float r = 1.0f;
-      if (p.norm) {
-        for (int o = L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        r = rsqrtf(fmaf(ss, inv_d, p.eps));
-      }
-      E* out = static_cast<E*>(S.out) + tok * S.ldo + col;
-      if (!kBwd) {
-#pragma unroll
-        for (int n = 0; n < NU; ++n) {
-          if (!(ok && on[n])) continue;
-          float oa[V], ob[V];
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float ua = a[n][k] * r * ga[n][k], ub = b[n][k] * r * gb[n][k];
-            oa[k] = ua * cs[n][k] - ub * sn[n][k];
-            ob[k] = ub * cs[n][k] + ua * sn[n][k];
+  const int first = (w % parts) * G, step = parts * G;
+  Cursor get, run;  // what is fetched next, what is worked on next
+  run.tok = w < rows * parts && first < heads ? w / parts : p.T;
+  run.h0 = first;
+  get = run;
+
+  // The queue: slot s holds, per vector and lane, this lane's bytes of a round.
+  const uint32_t queue = ptx::smem_u32(smem + at.queue + warp * queue_bytes<E, V, kBwd>()) + lane * kVecBytes;
+  auto fetch = [&](int slot) {
+    if constexpr (kQueue<V>) {
+      if (get.tok < p.T) {
+        const int h = get.h0 + grp;
+        if (on[0] && h < heads) {
+          const Head H = head[h];
+          const QkShard& S = p.shards[H.shard];
+          const uint32_t q = queue + slot * (kBwd ? 4 : 2) * 32 * kVecBytes;
+          const E* x = static_cast<const E*>(S.x) + get.tok * S.ldx + H.col;
+          copy_async<kVecBytes>(q, x + o1[0]);
+          copy_async<kVecBytes>(q + 32 * kVecBytes, x + o2[0]);
+          if (kBwd) {
+            const E* y = static_cast<const E*>(S.dy) + get.tok * S.lddy + H.col;
+            copy_async<kVecBytes>(q + 64 * kVecBytes, y + o1[0]);
+            copy_async<kVecBytes>(q + 96 * kVecBytes, y + o2[0]);
           }
-          store_unit<E, V, kPairs>(out, o1[n], o2[n], oa, ob);
         }
-      } else {
-        float m = 0.0f;
+        cursor_next(get, p, first, step, heads, rows);
+      }
+      copy_commit();  // one group a round, an empty one past the end
+    }
+  };
+  if constexpr (kQueue<V>) {
 #pragma unroll
-        for (int n = 0; n < NU; ++n)
+    for (int s = 0; s < kStages - 1; ++s) fetch(s);
+  }
+  int slot = 0;
+  // The position of the next token is fetched a token ahead.
+  auto position = [&](int64_t tok) {
+    return tok < p.T && p.pos ? static_cast<uint64_t>(p.pos[tok]) : static_cast<uint64_t>(tok);
+  };
+  uint64_t pos = position(run.tok);
+
+  // Forward: the coefficients of a and b in a' and b'; backward: the cosines,
+  // sines and gains.
+  float c1[NU][V], c2[NU][V], c3[NU][V], c4[NU][V];
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float wa = ya[n][k] * cs[n][k] + yb[n][k] * sn[n][k];
-            const float wb = yb[n][k] * cs[n][k] - ya[n][k] * sn[n][k];
-            a[n][k] *= r;  // n = x r
-            b[n][k] *= r;
-            dga[n][k] = fmaf(wa, a[n][k], dga[n][k]);
-            dgb[n][k] = fmaf(wb, b[n][k], dgb[n][k]);
-            ya[n][k] = wa * ga[n][k];
-            yb[n][k] = wb * gb[n][k];
-            m = fmaf(ya[n][k], a[n][k], fmaf(yb[n][k], b[n][k], m));
-          }
-        if (p.norm) {
-          for (int o = L >> 1; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-          m *= inv_d;
+  for (int i = 0; i < NU; ++i) {
+    read_v<V>(gains + 2 * V * un[i], c1[i]);
+    read_v<V>(gains + 2 * V * un[i] + V, c2[i]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) c3[i][k] = c4[i][k] = 0.0f;
+  }
+
+  while (run.tok < p.T) {
+    if (run.h0 == first) {  // a new token
+      for (int j = lane; j < p.R / 2; j += 32) {
+        const int32_t turn = static_cast<int32_t>((pos * freq[j]) >> 32);  // in 2^-32 turns
+        float c, s;
+        sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
+        cosines[j] = c;
+        sines[j] = s;
+      }
+      pos = position(run.tok + rows);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        if (kBwd) {
+          read_v<V>(cosines + V * un[i], c3[i]);
+          read_v<V>(sines + V * un[i], c4[i]);
         } else {
-          m = 0.0f;
+          float cs[V], sn[V], ga[V], gb[V];
+          read_v<V>(cosines + V * un[i], cs);
+          read_v<V>(sines + V * un[i], sn);
+          read_v<V>(gains + 2 * V * un[i], ga);
+          read_v<V>(gains + 2 * V * un[i] + V, gb);
+          mul_v<V>(ga, cs, c1[i]);
+          mul_v<V>(gb, sn, c2[i]);
+          mul_v<V>(gb, cs, c3[i]);
+          mul_v<V>(ga, sn, c4[i]);
         }
+      }
+      __syncwarp();  // read before the next token's are written
+    }
+    fetch((slot + kStages - 1) % kStages);
+    copy_wait<kQueue<V> ? kStages - 1 : 0>();
+
+    const int h = run.h0 + grp;
+    const bool ok = grp < G && h < heads;
+    const Head H = head[ok ? h : 0];
+    const QkShard& S = p.shards[H.shard];
+    float a[NU][V], b[NU][V], ya[NU][V], yb[NU][V];
+    float ss = 0.0f, sx = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NU; ++n) {
-          if (!(ok && on[n])) continue;
-          float oa[V], ob[V];
+    for (int i = 0; i < NU; ++i) {
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            oa[k] = r * (ya[n][k] - a[n][k] * m);
-            ob[k] = r * (yb[n][k] - b[n][k] * m);
+      for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = ya[i][k] = yb[i][k] = 0.0f;
+      if (ok && on[i]) {
+        if constexpr (kQueue<V>) {
+          const E* q = reinterpret_cast<const E*>(smem + at.queue + warp * queue_bytes<E, V, kBwd>() +
+                                                  slot * (kBwd ? 4 : 2) * 32 * kVecBytes + lane * kVecBytes);
+          load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
+          if (kBwd) load_unit<E, V, kPairs>(q + 64 * V, q + 96 * V, ya[i], yb[i]);
+        } else {
+          const E* x = static_cast<const E*>(S.x) + run.tok * S.ldx + H.col;
+          load_unit<E, V, kPairs>(x + o1[i], x + o2[i], a[i], b[i]);
+          if (kBwd) {
+            const E* y = static_cast<const E*>(S.dy) + run.tok * S.lddy + H.col;
+            load_unit<E, V, kPairs>(y + o1[i], y + o2[i], ya[i], yb[i]);
           }
-          store_unit<E, V, kPairs>(out, o1[n], o2[n], oa, ob);
+        }
+      }
+      ss += dot_v<V>(a[i], a[i], b[i], b[i]);
+      if (kBwd) {  // w = dy rotated back; the sum of w g x
+        float t[V], wa[V], wb[V], sa[V], sb[V];
+        mul_v<V>(yb[i], c4[i], t);
+        fma_v<V>(ya[i], c3[i], t, wa);
+        scale_v<V>(ya[i], -1.0f, t);
+        mul_v<V>(t, c4[i], t);
+        fma_v<V>(yb[i], c3[i], t, wb);
+        mul_v<V>(wa, c1[i], sa);
+        mul_v<V>(wb, c2[i], sb);
+        sx += dot_v<V>(sa, a[i], sb, b[i]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          ya[i][k] = wa[k];
+          yb[i][k] = wb[k];
         }
       }
     }
+    float r = 1.0f;
+    if (p.norm) {
+      ss = group_sum(ss, n, li, leader);
+      if (kBwd) sx = group_sum(sx, n, li, leader);
+      r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    }
+    E* out = static_cast<E*>(S.out) + run.tok * S.ldo + H.col;
+    const float m = kBwd && p.norm ? -(r * (sx * inv_d)) : 0.0f;  // - mean(s n)
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float oa[V], ob[V], t[V];
+      if (!kBwd) {
+        mul_v<V>(b[i], c2[i], t);
+#pragma unroll
+        for (int k = 0; k < V; ++k) t[k] = -t[k];
+        fma_v<V>(a[i], c1[i], t, oa);
+        mul_v<V>(a[i], c4[i], t);
+        fma_v<V>(b[i], c3[i], t, ob);
+        scale_v<V>(oa, r, oa);
+        scale_v<V>(ob, r, ob);
+      } else {
+        float sa[V], sb[V], mm[V];
+        scale_v<V>(a[i], r, a[i]);  // n = x r
+        scale_v<V>(b[i], r, b[i]);
+        fma_v<V>(ya[i], a[i], dga[i], dga[i]);
+        fma_v<V>(yb[i], b[i], dgb[i], dgb[i]);
+        mul_v<V>(ya[i], c1[i], sa);
+        mul_v<V>(yb[i], c2[i], sb);
+#pragma unroll
+        for (int k = 0; k < V; ++k) mm[k] = m;
+        fma_v<V>(a[i], mm, sa, oa);
+        fma_v<V>(b[i], mm, sb, ob);
+        scale_v<V>(oa, r, oa);
+        scale_v<V>(ob, r, ob);
+      }
+      if (ok && on[i]) store_unit<E, V, kPairs>(out, o1[i], o2[i], oa, ob);
+    }
+    slot = (slot + 1) % kStages;
+    cursor_next(run, p, first, step, heads, rows);
+  }
+  copy_wait<0>();
+  if (!kBwd || !p.partial) return;
+
+  // This CTA's sum of the gain's gradient: over the groups of a warp, then the
+  // warps, in a fixed order (the tables' memory is reused).
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);  // [warp][group][D]
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    if (!on[i]) continue;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int ea = kPairs ? o1[i] + 2 * k : o1[i] + k, eb = kPairs ? o1[i] + 2 * k + 1 : o2[i] + k;
+      sums[(warp * G + grp) * p.D + ea] = dga[i][k];
+      sums[(warp * G + grp) * p.D + eb] = dgb[i][k];
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.D; e += kThreads) {
+    float s = 0.0f;
+    for (int i = 0; i < kWarps * G; ++i) s += sums[i * p.D + e];
+    p.partial[static_cast<int64_t>(blockIdx.x) * p.D + e] = s;
   }
 }
 
-// dV into the value columns of dQKV: 16 bytes a lane.
+// dV into the value columns of dQKV: 16 bytes a lane and step, kFlight steps
+// (of one token after another) in flight.
 template <typename E>
 __device__ __forceinline__ void copy_values(const QkParams& p, int w, int nw) {
   constexpr int V = 16 / sizeof(E);
-  const int lane = threadIdx.x & 31;
-  for (int64_t tok = w; tok < p.T; tok += nw) {
-    for (int s = 0; s < p.t; ++s) {
+  constexpr int kFlight = 8;
+  const int chunks = static_cast<int>(p.values / V);  // of a token, over all shards
+  int64_t tok = w;
+  int c = threadIdx.x & 31;       // this lane's chunk of the token,
+  int s = 0, c0 = 0;              // its shard, and that shard's first chunk
+  while (c >= chunks && tok < p.T) {
+    c -= chunks;
+    tok += nw;
+  }
+  while (tok < p.T) {
+    uint4 q[kFlight];
+    uint4* dst[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      dst[u] = nullptr;
+      if (tok >= p.T) continue;
+      while (c - c0 >= p.shards[s].dkv / V) c0 += p.shards[s++].dkv / V;
       const QkShard& S = p.shards[s];
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const E*>(S.dv) + tok * S.dkv);
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<E*>(S.out) + tok * S.ldo + S.vcol);
-      for (int c = lane; c < S.dkv / V; c += 32) dst[c] = src[c];
+      q[u] = reinterpret_cast<const uint4*>(static_cast<const E*>(S.dv) + tok * S.dkv)[c - c0];
+      dst[u] = reinterpret_cast<uint4*>(static_cast<E*>(S.out) + tok * S.ldo + S.vcol) + (c - c0);
+      c += 32;
+      while (c >= chunks && tok < p.T) {
+        c -= chunks;
+        tok += nw;
+        s = c0 = 0;
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (dst[u]) *dst[u] = q[u];
   }
 }
 
 template <typename E, int V, int NU, bool kPairs, bool kBwd>
 __device__ __forceinline__ void qk_body(const QkParams& p) {
+  extern __shared__ __align__(16) uint8_t qk_smem[];
   const int cta = blockIdx.x, warp = threadIdx.x >> 5;
   const int kind = cta < p.cta_end[0] ? 0 : cta < p.cta_end[1] ? 1 : 2;
   const int c0 = kind ? p.cta_end[kind - 1] : 0;
@@ -313,57 +608,16 @@ __device__ __forceinline__ void qk_body(const QkParams& p) {
     if (kBwd) copy_values<E>(p, w, nw);
     return;
   }
-  float dga[NU][V], dgb[NU][V];
-#pragma unroll
-  for (int n = 0; n < NU; ++n)
-#pragma unroll
-    for (int k = 0; k < V; ++k) dga[n][k] = dgb[n][k] = 0.0f;
-  qk_walk<E, V, NU, kPairs, kBwd>(p, kind, w, nw, dga, dgb);
-  if (!kBwd || !p.partial) return;
-
-  // This CTA's sum of the gain's gradient: over the groups of a warp by
-  // shuffles, over the warps in shared memory, in a fixed order.
-  __shared__ float sums[kWarps][kMaxHeadDim];
-  const int lane = threadIdx.x & 31, L = p.lanes;
-#pragma unroll
-  for (int n = 0; n < NU; ++n)
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      for (int o = L; o < 32; o <<= 1) {
-        dga[n][k] += __shfl_xor_sync(0xffffffffu, dga[n][k], o);
-        dgb[n][k] += __shfl_xor_sync(0xffffffffu, dgb[n][k], o);
-      }
-  if (lane < L) {
-#pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      const int u = lane + n * L;
-      if (u >= p.D / (2 * V)) continue;
-      int o1, o2, j0;
-      unit_at<V, kPairs>(u, p.R, o1, o2, j0);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int ea = kPairs ? o1 + 2 * k : o1 + k, eb = kPairs ? o1 + 2 * k + 1 : o2 + k;
-        sums[warp][ea] = dga[n][k];
-        sums[warp][eb] = dgb[n][k];
-      }
-    }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.D; e += kThreads) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += sums[i][e];
-    p.partial[static_cast<int64_t>(cta) * p.D + e] = s;
-  }
+  qk_kind<E, V, NU, kPairs, kBwd>(p, kind, w, nw, qk_smem);
 }
 
 template <typename E, int V, int NU, bool kPairs>
-__global__ void __launch_bounds__(kThreads) tpmlp_attn_qk_norm_rope_fwd(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tpmlp_attn_qk_norm_rope_fwd(const __grid_constant__ QkParams p) {
   qk_body<E, V, NU, kPairs, false>(p);
 }
 
 template <typename E, int V, int NU, bool kPairs>
-__global__ void __launch_bounds__(kThreads) tpmlp_attn_qk_norm_rope_bwd(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tpmlp_attn_qk_norm_rope_bwd(const __grid_constant__ QkParams p) {
   qk_body<E, V, NU, kPairs, true>(p);
 }
 
@@ -408,6 +662,9 @@ int vector_width(bool bf16, int D, int R, bool pairs) {
   return 1;
 }
 
+// Bytes of a warp's queue.
+int queue_of(bool bf16, int V, bool bwd) { return V > 1 ? kStages * (bwd ? 4 : 2) * 32 * V * (bf16 ? 2 : 4) : 0; }
+
 QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
   if (bf16) {
     if (V == 8) return pick<__nv_bfloat16, 8, 1>(pairs, bwd);
@@ -425,53 +682,57 @@ cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, in
   if (p.T <= 0) return cudaSuccess;
   const int V = vector_width(bf16, p.D, p.R, pairs);
   const int units = p.D / (2 * V);
-  int L = 1;
-  while (L < units && L < 32) L *= 2;
-  p.lanes = L;
-  const int G = 32 / L;
+  p.lanes = std::min(units, 32);
+  p.groups = 32 / p.lanes;
+  const int G = p.groups;
   const QkKernel k = kernel_for(bf16, V, pairs, bwd);
-  static std::atomic<int> resident[2][9][2][2];  // CTAs per SM of each kernel, once known
-  std::atomic<int>& known = resident[bf16][V][pairs][bwd];
+  int bytes = place(std::max(p.heads[0], p.heads[1]), p.D, queue_of(bf16, V, bwd)).total;
+  if (bwd) bytes = std::max(bytes, kWarps * G * p.D * 4);  // the sums of the gain's gradient
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e != cudaSuccess) return e;
+  // CTAs that an SM holds: by registers (asked once per kernel) and by shared memory.
+  static std::atomic<int> by_registers[2][9][2][2];
+  std::atomic<int>& known = by_registers[bf16][V][pairs][bwd];
   int per_sm = known.load(std::memory_order_relaxed);
   if (per_sm == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, kThreads, 0);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, kThreads, 0);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     known.store(per_sm, std::memory_order_relaxed);
   }
+  per_sm = std::max(1, std::min(per_sm, kSmemPerSm / (bytes + 1024)));
   const int slots = sms * per_sm;
   const int64_t most_warps = int64_t{slots} * kWarps;
 
   // Heads of a token in parts, so that a launch of few tokens still has a
   // warp for every slot: a part is a whole number of rounds of G heads.
-  int rounds[2], most_rounds = 1;
+  int rounds[2];
+  for (int kind = 0; kind < 2; ++kind) rounds[kind] = (p.heads[kind] + G - 1) / G;
+  auto parts_of = [&](int kind, int per_part) { return (rounds[kind] + per_part - 1) / per_part; };
+  int per_part = std::max(rounds[0], rounds[1]);
+  while (per_part > 1 && p.T * (parts_of(0, per_part) + parts_of(1, per_part)) < most_warps) per_part = (per_part + 1) / 2;
+  // CTAs of each kind in proportion to its work, in rounds: a token's angles
+  // count as one more.
+  double work[3], total = 0;
+  int64_t want[3];
   for (int kind = 0; kind < 2; ++kind) {
-    rounds[kind] = (p.heads[kind] + G - 1) / G;
-    most_rounds = rounds[kind] > most_rounds ? rounds[kind] : most_rounds;
-  }
-  int per_part = most_rounds;
-  while (per_part > 1 && p.T * ((rounds[0] + per_part - 1) / per_part + (rounds[1] + per_part - 1) / per_part) < most_warps)
-    per_part = (per_part + 1) / 2;
-  // CTAs of each kind in proportion to its bytes.
-  int64_t cost[3], total = 0, want[3];
-  for (int kind = 0; kind < 2; ++kind) {
-    p.parts[kind] = (rounds[kind] + per_part - 1) / per_part;
-    cost[kind] = static_cast<int64_t>(p.heads[kind]) * p.D * (bwd ? 3 : 2);
+    p.parts[kind] = parts_of(kind, per_part);
+    work[kind] = rounds[kind] + p.parts[kind];
     want[kind] = (p.T * p.parts[kind] + kWarps - 1) / kWarps;
   }
-  cost[2] = bwd && p.values ? p.values * 2 : 0;
-  want[2] = cost[2] ? (p.T + kWarps - 1) / kWarps : 0;
-  for (int kind = 0; kind < 3; ++kind) total += cost[kind];
+  work[2] = bwd ? 2.0 / 3.0 * static_cast<double>(p.values) / (G * p.D) : 0.0;
+  want[2] = work[2] > 0 ? (p.T + kWarps - 1) / kWarps : 0;
+  for (double v : work) total += v;
   int end = 0;
   for (int kind = 0; kind < 3; ++kind) {
-    int64_t n = (cost[kind] * slots + total - 1) / total;
-    if (n > want[kind]) n = want[kind];
-    if (kind < 2) n = std::max<int64_t>(n, (p.parts[kind] + kWarps - 1) / kWarps);  // a warp for every part
-    end += static_cast<int>(n);
+    int64_t c = static_cast<int64_t>(work[kind] / total * slots + 0.999);
+    c = std::min(c, want[kind]);
+    if (kind < 2) c = std::max<int64_t>(c, (p.parts[kind] + kWarps - 1) / kWarps);  // a warp for every part
+    end += static_cast<int>(c);
     p.cta_end[kind] = end;
   }
   if (end > kQkMaxCtas) return cudaErrorInvalidConfiguration;  // parts < 2 x the slots' warps: not reached
-  k<<<end, kThreads, 0, stream>>>(p);
+  k<<<end, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -1719,6 +1719,13 @@ tpmlp_status tpmlp_attn_plan_set_qk_norm_rope(tpmlp_plan* plan, const tpmlp_qk_d
     if (plan->dq_i[i] % D || plan->dkv_i[i] % D)
       return fail(TPMLP_ERR_SHAPE, "shard %d: dq_i = %lld and dkv_i = %lld must be multiples of head_dim = %d", i,
                   static_cast<long long>(plan->dq_i[i]), static_cast<long long>(plan->dkv_i[i]), D);
+  for (const std::vector<int64_t>* w : {&plan->dq_i, &plan->dkv_i}) {
+    int64_t heads = 0;
+    for (int64_t v : *w) heads += v / D;
+    if (heads > kMaxHeads)
+      return fail(TPMLP_ERR_UNSUPPORTED, "%lld query or key heads over all shards: at most %d",
+                  static_cast<long long>(heads), kMaxHeads);
+  }
   if (desc->norm && !(desc->eps > 0.0f && std::isfinite(desc->eps)))
     return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive number", static_cast<double>(desc->eps));
   if (R && !desc->inv_freq && !(desc->base > 0.0 && std::isfinite(desc->base)))

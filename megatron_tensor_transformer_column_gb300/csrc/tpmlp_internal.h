@@ -278,6 +278,7 @@ cudaError_t launch_colsum(const ColsumParams& p, bool bf16, ColsumShape shape, c
 // Norm of the query and key heads with the position rotation
 // (qk_norm_rope.cu).  Kind 0: queries, 1: keys, 2: the copy of dV.
 constexpr int kMaxHeadDim = 256;
+constexpr int kMaxHeads = 4096;    // of a kind, over all shards
 constexpr int kQkMaxCtas = 4096;  // bound of a launch's CTAs: rows of its partial gain gradients
 struct QkShard {
   const void* x;   // [T x ldx]: q | k | v before the norm
@@ -298,7 +299,8 @@ struct QkParams {
   int64_t T, values;                  // tokens; value columns to copy
   int32_t t, D, R, norm;
   float eps;
-  int32_t lanes, heads[2], parts[2], cta_end[3];  // set by the launcher, but heads
+  int32_t heads[2];
+  int32_t lanes, groups, parts[2], cta_end[3];  // set by the launcher
 };
 cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, int sms, cudaStream_t stream);
 cudaError_t launch_qk_gain_grad(const QkParams& p, bool bf16, void* dgq, void* dgk, cudaStream_t stream);
