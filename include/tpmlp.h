@@ -344,7 +344,8 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * tpmlp_attn_plan_set_qk_norm_rope describes the heads (copied into the plan,
  * inv_freq included; may not run while another call uses the plan).  Every
  * dq_i and dkv_i must be a multiple of head_dim, an even number up to 256, with
- * at most 4096 query heads and 4096 key heads over all shards; rotary_dim is even, 0 (norm only) to head_dim.  With an fp32 plan and
+ * at most 1024 query heads and 1024 key heads over all shards; rotary_dim is
+ * even, 0 (norm only) to head_dim.  With an fp32 plan and
  * norm = 1 tpmlp_workspace_size grows: query it after this call.  Errors:
  * TPMLP_ERR_INVALID_ARG (NULL, an MLP plan, unknown layout, norm not 0 or 1,
  * eps, base or inv_freq not usable), TPMLP_ERR_SHAPE, TPMLP_ERR_UNSUPPORTED

@@ -549,6 +549,11 @@ def _ptrs(name: str, xs, shapes, dtype, device):
     return (ctypes.c_void_p * len(shapes))(*[_ptr(name, x, s, dtype, device) for x, s in zip(xs, shapes)])
 
 
+def _addresses(xs):
+    """The addresses of tensors that were made here."""
+    return (ctypes.c_void_p * len(xs))(*[x.data_ptr() for x in xs])
+
+
 def _on(device, stream):
     """A context with the call's device and stream as the current ones, so that what the call allocates belongs to
     that stream.  stream: None (the device's current one), a torch stream or a raw handle (0: the default stream)."""
@@ -719,11 +724,15 @@ class ShardedMLP:
         sizes = self.ckpt8_sizes()
         with _on(dev, stream):
             if out is None:
-                out = X.new_empty((p.T, p.d)), [torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes]
-            Y, ckpt = out
+                Y = X.new_empty((p.T, p.d))
+                ckpt = [X.new_empty(n, dtype=torch.uint8) for n in sizes]
+                y, c = Y.data_ptr(), _addresses(ckpt)
+            else:
+                Y, ckpt = out
+                y = _ptr("Y", Y, (p.T, p.d), td, dev)
+                c = _ptrs("ckpt", ckpt, [(n,) for n in sizes], torch.uint8, dev)
             scratch, H = _pieces([p.T * w * X.element_size() for w in p.d_i], dev)
-            tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, _ptr("Y", Y, (p.T, p.d), td, dev),
-                                _ptrs("ckpt", ckpt, [(n,) for n in sizes], torch.uint8, dev), H, self.workspace)
+            tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, y, c, H, self.workspace.data_ptr())
         return Y, ckpt
 
     def backward_ckpt8(self, X, W1_i, W2_i, ckpt, dY, W3_i=None, stream=None, bias_grads=False, out=None):
@@ -737,16 +746,22 @@ class ShardedMLP:
         es = X.element_size()
         with _on(dev, stream):
             if out is None:
-                out = (X.new_empty((p.T, p.d)), [X.new_empty(s) for s in col],
-                       [X.new_empty(s) for s in col] if self.swiglu else None, [X.new_empty(s) for s in row])
-            dX, dW1, dW3, dW2 = out
-            db1, db3, db2 = self.alloc_bias_grads() if bias_grads else (None, None, None)
+                dX, dW1, dW2 = X.new_empty((p.T, p.d)), [X.new_empty(s) for s in col], [X.new_empty(s) for s in row]
+                dW3 = [X.new_empty(s) for s in col] if self.swiglu else None
+                to = dX.data_ptr(), _addresses(dW1), _addresses(dW3) if self.swiglu else None, _addresses(dW2)
+            else:
+                dX, dW1, dW3, dW2 = out
+                to = (_ptr("dX", dX, (p.T, p.d), td, dev), _ptrs("dW1", dW1, col, td, dev),
+                      _ptrs("dW3", dW3, col, td, dev) if self.swiglu else None, _ptrs("dW2", dW2, row, td, dev))
+            db1 = db3 = db2 = None
+            db = (None, None, None)
+            if bias_grads:
+                db1, db2 = [X.new_empty(w) for w in p.d_i], X.new_empty(p.d)
+                db3 = [X.new_empty(w) for w in p.d_i] if self.swiglu else None
+                db = _addresses(db1), _addresses(db3) if self.swiglu else None, db2.data_ptr()
             wide = [p.T * w * es for w in p.d_i]
             scratch, at = _pieces(wide * (3 if self.swiglu else 2), dev)  # H_i, then dact
-            tpmlp_backward_ckpt8(p, x, w1, w3, w2, c, at[:p.t], dy, at[p.t:], _ptr("dX", dX, (p.T, p.d), td, dev),
-                                 _ptrs("dW1", dW1, col, td, dev),
-                                 _ptrs("dW3", dW3, col, td, dev) if self.swiglu else None,
-                                 _ptrs("dW2", dW2, row, td, dev), db1, db3, db2, self.workspace)
+            tpmlp_backward_ckpt8(p, x, w1, w3, w2, c, at[:p.t], dy, at[p.t:], *to, *db, self.workspace.data_ptr())
         return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "db1": db1, "db3": db3, "db2": db2}
 
     def check(self, stream=None):
@@ -859,7 +874,10 @@ class ShardedAttentionProj:
         with _on(self.workspace.device, stream):
             if out is None:
                 out = [x.new_empty((p.T, q_ + k_)) for x, q_, k_ in zip(QKV_i, p.dq_i, p.dkv_i)]
-            tpmlp_attn_qk_norm_rope_forward(p, qkv, pos, q, k, self._in_place_or_dense("out", out, qkv))
+                to = _addresses(out)
+            else:
+                to = self._in_place_or_dense("out", out, qkv)
+            tpmlp_attn_qk_norm_rope_forward(p, qkv, pos, q, k, to)
         return out
 
     def qk_norm_rope_backward(self, QKV_i, dQK_i, positions=None, gq=None, gk=None, dV_i=None, out=None, stream=None,
@@ -877,7 +895,9 @@ class ShardedAttentionProj:
         with _on(dev, stream):
             if out is None:
                 out = [x.new_empty(x.shape) for x in QKV_i]
-            dqkv = _ptrs("out", out, [(p.T, n) for n in p.d_i], td, dev)
+                dqkv = _addresses(out)
+            else:
+                dqkv = _ptrs("out", out, [(p.T, n) for n in p.d_i], td, dev)
             dgq, dgk = (self._empty(p.head_dim), self._empty(p.head_dim)) if gain_grads else (None, None)
             tpmlp_attn_qk_norm_rope_backward(p, qkv, pos, q, k, self._in_place_or_dense("dQK_i", dQK_i, dqkv), dv,
                                              dqkv, dgq, dgk, self.workspace)

@@ -30,7 +30,23 @@
 // without registers.  CTAs belong to one kind, so that the gains (and,
 // backward, the lane's sums of the gain's gradient) stay with the CTA for the
 // whole launch; the host deals the CTAs to the kinds by their work.  With few
-// tokens the heads of a token are split over several warps.
+// tokens the heads of a token are split over several warps.  Every CTA first
+// copies its share of dV, eight 16-byte accesses of a lane in flight (CTAs of
+// their own for it were the last to finish: 228 against 160 us on 8192 tokens
+// of 8 shards of 16 + 1 heads of 128).
+//
+// Measured on GB300, bf16, device time and share of the copy bandwidth:
+//   16384 tokens, 8 shards of 4 + 4 heads of 96:   68 us (0.87), backward 141 us (0.84)
+//   8192 tokens, 8 shards of 16 + 1 heads of 128: 102 us (0.82), backward 158 us (0.83)
+// A first version with the loads in registers and every lane computing its own
+// angles took 147 and 359 us on the former: it was bound by instruction issue
+// (250 instructions a round forward) and latency.  What bounds it now is issue
+// and the latency of a round's chain (load, sum, root, store) together: 60 % of
+// the issue slots taken with 16 warps an SM, which is what the registers allow.
+// Two heads a lane and round (4 % less time on the former shape, 1 to 30 %
+// more on small and 64-wide ones) and queues of four or six rounds (no gain)
+// were measured and not kept; a queue of two helps the latter shape (94 us) and
+// costs the former 11 %.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,7 +60,7 @@
 namespace tpmlp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSmem = 227 * 1024;    // dynamic shared memory of a CTA
 constexpr int kSmemPerSm = 228 * 1024;  // of an SM, 1 KB of it taken by each CTA
@@ -108,7 +124,7 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[V]) {
   }
 }
 
-constexpr int kStages = 4;  // rounds of a lane's queue: one being worked on, three on their way
+constexpr int kStages = 3;  // rounds of a lane's queue: one being worked on, two on their way
 
 // Element-wise operations on V floats, two at a time where V is even.
 template <int V>
@@ -228,42 +244,82 @@ __device__ __forceinline__ void store_unit(E* row, int o1, int o2, const float (
   store_vec<E, V>(row + o2, v2);
 }
 
-// Where unit u of a head lies; its pairs are V u .. V u + V - 1, those from
-// R / 2 on being no pairs but elements that are not rotated.  Halves: the units
-// of the rotated part, then the rest cut into neighbouring vectors.
+// Where unit u of a head lies: two vectors far apart, so that the vectors that
+// neighbouring lanes read at once are neighbours too (two next to each other
+// made every 32-byte sector travel twice: 127 against 105 us on 8192 tokens
+// of 136 heads of 128, neighbouring pairs).  Halves: the units of the rotated part, then those of
+// the rest; pairs: the vectors of the head's two halves (whole pairs, V even).
 template <int V, bool kPairs>
-__device__ __forceinline__ void unit_at(int u, int R, int& o1, int& o2) {
-  const int ru = kPairs ? 0 : R / (2 * V);
+__device__ __forceinline__ void unit_at(int u, int D, int R, int& o1, int& o2) {
+  if (kPairs) {
+    o1 = V > 1 ? V * u : 2 * u;
+    o2 = V > 1 ? D / 2 + V * u : 2 * u + 1;
+    return;
+  }
+  const int ru = R / (2 * V);
   if (u < ru) {
     o1 = V * u;
     o2 = R / 2 + V * u;
   } else {
-    o1 = (kPairs ? 0 : R) + 2 * V * (u - ru);
-    o2 = o1 + V;
+    o1 = R + V * (u - ru);
+    o2 = R + (D - R) / 2 + V * (u - ru);
   }
 }
 
-// The sum over the n lanes of a group, to all of them (the same bits).
-__device__ __forceinline__ float group_sum(float s, int n, int li, int leader) {
+// A unit's V entries of a per-pair table (an entry per pair; past R / 2 pairs
+// that are not rotated, whichever two elements those are).
+template <int V, bool kPairs>
+__device__ __forceinline__ void read_pairs(const float* table, int u, int D, float (&o)[V]) {
+  if constexpr (kPairs && V > 1) {
+    float lo[V / 2], hi[V / 2];
+    read_v<V / 2>(table + V / 2 * u, lo);
+    read_v<V / 2>(table + D / 4 + V / 2 * u, hi);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      o[k] = lo[k];
+      o[V / 2 + k] = hi[k];
+    }
+  } else {
+    read_v<V>(table + V * u, o);
+  }
+}
+
+// The sums of s (and t) over the n lanes of a group, to all of them (the same
+// bits): a tree to the group's first lane and back for an n that is no power of
+// two.  n is the same for the whole warp.
+template <bool kTwo>
+__device__ __forceinline__ void group_sum(float& s, float& t, int n, int li, int leader) {
   if ((n & (n - 1)) == 0) {
-    for (int o = n >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= n) continue;
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (kTwo) t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    return;
   }
-  int o = 16;
-  while (o >= n) o >>= 1;
-  for (; o > 0; o >>= 1) {
-    const float t = __shfl_down_sync(0xffffffffu, s, o);
-    if (li + o < n) s += t;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o >= n) continue;
+    const float us = __shfl_down_sync(0xffffffffu, s, o);
+    const float ut = kTwo ? __shfl_down_sync(0xffffffffu, t, o) : 0.0f;
+    if (li + o < n) {
+      s += us;
+      t += ut;
+    }
   }
-  return __shfl_sync(0xffffffffu, s, leader);
+  s = __shfl_sync(0xffffffffu, s, leader);
+  if (kTwo) t = __shfl_sync(0xffffffffu, t, leader);
 }
 
+// B bytes to shared memory, or zeros (src is not read then).
 template <int B>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? B : 0;
   if constexpr (B == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -274,20 +330,39 @@ __device__ __forceinline__ void copy_wait() {
 // Shared memory of a CTA (bytes from the start of the dynamic part): the
 // kind's heads, the frequencies, the gains by unit, each warp's cosines and
 // sines, each warp's queue.
-struct Head {
-  int32_t shard, col;
+// At most kMaxHeads heads of at most kMaxHeadDim elements a kind: a row is
+// below 2^22 bytes, a token's offset one 32-bit product.
+template <bool kBwd>
+struct Head {  // of token 0, and the row strides in bytes
+  const char* x;
+  char* out;
+  uint32_t ldx, ldo;
+  uint64_t pad;
 };
+template <>
+struct Head<true> {
+  const char* x;
+  char* out;
+  const char* dy;
+  uint32_t ldx, ldo, lddy, pad[3];
+};
+template <typename P>
+__device__ __forceinline__ P row_of(P base, uint32_t tok, uint32_t ld) {
+  return base + static_cast<uint64_t>(tok) * ld;
+}
 template <int V>
 constexpr bool kQueue = V > 1;  // single elements are loaded when they are needed
-template <typename E, int V, bool kBwd>
-constexpr int queue_bytes() { return kQueue<V> ? kStages * (kBwd ? 4 : 2) * 32 * V * int(sizeof(E)) : 0; }
+// Bytes of a warp's queue.
+__host__ __device__ constexpr int queue_bytes(int V, int elem, bool bwd) {
+  return V > 1 ? kStages * (bwd ? 4 : 2) * 32 * V * elem : 0;
+}
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 struct Place {
   int freq, gain, angle, queue, total;
 };
-__host__ __device__ inline Place place(int heads, int D, int queue) {
+__host__ __device__ inline Place place(int heads, int D, int queue, bool bwd) {
   Place p;
-  p.freq = round16(heads * int(sizeof(Head)));
+  p.freq = heads * int(bwd ? sizeof(Head<true>) : sizeof(Head<false>));
   p.gain = p.freq + round16(D / 2 * 8);
   p.angle = p.gain + round16(D * 4);
   p.queue = p.angle + kWarps * round16(D * 4);
@@ -297,10 +372,10 @@ __host__ __device__ inline Place place(int heads, int D, int queue) {
 
 // A position in a warp's sequence of (token, round).
 struct Cursor {
-  int64_t tok;
+  uint32_t tok;
   int h0;
 };
-__device__ __forceinline__ void cursor_next(Cursor& c, const QkParams& p, int first, int step, int heads, int rows) {
+__device__ __forceinline__ void cursor_next(Cursor& c, int first, int step, int heads, uint32_t rows) {
   c.h0 += step;
   if (c.h0 >= heads) {
     c.h0 = first;
@@ -311,13 +386,16 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const QkParams& p, int fi
 template <typename E, int V, int NU, bool kPairs, bool kBwd>
 __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int nw, uint8_t* smem) {
   constexpr int kVecBytes = V * int(sizeof(E));
+  constexpr int kQueueBytes = queue_bytes(V, sizeof(E), kBwd);
+  constexpr int kHeadVecs = kBwd ? 4 : 2;  // a head's vectors in the queue
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = p.lanes, G = p.groups;  // lanes of a head, heads of a round
   const int grp = lane / n, li = lane - grp * n, leader = grp * n;
   const int units = p.D / (2 * V), heads = p.heads[kind], parts = p.parts[kind];
   const float inv_d = 1.0f / static_cast<float>(p.D);
-  const Place at = place(max(p.heads[0], p.heads[1]), p.D, queue_bytes<E, V, kBwd>());
-  Head* head = reinterpret_cast<Head*>(smem);
+  const uint32_t T = static_cast<uint32_t>(p.T);
+  const Place at = place(max(p.heads[0], p.heads[1]), p.D, kQueueBytes, kBwd);
+  Head<kBwd>* head = reinterpret_cast<Head<kBwd>*>(smem);
   uint64_t* freq = reinterpret_cast<uint64_t*>(smem + at.freq);
   float* gains = reinterpret_cast<float*>(smem + at.gain);  // by unit: V a's, V b's
   float* cosines = reinterpret_cast<float*>(smem + at.angle + warp * round16(p.D * 4));
@@ -327,13 +405,24 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
   for (int h = threadIdx.x; h < heads; h += kThreads) {
     int s = 0;
     while (h >= p.head_end[kind][s]) ++s;
-    head[h] = Head{s, p.shards[s].col[kind] + (h - (s ? p.head_end[kind][s - 1] : 0)) * p.D};
+    const QkShard& S = p.shards[s];
+    const int col = S.col[kind] + (h - (s ? p.head_end[kind][s - 1] : 0)) * p.D;
+    Head<kBwd> H;
+    H.x = reinterpret_cast<const char*>(static_cast<const E*>(S.x) + col);
+    H.out = reinterpret_cast<char*>(static_cast<E*>(S.out) + col);
+    H.ldx = static_cast<uint32_t>(S.ldx * sizeof(E));
+    H.ldo = static_cast<uint32_t>(S.ldo * sizeof(E));
+    if constexpr (kBwd) {
+      H.dy = reinterpret_cast<const char*>(static_cast<const E*>(S.dy) + col);
+      H.lddy = static_cast<uint32_t>(S.lddy * sizeof(E));
+    }
+    head[h] = H;
   }
   for (int j = threadIdx.x; j < p.R / 2; j += kThreads) freq[j] = p.freq[j];
   const E* g = static_cast<const E*>(p.gain[kind]);
   for (int u = threadIdx.x; u < units; u += kThreads) {
     int o1, o2;
-    unit_at<V, kPairs>(u, p.R, o1, o2);
+    unit_at<V, kPairs>(u, p.D, p.R, o1, o2);
     float a[V], b[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) a[k] = b[k] = 1.0f;
@@ -357,7 +446,7 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     const int u = li + i * n;
     on[i] = grp < G && u < units;
     un[i] = on[i] ? u : 0;
-    unit_at<V, kPairs>(un[i], p.R, o1[i], o2[i]);
+    unit_at<V, kPairs>(un[i], p.D, p.R, o1[i], o2[i]);
   }
   float dga[NU][V], dgb[NU][V];
 #pragma unroll
@@ -365,33 +454,31 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
 #pragma unroll
     for (int k = 0; k < V; ++k) dga[i][k] = dgb[i][k] = 0.0f;
 
-  const int rows = nw / parts;  // tokens at a time; warps left over have none
+  const uint32_t rows = nw / parts;  // tokens at a time; warps left over have none
   const int first = (w % parts) * G, step = parts * G;
   Cursor get, run;  // what is fetched next, what is worked on next
-  run.tok = w < rows * parts && first < heads ? w / parts : p.T;
+  run.tok = static_cast<uint32_t>(w) < rows * parts && first < heads ? w / parts : T;
   run.h0 = first;
   get = run;
 
   // The queue: slot s holds, per vector and lane, this lane's bytes of a round.
-  const uint32_t queue = ptx::smem_u32(smem + at.queue + warp * queue_bytes<E, V, kBwd>()) + lane * kVecBytes;
+  const uint32_t queue = ptx::smem_u32(smem + at.queue + warp * kQueueBytes) + lane * kVecBytes;
   auto fetch = [&](int slot) {
     if constexpr (kQueue<V>) {
-      if (get.tok < p.T) {
+      if (get.tok < T) {
         const int h = get.h0 + grp;
-        if (on[0] && h < heads) {
-          const Head H = head[h];
-          const QkShard& S = p.shards[H.shard];
-          const uint32_t q = queue + slot * (kBwd ? 4 : 2) * 32 * kVecBytes;
-          const E* x = static_cast<const E*>(S.x) + get.tok * S.ldx + H.col;
-          copy_async<kVecBytes>(q, x + o1[0]);
-          copy_async<kVecBytes>(q + 32 * kVecBytes, x + o2[0]);
-          if (kBwd) {
-            const E* y = static_cast<const E*>(S.dy) + get.tok * S.lddy + H.col;
-            copy_async<kVecBytes>(q + 64 * kVecBytes, y + o1[0]);
-            copy_async<kVecBytes>(q + 96 * kVecBytes, y + o2[0]);
-          }
+        const bool ok = on[0] && h < heads;  // else zeros, which add nothing to any sum
+        const Head<kBwd>& H = head[ok ? h : 0];
+        const uint32_t q = queue + slot * kHeadVecs * 32 * kVecBytes;
+        const E* x = reinterpret_cast<const E*>(row_of(H.x, get.tok, H.ldx));
+        copy_async<kVecBytes>(q, x + o1[0], ok);
+        copy_async<kVecBytes>(q + 32 * kVecBytes, x + o2[0], ok);
+        if constexpr (kBwd) {
+          const E* y = reinterpret_cast<const E*>(row_of(H.dy, get.tok, H.lddy));
+          copy_async<kVecBytes>(q + 64 * kVecBytes, y + o1[0], ok);
+          copy_async<kVecBytes>(q + 96 * kVecBytes, y + o2[0], ok);
         }
-        cursor_next(get, p, first, step, heads, rows);
+        cursor_next(get, first, step, heads, rows);
       }
       copy_commit();  // one group a round, an empty one past the end
     }
@@ -402,8 +489,8 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
   }
   int slot = 0;
   // The position of the next token is fetched a token ahead.
-  auto position = [&](int64_t tok) {
-    return tok < p.T && p.pos ? static_cast<uint64_t>(p.pos[tok]) : static_cast<uint64_t>(tok);
+  auto position = [&](uint32_t tok) {
+    return tok < T && p.pos ? static_cast<uint64_t>(p.pos[tok]) : static_cast<uint64_t>(tok);
   };
   uint64_t pos = position(run.tok);
 
@@ -418,7 +505,114 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     for (int k = 0; k < V; ++k) c3[i][k] = c4[i][k] = 0.0f;
   }
 
-  while (run.tok < p.T) {
+  // Vector 0 of a round in the queue.
+  auto queued = [&](int slot) {
+    return reinterpret_cast<const E*>(smem + at.queue + warp * kQueueBytes + slot * kHeadVecs * 32 * kVecBytes +
+                                      lane * kVecBytes);
+  };
+
+  auto forward_head = [&](const Cursor& run, int slot) {
+    const int h = run.h0 + grp;
+    const bool ok = grp < G && h < heads;
+    const Head<kBwd>& H = head[ok ? h : 0];
+    float a[NU][V], b[NU][V], ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      if constexpr (kQueue<V>) {
+        const E* q = queued(slot);
+        load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = 0.0f;
+        if (ok && on[i]) {
+          const E* x = reinterpret_cast<const E*>(row_of(H.x, run.tok, H.ldx));
+          load_unit<E, V, kPairs>(x + o1[i], x + o2[i], a[i], b[i]);
+        }
+      }
+      ss += dot_v<V>(a[i], a[i], b[i], b[i]);
+    }
+    float r = 1.0f, none = 0.0f;
+    if (p.norm) {
+      group_sum<false>(ss, none, n, li, leader);
+      r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    }
+    E* out = reinterpret_cast<E*>(row_of(H.out, run.tok, H.ldo));
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float oa[V], ob[V], t[V];
+      mul_v<V>(b[i], c2[i], t);
+      fma_v<V>(a[i], c1[i], t, oa);
+      mul_v<V>(a[i], c4[i], t);
+      fma_v<V>(b[i], c3[i], t, ob);
+      scale_v<V>(oa, r, oa);
+      scale_v<V>(ob, r, ob);
+      if (ok && on[i]) store_unit<E, V, kPairs>(out, o1[i], o2[i], oa, ob);
+    }
+  };
+
+  auto backward_head = [&](const Cursor& run, int slot) {
+    const int h = run.h0 + grp;
+    const bool ok = grp < G && h < heads;
+    const Head<kBwd>& H = head[ok ? h : 0];
+    float a[NU][V], b[NU][V], wa[NU][V], wb[NU][V];
+    float ss = 0.0f, sx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float ya[V], yb[V], sa[V], sb[V], t[V];
+      if constexpr (kQueue<V>) {
+        const E* q = queued(slot);
+        load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
+        load_unit<E, V, kPairs>(q + 64 * V, q + 96 * V, ya, yb);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = ya[k] = yb[k] = 0.0f;
+        if constexpr (kBwd) {
+          if (ok && on[i]) {
+            const E* x = reinterpret_cast<const E*>(row_of(H.x, run.tok, H.ldx));
+            load_unit<E, V, kPairs>(x + o1[i], x + o2[i], a[i], b[i]);
+            const E* y = reinterpret_cast<const E*>(row_of(H.dy, run.tok, H.lddy));
+            load_unit<E, V, kPairs>(y + o1[i], y + o2[i], ya, yb);
+          }
+        }
+      }
+      ss += dot_v<V>(a[i], a[i], b[i], b[i]);
+      // w = dy rotated back; the sum of w g x
+      mul_v<V>(yb, c4[i], t);
+      fma_v<V>(ya, c3[i], t, wa[i]);
+      scale_v<V>(ya, -1.0f, t);
+      mul_v<V>(t, c4[i], t);
+      fma_v<V>(yb, c3[i], t, wb[i]);
+      mul_v<V>(wa[i], c1[i], sa);
+      mul_v<V>(wb[i], c2[i], sb);
+      sx += dot_v<V>(sa, a[i], sb, b[i]);
+    }
+    float r = 1.0f, m = 0.0f;
+    if (p.norm) {
+      group_sum<true>(ss, sx, n, li, leader);
+      r = rsqrtf(fmaf(ss, inv_d, p.eps));
+      m = -(r * (sx * inv_d));  // - mean(s n)
+    }
+    E* out = reinterpret_cast<E*>(row_of(H.out, run.tok, H.ldo));
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float oa[V], ob[V], sa[V], sb[V], mm[V];
+      scale_v<V>(a[i], r, a[i]);  // n = x r
+      scale_v<V>(b[i], r, b[i]);
+      fma_v<V>(wa[i], a[i], dga[i], dga[i]);
+      fma_v<V>(wb[i], b[i], dgb[i], dgb[i]);
+      mul_v<V>(wa[i], c1[i], sa);
+      mul_v<V>(wb[i], c2[i], sb);
+#pragma unroll
+      for (int k = 0; k < V; ++k) mm[k] = m;
+      fma_v<V>(a[i], mm, sa, oa);
+      fma_v<V>(b[i], mm, sb, ob);
+      scale_v<V>(oa, r, oa);
+      scale_v<V>(ob, r, ob);
+      if (ok && on[i]) store_unit<E, V, kPairs>(out, o1[i], o2[i], oa, ob);
+    }
+  };
+
+  while (run.tok < T) {
     if (run.h0 == first) {  // a new token
       for (int j = lane; j < p.R / 2; j += 32) {
         const int32_t turn = static_cast<int32_t>((pos * freq[j]) >> 32);  // in 2^-32 turns
@@ -432,16 +626,17 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (kBwd) {
-          read_v<V>(cosines + V * un[i], c3[i]);
-          read_v<V>(sines + V * un[i], c4[i]);
+          read_pairs<V, kPairs>(cosines, un[i], p.D, c3[i]);
+          read_pairs<V, kPairs>(sines, un[i], p.D, c4[i]);
         } else {
           float cs[V], sn[V], ga[V], gb[V];
-          read_v<V>(cosines + V * un[i], cs);
-          read_v<V>(sines + V * un[i], sn);
+          read_pairs<V, kPairs>(cosines, un[i], p.D, cs);
+          read_pairs<V, kPairs>(sines, un[i], p.D, sn);
           read_v<V>(gains + 2 * V * un[i], ga);
           read_v<V>(gains + 2 * V * un[i] + V, gb);
           mul_v<V>(ga, cs, c1[i]);
           mul_v<V>(gb, sn, c2[i]);
+          scale_v<V>(c2[i], -1.0f, c2[i]);
           mul_v<V>(gb, cs, c3[i]);
           mul_v<V>(ga, sn, c4[i]);
         }
@@ -451,88 +646,10 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     fetch((slot + kStages - 1) % kStages);
     copy_wait<kQueue<V> ? kStages - 1 : 0>();
 
-    const int h = run.h0 + grp;
-    const bool ok = grp < G && h < heads;
-    const Head H = head[ok ? h : 0];
-    const QkShard& S = p.shards[H.shard];
-    float a[NU][V], b[NU][V], ya[NU][V], yb[NU][V];
-    float ss = 0.0f, sx = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = ya[i][k] = yb[i][k] = 0.0f;
-      if (ok && on[i]) {
-        if constexpr (kQueue<V>) {
-          const E* q = reinterpret_cast<const E*>(smem + at.queue + warp * queue_bytes<E, V, kBwd>() +
-                                                  slot * (kBwd ? 4 : 2) * 32 * kVecBytes + lane * kVecBytes);
-          load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
-          if (kBwd) load_unit<E, V, kPairs>(q + 64 * V, q + 96 * V, ya[i], yb[i]);
-        } else {
-          const E* x = static_cast<const E*>(S.x) + run.tok * S.ldx + H.col;
-          load_unit<E, V, kPairs>(x + o1[i], x + o2[i], a[i], b[i]);
-          if (kBwd) {
-            const E* y = static_cast<const E*>(S.dy) + run.tok * S.lddy + H.col;
-            load_unit<E, V, kPairs>(y + o1[i], y + o2[i], ya[i], yb[i]);
-          }
-        }
-      }
-      ss += dot_v<V>(a[i], a[i], b[i], b[i]);
-      if (kBwd) {  // w = dy rotated back; the sum of w g x
-        float t[V], wa[V], wb[V], sa[V], sb[V];
-        mul_v<V>(yb[i], c4[i], t);
-        fma_v<V>(ya[i], c3[i], t, wa);
-        scale_v<V>(ya[i], -1.0f, t);
-        mul_v<V>(t, c4[i], t);
-        fma_v<V>(yb[i], c3[i], t, wb);
-        mul_v<V>(wa, c1[i], sa);
-        mul_v<V>(wb, c2[i], sb);
-        sx += dot_v<V>(sa, a[i], sb, b[i]);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          ya[i][k] = wa[k];
-          yb[i][k] = wb[k];
-        }
-      }
-    }
-    float r = 1.0f;
-    if (p.norm) {
-      ss = group_sum(ss, n, li, leader);
-      if (kBwd) sx = group_sum(sx, n, li, leader);
-      r = rsqrtf(fmaf(ss, inv_d, p.eps));
-    }
-    E* out = static_cast<E*>(S.out) + run.tok * S.ldo + H.col;
-    const float m = kBwd && p.norm ? -(r * (sx * inv_d)) : 0.0f;  // - mean(s n)
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      float oa[V], ob[V], t[V];
-      if (!kBwd) {
-        mul_v<V>(b[i], c2[i], t);
-#pragma unroll
-        for (int k = 0; k < V; ++k) t[k] = -t[k];
-        fma_v<V>(a[i], c1[i], t, oa);
-        mul_v<V>(a[i], c4[i], t);
-        fma_v<V>(b[i], c3[i], t, ob);
-        scale_v<V>(oa, r, oa);
-        scale_v<V>(ob, r, ob);
-      } else {
-        float sa[V], sb[V], mm[V];
-        scale_v<V>(a[i], r, a[i]);  // n = x r
-        scale_v<V>(b[i], r, b[i]);
-        fma_v<V>(ya[i], a[i], dga[i], dga[i]);
-        fma_v<V>(yb[i], b[i], dgb[i], dgb[i]);
-        mul_v<V>(ya[i], c1[i], sa);
-        mul_v<V>(yb[i], c2[i], sb);
-#pragma unroll
-        for (int k = 0; k < V; ++k) mm[k] = m;
-        fma_v<V>(a[i], mm, sa, oa);
-        fma_v<V>(b[i], mm, sb, ob);
-        scale_v<V>(oa, r, oa);
-        scale_v<V>(ob, r, ob);
-      }
-      if (ok && on[i]) store_unit<E, V, kPairs>(out, o1[i], o2[i], oa, ob);
-    }
+    if constexpr (kBwd) backward_head(run, slot);
+    else forward_head(run, slot);
     slot = (slot + 1) % kStages;
-    cursor_next(run, p, first, step, heads, rows);
+    cursor_next(run, first, step, heads, rows);
   }
   copy_wait<0>();
   if (!kBwd || !p.partial) return;
@@ -546,7 +663,11 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     if (!on[i]) continue;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int ea = kPairs ? o1[i] + 2 * k : o1[i] + k, eb = kPairs ? o1[i] + 2 * k + 1 : o2[i] + k;
+      int ea = o1[i] + k, eb = o2[i] + k;
+      if (kPairs && V > 1) {
+        ea = 2 * k < V ? o1[i] + 2 * k : o2[i] + 2 * k - V;
+        eb = ea + 1;
+      }
       sums[(warp * G + grp) * p.D + ea] = dga[i][k];
       sums[(warp * G + grp) * p.D + eb] = dgb[i][k];
     }
@@ -601,23 +722,19 @@ template <typename E, int V, int NU, bool kPairs, bool kBwd>
 __device__ __forceinline__ void qk_body(const QkParams& p) {
   extern __shared__ __align__(16) uint8_t qk_smem[];
   const int cta = blockIdx.x, warp = threadIdx.x >> 5;
-  const int kind = cta < p.cta_end[0] ? 0 : cta < p.cta_end[1] ? 1 : 2;
-  const int c0 = kind ? p.cta_end[kind - 1] : 0;
-  const int w = (cta - c0) * kWarps + warp, nw = (p.cta_end[kind] - c0) * kWarps;
-  if (kind == 2) {
-    if (kBwd) copy_values<E>(p, w, nw);
-    return;
-  }
-  qk_kind<E, V, NU, kPairs, kBwd>(p, kind, w, nw, qk_smem);
+  if (kBwd && p.values) copy_values<E>(p, cta * kWarps + warp, gridDim.x * kWarps);
+  const int kind = cta < p.cta_end[0] ? 0 : 1;
+  const int c0 = kind ? p.cta_end[0] : 0;
+  qk_kind<E, V, NU, kPairs, kBwd>(p, kind, (cta - c0) * kWarps + warp, (p.cta_end[kind] - c0) * kWarps, qk_smem);
 }
 
 template <typename E, int V, int NU, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 2) tpmlp_attn_qk_norm_rope_fwd(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, 4) tpmlp_attn_qk_norm_rope_fwd(const __grid_constant__ QkParams p) {
   qk_body<E, V, NU, kPairs, false>(p);
 }
 
 template <typename E, int V, int NU, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 2) tpmlp_attn_qk_norm_rope_bwd(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kThreads, 4) tpmlp_attn_qk_norm_rope_bwd(const __grid_constant__ QkParams p) {
   qk_body<E, V, NU, kPairs, true>(p);
 }
 
@@ -662,9 +779,6 @@ int vector_width(bool bf16, int D, int R, bool pairs) {
   return 1;
 }
 
-// Bytes of a warp's queue.
-int queue_of(bool bf16, int V, bool bwd) { return V > 1 ? kStages * (bwd ? 4 : 2) * 32 * V * (bf16 ? 2 : 4) : 0; }
-
 QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
   if (bf16) {
     if (V == 8) return pick<__nv_bfloat16, 8, 1>(pairs, bwd);
@@ -677,6 +791,8 @@ QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
 
 }  // namespace
 
+constexpr double kAngleWork = 1.0;
+
 // Lays the launch out (lanes, parts, CTAs of each kind) and launches it.
 cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, int sms, cudaStream_t stream) {
   if (p.T <= 0) return cudaSuccess;
@@ -686,7 +802,7 @@ cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, in
   p.groups = 32 / p.lanes;
   const int G = p.groups;
   const QkKernel k = kernel_for(bf16, V, pairs, bwd);
-  int bytes = place(std::max(p.heads[0], p.heads[1]), p.D, queue_of(bf16, V, bwd)).total;
+  int bytes = place(std::max(p.heads[0], p.heads[1]), p.D, queue_bytes(V, bf16 ? 2 : 4, bwd), bwd).total;
   if (bwd) bytes = std::max(bytes, kWarps * G * p.D * 4);  // the sums of the gain's gradient
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
@@ -712,22 +828,19 @@ cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, in
   int per_part = std::max(rounds[0], rounds[1]);
   while (per_part > 1 && p.T * (parts_of(0, per_part) + parts_of(1, per_part)) < most_warps) per_part = (per_part + 1) / 2;
   // CTAs of each kind in proportion to its work, in rounds: a token's angles
-  // count as one more.
-  double work[3], total = 0;
-  int64_t want[3];
+  // count as one more.  (Every CTA copies an equal share of dV first.)
+  double work[2];
+  int64_t want[2];
   for (int kind = 0; kind < 2; ++kind) {
     p.parts[kind] = parts_of(kind, per_part);
-    work[kind] = rounds[kind] + p.parts[kind];
+    work[kind] = rounds[kind] + kAngleWork * p.parts[kind];
     want[kind] = (p.T * p.parts[kind] + kWarps - 1) / kWarps;
   }
-  work[2] = bwd ? 2.0 / 3.0 * static_cast<double>(p.values) / (G * p.D) : 0.0;
-  want[2] = work[2] > 0 ? (p.T + kWarps - 1) / kWarps : 0;
-  for (double v : work) total += v;
   int end = 0;
-  for (int kind = 0; kind < 3; ++kind) {
-    int64_t c = static_cast<int64_t>(work[kind] / total * slots + 0.999);
+  for (int kind = 0; kind < 2; ++kind) {
+    int64_t c = static_cast<int64_t>(work[kind] / (work[0] + work[1]) * slots + 0.5);
     c = std::min(c, want[kind]);
-    if (kind < 2) c = std::max<int64_t>(c, (p.parts[kind] + kWarps - 1) / kWarps);  // a warp for every part
+    c = std::max<int64_t>(c, (p.parts[kind] + kWarps - 1) / kWarps);  // a warp for every part
     end += static_cast<int>(c);
     p.cta_end[kind] = end;
   }

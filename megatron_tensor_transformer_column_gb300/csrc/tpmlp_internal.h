@@ -276,9 +276,9 @@ ColsumShape colsum_shape(const ColsumJob* jobs, int num_jobs, bool bf16, int sms
 cudaError_t launch_colsum(const ColsumParams& p, bool bf16, ColsumShape shape, cudaStream_t stream);
 
 // Norm of the query and key heads with the position rotation
-// (qk_norm_rope.cu).  Kind 0: queries, 1: keys, 2: the copy of dV.
+// (qk_norm_rope.cu).  Kind 0: queries, 1: keys.
 constexpr int kMaxHeadDim = 256;
-constexpr int kMaxHeads = 4096;    // of a kind, over all shards
+constexpr int kMaxHeads = 1024;    // of a kind, over all shards
 constexpr int kQkMaxCtas = 4096;  // bound of a launch's CTAs: rows of its partial gain gradients
 struct QkShard {
   const void* x;   // [T x ldx]: q | k | v before the norm
@@ -300,7 +300,7 @@ struct QkParams {
   int32_t t, D, R, norm;
   float eps;
   int32_t heads[2];
-  int32_t lanes, groups, parts[2], cta_end[3];  // set by the launcher
+  int32_t lanes, groups, parts[2], cta_end[2];  // set by the launcher
 };
 cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, int sms, cudaStream_t stream);
 cudaError_t launch_qk_gain_grad(const QkParams& p, bool bf16, void* dgq, void* dgk, cudaStream_t stream);
