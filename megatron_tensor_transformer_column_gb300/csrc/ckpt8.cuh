@@ -24,6 +24,10 @@
 
 #include <stdint.h>
 
+#ifdef __CUDACC__
+#include "act.cuh"
+#endif
+
 namespace tpmlp {
 namespace ck {
 
@@ -64,18 +68,22 @@ __device__ __forceinline__ uint32_t encode2(float x0, float x1) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
   return r;
 }
-// Four codes of x[0..3] * inv; top: scale byte 247 (e = 120), whose codes stop at 240.
-__device__ __forceinline__ uint32_t encode4(const float* x, float inv, bool top) {
-  float v[4];
+constexpr uint32_t kTopScale = 247;  // e = 120, whose codes stop at 240
+// N / 4 words of codes of x[0 .. N - 1] * inv.
+template <int N>
+__device__ __forceinline__ void encode(const float* x, uint32_t byte, uint32_t (&c)[N / 4]) {
+  const uint64_t inv = act::x2::splat(inv_scale(byte));
+  float v[N];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = x[k] * inv;
-  if (top) {
+  for (int k = 0; k < N; k += 2) act::x2::upk(act::x2::mul2(act::x2::pk(x[k], x[k + 1]), inv), v[k], v[k + 1]);
+  if (__builtin_expect(byte == kTopScale, 0)) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = fminf(fmaxf(v[k], -240.0f), 240.0f);
+    for (int k = 0; k < N; ++k) v[k] = fminf(fmaxf(v[k], -240.0f), 240.0f);
   }
-  return encode2(v[0], v[1]) | (encode2(v[2], v[3]) << 16);
+#pragma unroll
+  for (int k = 0; k < N / 4; ++k)
+    c[k] = encode2(v[4 * k], v[4 * k + 1]) | (encode2(v[4 * k + 2], v[4 * k + 3]) << 16);
 }
-constexpr uint32_t kTopScale = 247;
 
 // Two values from the low 16 bits of c (exact: every e4m3 number is an fp16
 // number).
@@ -94,17 +102,24 @@ __device__ __forceinline__ void decode4(uint32_t c, float s, float* x) {
   decode2(c >> 16, s, x[2], x[3]);
 }
 
+// The bits of the largest magnitude of x[0 .. N - 1] (a NaN's where there is one).
+template <int N>
+__device__ __forceinline__ uint32_t largest(const float* x) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int k = 1; k + 1 < N; k += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x[k]), "f"(x[k + 1]));
+  if (N % 2 == 0) asm("max.NaN.abs.f32 %0, %0, %1, %1;" : "+f"(m) : "f"(x[N - 1]));
+  return __float_as_uint(m) & 0x7fffffffu;
+}
+
 // One row of a group, held by one thread: 16 values to 16 codes and the scale
 // byte, and back.
 __device__ __forceinline__ uint4 encode_row(const float* x, uint32_t& byte) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < kGroup; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
-  byte = scale_byte(m);
-  const float inv = inv_scale(byte);
-  const bool top = byte == kTopScale;
-  return make_uint4(encode4(x, inv, top), encode4(x + 4, inv, top), encode4(x + 8, inv, top),
-                    encode4(x + 12, inv, top));
+  byte = scale_byte(largest<kGroup>(x));
+  uint32_t c[kGroup / 4];
+  encode<kGroup>(x, byte, c);
+  return make_uint4(c[0], c[1], c[2], c[3]);
 }
 __device__ __forceinline__ void decode_row(uint4 c, uint32_t byte, float* x) {
   const float s = scale(byte);

@@ -55,10 +55,12 @@ __device__ __forceinline__ void store_ckpt8(void* ckpt, const Prob& P, int64_t r
   const int64_t k = col % ck::kGroup;
   if (!row_ok || col - k >= P.N) return;
   const float w[4] = {col < P.N ? v : 0.0f, 0.0f, 0.0f, 0.0f};
+  uint32_t c[1];
+  ck::encode<4>(w, b, c);
   const int64_t blk = ckpt8_block(P, row, col);
   uint8_t* base = static_cast<uint8_t*>(ckpt);
   base[blk * ck::kBlockBytes + (row % ck::kRows) * ck::kGroup + k] =
-      static_cast<uint8_t>(ck::encode4(w, ck::inv_scale(b), b == ck::kTopScale));
+      static_cast<uint8_t>(c[0]);
   if (k == 0) base[ck::scale_offset(P.M, P.N) + blk * ck::kRows + row % ck::kRows] = static_cast<uint8_t>(b);
 }
 

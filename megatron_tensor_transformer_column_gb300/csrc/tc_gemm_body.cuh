@@ -672,7 +672,7 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
     const int part = (warp - 2) >> 2;    // which of the kParts column ranges of a tile
     constexpr int kCols = 256 / kParts;  // accumulator columns per warp (4 chunks of N)
     EpiStore es{smem_base + static_cast<uint32_t>(kStages * kStageBytes + (warp - 2) * 2 * epi_block_bytes<N>()), 0u,
-                0, 0, 0};
+                0, 0, 0, 0, 0};
     const int wi = static_cast<int>(rank) * kEW + (warp - 2);  // stream-K slot position of this warp
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -687,6 +687,11 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
       const int64_t grow = static_cast<int64_t>(ti.m0) + kBM * static_cast<int>(rank) + row;
       const int wrow = ti.m0 + kBM * static_cast<int>(rank) + q * 32;  // this warp's first row
       es.rows = P.M;
+      if (kCk8) {
+        const int64_t blk = static_cast<int64_t>(wrow >> 5) * ck::groups(P.N);
+        es.ck_codes = blk * ck::kBlockBytes + lane * ck::kGroup;
+        es.ck_scales = ck::scale_offset(P.M, P.N) + blk * ck::kRows + lane;
+      }
       if (P.out_striped && wrow < P.M) {  // a warp's 32 rows never cross a stripe boundary
         es.sj = stripe_of(p.stripes, wrow);
         es.sy0 = static_cast<int>(p.stripes.row0[es.sj]);
@@ -763,8 +768,8 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
             act::x2::swiglu_xn(g, u, h);
             if constexpr (kCk8) {
               if (row_ok) {
-                store_ckpt8<N>(P.out0, P, grow, ti.n0 + oc, nvalid, g);
-                store_ckpt8<N>(P.out1, P, grow, ti.n0 + oc, nvalid, u);
+                store_ckpt8<N>(P.out0, es, ti.n0 + oc, nvalid, g);
+                store_ckpt8<N>(P.out1, es, ti.n0 + oc, nvalid, u);
               }
             } else {
               store_block<N>(es, p, P, 0, ti.n0 + oc, wrow, nvalid, g, lane);

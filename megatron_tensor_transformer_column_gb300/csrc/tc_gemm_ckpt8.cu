@@ -4,9 +4,17 @@
 // accumulators, and the dgrad GEMM, whose epilogue reads them, takes act' of
 // the kept values and recomputes H.
 //
-// Bound by the tensor cores like the launches they stand beside: an epilogue
-// moves 1.0625 bytes per pre-activation instead of 2, with plain stores and
-// loads of a warp's own block, and does about two instructions more for it.
+// Bound by the tensor cores like the launches they stand beside, or, with short
+// K, by the epilogue: it moves 1.0625 bytes per pre-activation instead of 2,
+// with plain stores and loads of a warp's own block, and a thread finds its
+// row's largest magnitudes, scales and codes in about 35 instructions per 16
+// elements.  Measured on GB300 (device time of the launch, against the one with
+// bf16 pre-activations and, for dgrad, recomputed H):
+//   GeLU, 8192 x 768, 4 x 768:          column 54 against 51 us, dgrad 61 against 68
+//   GeLU, 8192 x 2048, 8192 hidden:     column 176 against 176 us, dgrad 192 against 200
+//   SwiGLU, 8192 x 4096, 8 x 1376:      column 820 against 849-875 us, dgrad 499 against 554
+// Where the checkpoint's rows lie is worked out once per tile (column of the
+// first shape 57 -> 54 us), dA and H leave behind one fence (dgrad 65 -> 63).
 #include "tc_gemm_body.cuh"
 
 namespace tpmlp {

@@ -257,6 +257,9 @@ struct EpiStore {
   uint32_t next; // the block the next store uses (every bulk group reads one block)
   int rows;      // rows of the current problem's outputs
   int sj, sy0;   // striped out0: the stripe of this warp's rows and its first row
+  // 8-bit checkpoints of the current problem: where this thread's row of the
+  // problem's first group and its scale byte lie (the same in every buffer).
+  int64_t ck_codes, ck_scales;
 };
 
 template <int N>
@@ -396,23 +399,24 @@ __device__ __forceinline__ void add_bias(const void* bias, int col, int nvalid, 
   for (int j = 0; j < N; ++j) v[j] += b[j];
 }
 
-// This thread's row of a chunk (columns x .. x + N - 1 of row grow, nvalid of
-// them inside the tensor) to an 8-bit checkpoint of the problem's output and
-// back.  x is a multiple of 16 and a warp's rows are one block of 32, so each
-// group's 16 bytes a lane are 512 contiguous bytes a warp: plain stores, no
-// staging.
+// This thread's row of a chunk (columns x .. x + N - 1, nvalid of them inside
+// the tensor) to an 8-bit checkpoint and back.  x is a multiple of 16 and a
+// warp's rows are one block of 32, so each group's 16 bytes a lane are 512
+// contiguous bytes a warp: plain stores, no staging.
 template <int N>
-__device__ __forceinline__ void store_ckpt8(void* ckpt, const Prob& P, int64_t grow, int x, int nvalid,
-                                            const float (&v)[N]) {
-  const int64_t blk = (grow >> 5) * ck::groups(P.N) + x / ck::kGroup;
-  uint8_t* codes = static_cast<uint8_t*>(ckpt) + blk * ck::kBlockBytes + (grow & 31) * ck::kGroup;
-  uint8_t* scales = static_cast<uint8_t*>(ckpt) + ck::scale_offset(P.M, P.N) + blk * ck::kRows + (grow & 31);
+__device__ __forceinline__ void store_ckpt8(void* ckpt, const EpiStore& es, int x, int nvalid, const float (&v)[N]) {
+  uint8_t* codes = static_cast<uint8_t*>(ckpt) + es.ck_codes + int64_t{x} * (ck::kBlockBytes / ck::kGroup);
+  uint8_t* scales = static_cast<uint8_t*>(ckpt) + es.ck_scales + int64_t{x} * (ck::kRows / ck::kGroup);
 #pragma unroll
   for (int g = 0; g < N / ck::kGroup; ++g) {
     if (ck::kGroup * g >= nvalid) break;
     float w[ck::kGroup];
 #pragma unroll
-    for (int k = 0; k < ck::kGroup; ++k) w[k] = ck::kGroup * g + k < nvalid ? v[ck::kGroup * g + k] : 0.0f;
+    for (int k = 0; k < ck::kGroup; ++k) w[k] = v[ck::kGroup * g + k];
+    if (ck::kGroup * (g + 1) > nvalid) {  // the tensor ends inside the group
+#pragma unroll
+      for (int k = 0; k < ck::kGroup; ++k) w[k] = ck::kGroup * g + k < nvalid ? w[k] : 0.0f;
+    }
     uint32_t byte;
     const uint4 c = ck::encode_row(w, byte);
     *reinterpret_cast<uint4*>(codes + g * ck::kBlockBytes) = c;
@@ -421,11 +425,9 @@ __device__ __forceinline__ void store_ckpt8(void* ckpt, const Prob& P, int64_t g
 }
 
 template <int N>
-__device__ __forceinline__ void load_ckpt8(const void* ckpt, const Prob& P, int64_t grow, int x, int nvalid,
-                                           float (&v)[N]) {
-  const int64_t blk = (grow >> 5) * ck::groups(P.N) + x / ck::kGroup;
-  const uint8_t* codes = static_cast<const uint8_t*>(ckpt) + blk * ck::kBlockBytes + (grow & 31) * ck::kGroup;
-  const uint8_t* scales = static_cast<const uint8_t*>(ckpt) + ck::scale_offset(P.M, P.N) + blk * ck::kRows + (grow & 31);
+__device__ __forceinline__ void load_ckpt8(const void* ckpt, const EpiStore& es, int x, int nvalid, float (&v)[N]) {
+  const uint8_t* codes = static_cast<const uint8_t*>(ckpt) + es.ck_codes + int64_t{x} * (ck::kBlockBytes / ck::kGroup);
+  const uint8_t* scales = static_cast<const uint8_t*>(ckpt) + es.ck_scales + int64_t{x} * (ck::kRows / ck::kGroup);
 #pragma unroll
   for (int g = 0; g < N / ck::kGroup; ++g) {
     uint4 c = make_uint4(0, 0, 0, 0);
@@ -458,7 +460,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
     case EPI_GELU_FWD: {
       add_bias<N>(P.aux0, x, nvalid, acc);
       if constexpr (kCk8) {
-        if (row_ok) store_ckpt8<N>(P.out0, P, grow, x, nvalid, acc);
+        if (row_ok) store_ckpt8<N>(P.out0, es, x, nvalid, acc);
         act::x2::gelu_xn(acc);
         store_block<N>(es, p, P, 1, x, y, nvalid, acc, lane);
         break;
@@ -479,10 +481,9 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
     case EPI_GELU_BWD: {
       if constexpr (kCk8) {
         float a[N], h[N];
-        load_ckpt8<N>(P.aux0, P, grow, x, nload, a);
+        load_ckpt8<N>(P.aux0, es, x, nload, a);
         act::x2::gelu_bwd_xn<true>(acc, a, h);
-        store_block<N>(es, p, P, 1, x, y, nvalid, h, lane);
-        store_block<N>(es, p, P, 0, x, y, nvalid, a, lane);
+        store_pair<N>(es, p, P, 1, 0, x, y, h, a, lane);
         break;
       }
       if (N == 32 && !P.out1 && y < es.rows) {  // A staged through the output block, dA written over it
@@ -519,12 +520,11 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
     case EPI_SWIGLU_BWD: {
       if constexpr (kCk8) {
         float g[N], u[N], h[N];
-        load_ckpt8<N>(P.aux0, P, grow, x, nload, g);
-        load_ckpt8<N>(P.aux1, P, grow, x, nload, u);
+        load_ckpt8<N>(P.aux0, es, x, nload, g);
+        load_ckpt8<N>(P.aux1, es, x, nload, u);
         act::x2::swiglu_bwd_xn<true>(acc, g, u, h);
         store_block<N>(es, p, P, 2, x, y, nvalid, h, lane);
-        store_block<N>(es, p, P, 0, x, y, nvalid, g, lane);
-        store_block<N>(es, p, P, 1, x, y, nvalid, u, lane);
+        store_pair<N>(es, p, P, 0, 1, x, y, g, u, lane);
         break;
       }
       if (N == 32 && !P.out2 && y < es.rows) {  // G and U staged through both blocks, dG and dU written over them
