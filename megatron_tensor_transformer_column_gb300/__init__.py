@@ -549,9 +549,16 @@ def _ptrs(name: str, xs, shapes, dtype, device):
     return (ctypes.c_void_p * len(shapes))(*[_ptr(name, x, s, dtype, device) for x, s in zip(xs, shapes)])
 
 
-def _addresses(xs):
-    """The addresses of tensors that were made here."""
-    return (ctypes.c_void_p * len(xs))(*[x.data_ptr() for x in xs])
+def _new_list(like, shapes):
+    """New tensors of like's type and device, and their addresses."""
+    xs = [like.new_empty(s) for s in shapes]
+    return xs, (ctypes.c_void_p * len(xs))(*[x.data_ptr() for x in xs])
+
+
+def _current(device) -> int:
+    """The handle of the device's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _on(device, stream):
@@ -604,7 +611,7 @@ def ckpt8_pack(x, out=None, stream=None):
         if out is None:
             out = torch.empty(n, dtype=torch.uint8, device=x.device)
         tpmlp_ckpt8_pack("bf16" if x.dtype == torch.bfloat16 else "fp32", rows, cols, src, ld,
-                         _ptr("out", out, (n,), torch.uint8, x.device))
+                         _ptr("out", out, (n,), torch.uint8, x.device), _current(x.device))
     return out
 
 
@@ -622,7 +629,7 @@ def ckpt8_unpack(ckpt, rows: int, cols: int, dtype: str = "bf16", out=None, stre
             raise ValueError(f"out: expected {(rows, cols)} of {td} on {ckpt.device}, got {tuple(out.shape)} of "
                              f"{out.dtype} on {out.device}")
         dst, ld = _rows_apart("out", out)
-        tpmlp_ckpt8_unpack(dtype, rows, cols, src, dst, ld)
+        tpmlp_ckpt8_unpack(dtype, rows, cols, src, dst, ld, _current(ckpt.device))
     return out
 
 
@@ -639,6 +646,7 @@ class ShardedMLP:
         self.device = torch.device(device or "cuda")
         self.tdtype = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
         self.workspace = torch.zeros(tpmlp_workspace_size(self.plan), dtype=torch.uint8, device=self.device)
+        self._ckpt8_sizes = None
 
     @property
     def swiglu(self) -> bool:
@@ -702,7 +710,9 @@ class ShardedMLP:
     # ---- 8-bit activation checkpoints: what backward needs of the pre-activations in 1.0625 bytes each
     def ckpt8_sizes(self):
         """Bytes of each checkpoint: one per shard (A_i), SwiGLU two (G_i, then U_i)."""
-        return [tpmlp_ckpt8_size(self.plan.T, w) for w in self.plan.d_i] * (2 if self.swiglu else 1)
+        if self._ckpt8_sizes is None:
+            self._ckpt8_sizes = [tpmlp_ckpt8_size(self.plan.T, w) for w in self.plan.d_i] * (2 if self.swiglu else 1)
+        return self._ckpt8_sizes
 
     def _ckpt8_args(self, X, W1_i, W2_i, W3_i):
         """Checked addresses of the inputs that both passes share, and the shapes they are checked by."""
@@ -726,13 +736,13 @@ class ShardedMLP:
             if out is None:
                 Y = X.new_empty((p.T, p.d))
                 ckpt = [X.new_empty(n, dtype=torch.uint8) for n in sizes]
-                y, c = Y.data_ptr(), _addresses(ckpt)
+                y, c = Y.data_ptr(), (ctypes.c_void_p * len(ckpt))(*[x.data_ptr() for x in ckpt])
             else:
                 Y, ckpt = out
                 y = _ptr("Y", Y, (p.T, p.d), td, dev)
                 c = _ptrs("ckpt", ckpt, [(n,) for n in sizes], torch.uint8, dev)
             scratch, H = _pieces([p.T * w * X.element_size() for w in p.d_i], dev)
-            tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, y, c, H, self.workspace.data_ptr())
+            tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, y, c, H, self.workspace.data_ptr(), _current(dev))
         return Y, ckpt
 
     def backward_ckpt8(self, X, W1_i, W2_i, ckpt, dY, W3_i=None, stream=None, bias_grads=False, out=None):
@@ -746,9 +756,10 @@ class ShardedMLP:
         es = X.element_size()
         with _on(dev, stream):
             if out is None:
-                dX, dW1, dW2 = X.new_empty((p.T, p.d)), [X.new_empty(s) for s in col], [X.new_empty(s) for s in row]
-                dW3 = [X.new_empty(s) for s in col] if self.swiglu else None
-                to = dX.data_ptr(), _addresses(dW1), _addresses(dW3) if self.swiglu else None, _addresses(dW2)
+                dX = X.new_empty((p.T, p.d))
+                (dW1, to1), (dW2, to2) = _new_list(X, col), _new_list(X, row)
+                dW3, to3 = _new_list(X, col) if self.swiglu else (None, None)
+                to = dX.data_ptr(), to1, to3, to2
             else:
                 dX, dW1, dW3, dW2 = out
                 to = (_ptr("dX", dX, (p.T, p.d), td, dev), _ptrs("dW1", dW1, col, td, dev),
@@ -756,12 +767,14 @@ class ShardedMLP:
             db1 = db3 = db2 = None
             db = (None, None, None)
             if bias_grads:
-                db1, db2 = [X.new_empty(w) for w in p.d_i], X.new_empty(p.d)
-                db3 = [X.new_empty(w) for w in p.d_i] if self.swiglu else None
-                db = _addresses(db1), _addresses(db3) if self.swiglu else None, db2.data_ptr()
+                db2 = X.new_empty(p.d)
+                db1, to1 = _new_list(X, p.d_i)
+                db3, to3 = _new_list(X, p.d_i) if self.swiglu else (None, None)
+                db = to1, to3, db2.data_ptr()
             wide = [p.T * w * es for w in p.d_i]
             scratch, at = _pieces(wide * (3 if self.swiglu else 2), dev)  # H_i, then dact
-            tpmlp_backward_ckpt8(p, x, w1, w3, w2, c, at[:p.t], dy, at[p.t:], *to, *db, self.workspace.data_ptr())
+            tpmlp_backward_ckpt8(p, x, w1, w3, w2, c, at[:p.t], dy, at[p.t:], *to, *db, self.workspace.data_ptr(),
+                                 _current(dev))
         return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "db1": db1, "db3": db3, "db2": db2}
 
     def check(self, stream=None):
@@ -873,11 +886,10 @@ class ShardedAttentionProj:
         qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk)
         with _on(self.workspace.device, stream):
             if out is None:
-                out = [x.new_empty((p.T, q_ + k_)) for x, q_, k_ in zip(QKV_i, p.dq_i, p.dkv_i)]
-                to = _addresses(out)
+                out, to = _new_list(QKV_i[0], [(p.T, q_ + k_) for q_, k_ in zip(p.dq_i, p.dkv_i)])
             else:
                 to = self._in_place_or_dense("out", out, qkv)
-            tpmlp_attn_qk_norm_rope_forward(p, qkv, pos, q, k, to)
+            tpmlp_attn_qk_norm_rope_forward(p, qkv, pos, q, k, to, _current(self.workspace.device))
         return out
 
     def qk_norm_rope_backward(self, QKV_i, dQK_i, positions=None, gq=None, gk=None, dV_i=None, out=None, stream=None,
@@ -894,13 +906,14 @@ class ShardedAttentionProj:
             gain_grads = gq is not None or gk is not None
         with _on(dev, stream):
             if out is None:
-                out = [x.new_empty(x.shape) for x in QKV_i]
-                dqkv = _addresses(out)
+                out, dqkv = _new_list(QKV_i[0], [(p.T, n) for n in p.d_i])
             else:
                 dqkv = _ptrs("out", out, [(p.T, n) for n in p.d_i], td, dev)
-            dgq, dgk = (self._empty(p.head_dim), self._empty(p.head_dim)) if gain_grads else (None, None)
+            dgq = dgk = None
+            if gain_grads:
+                dgq, dgk = QKV_i[0].new_empty(p.head_dim), QKV_i[0].new_empty(p.head_dim)
             tpmlp_attn_qk_norm_rope_backward(p, qkv, pos, q, k, self._in_place_or_dense("dQK_i", dQK_i, dqkv), dv,
-                                             dqkv, dgq, dgk, self.workspace)
+                                             dqkv, dgq, dgk, self.workspace, _current(dev))
         return out, dgq, dgk
 
     def check(self, stream=None):
