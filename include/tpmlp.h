@@ -363,8 +363,9 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * columns of the [T x n_i] buffer are then read and overwritten.  dgq, dgk
  * [head_dim] (optional) in the plan's dtype.  One launch, and a second one when
  * a gain's gradient is asked for, which is also when workspace is needed (the
- * plan's, zero-filled or used).  Other overlaps of inputs and outputs are
- * refused (TPMLP_ERR_INVALID_ARG).  With T = 0 the gradients of the gains are
+ * plan's, zero-filled or used).  Other overlaps of the [T x ...] arrays, of
+ * outputs with inputs or with each other, are refused (TPMLP_ERR_INVALID_ARG).
+ * A gain's gradient is added in an order that depends on the device's SM count.  With T = 0 the gradients of the gains are
  * zero-filled.                                                               */
 typedef enum { TPMLP_ROPE_HALVES = 0, TPMLP_ROPE_PAIRS = 1 } tpmlp_rope_layout;
 typedef struct {
@@ -504,7 +505,8 @@ TPMLP_API const char* tpmlp_last_error(void);
 /* ABI version: 100 * major + minor (1.01: optional biases; 1.02: attention
  * projections; 1.03: sequence-parallel layout; 1.04: stream-K tail, larger
  * bf16 workspace; 1.05: tpmlp_last_split_tiles, tpmlp_eval_activation, a
- * 16 KB counter block in the bf16 workspace). */
+ * 16 KB counter block in the bf16 workspace).  The norm and rotation of the
+ * heads and the 8-bit checkpoints were added to 1.05; nothing of it changed. */
 TPMLP_API int tpmlp_version(void);
 
 /* Kernel launches the last compute call (tpmlp_forward, tpmlp_backward, a

@@ -1768,6 +1768,7 @@ tpmlp_status tpmlp_attn_qk_norm_rope_forward(const tpmlp_plan* plan, const void*
     for (int j = 0; j < plan->t; ++j) {
       if (!(in_place && j == i))
         TPMLP_TRY(check_overlap("QK", i, QK[i], plan->T * ldo * es, "QKV", j, QKV[j], plan->T * plan->d_i[j] * es));
+      if (j < i) TPMLP_TRY(check_overlap("QK", i, QK[i], plan->T * ldo * es, "QK", j, QK[j], plan->T * p.shards[j].ldo * es));
     }
     p.shards[i].x = QKV[i];
     p.shards[i].out = QK[i];
@@ -1797,6 +1798,7 @@ tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void
   const bool gains = dgq || dgk;
   if (gains && !plan->qk_norm)
     return fail(TPMLP_ERR_INVALID_ARG, "gain gradients without a norm (the plan rotates only)");
+  if (dgq && dgq == dgk) return fail(TPMLP_ERR_INVALID_ARG, "dgq and dgk are the same");
   TPMLP_TRY(check_ptr("workspace", workspace, !gains));
   const int64_t es = esize(plan);
   DeviceInfo di;
@@ -1820,6 +1822,7 @@ tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void
       TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "QKV", j, QKV[j], plan->T * plan->d_i[j] * es));
       if (!(in_place && j == i)) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dQK", j, dQK[j], qk));
       if (dV) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dV", j, dV[j], v));
+      if (j < i) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dQKV", j, dQKV[j], plan->T * plan->d_i[j] * es));
     }
     QkShard& S = p.shards[i];
     S.x = QKV[i];
@@ -1866,6 +1869,8 @@ tpmlp_status ckpt8_checks(tpmlp_dtype dtype, int64_t rows, int64_t cols, const c
     return fail(TPMLP_ERR_ALIGNMENT, "cols = %lld and ld = %lld must be multiples of %lld",
                 static_cast<long long>(cols), static_cast<long long>(ld), static_cast<long long>(mult));
   if (rows > kMax32 || ld > kMax32) return fail(TPMLP_ERR_UNSUPPORTED, "rows, cols and ld must each be below 2^31");
+  if (rows > (int64_t(1) << 48) / ld)  // past any memory; the products below stay within 64 bits
+    return fail(TPMLP_ERR_UNSUPPORTED, "rows * ld is above 2^48");
   TPMLP_TRY(check_ptr(name, x, rows == 0));
   TPMLP_TRY(check_ptr("ckpt", ckpt, rows == 0));
   if (rows && overlap(x, ((rows - 1) * ld + cols) * es, ckpt, ck::bytes(rows, cols)))
@@ -1901,6 +1906,15 @@ tpmlp_status tpmlp_ckpt8_unpack(tpmlp_dtype dtype, int64_t rows, int64_t cols, c
   return TPMLP_OK;
 }
 
+// No C++ exception leaves a C entry point: the planner's tables are host memory
+// that may run out.
+#define TPMLP_NO_THROW(body)                                              \
+  try {                                                                   \
+    body                                                                  \
+  } catch (...) {                                                         \
+    return fail(TPMLP_ERR_INVALID_ARG, "out of host memory");             \
+  }
+
 tpmlp_status tpmlp_forward_ckpt8(const tpmlp_plan* plan, const void* X, const void* const* W1, const void* const* W3,
                                  const void* const* W2, const void* const* b1, const void* const* b3, const void* b2,
                                  void* Y, void* const* ckpt, void* const* H, void* workspace, tpmlp_stream_t stream) {
@@ -1918,9 +1932,11 @@ tpmlp_status tpmlp_forward_ckpt8(const tpmlp_plan* plan, const void* X, const vo
   if (swiglu(plan)) TPMLP_TRY(check_bias("b3", b3, plan->t));
   TPMLP_TRY(check_ptr("b2", b2, true));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  TPMLP_TRY(fwd_column(plan, di, X, W1, W3, b1, swiglu(plan) ? b3 : nullptr, ckpt, H, workspace, st, nullptr,
-                       /*ckpt8=*/true));
-  return fwd_row(plan, di, W2, b2, Y, H, workspace, st);
+  TPMLP_NO_THROW(
+    TPMLP_TRY(fwd_column(plan, di, X, W1, W3, b1, swiglu(plan) ? b3 : nullptr, ckpt, H, workspace, st, nullptr,
+                         /*ckpt8=*/true));
+    return fwd_row(plan, di, W2, b2, Y, H, workspace, st);
+  )
 }
 
 tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* X, const void* const* W1, const void* const* W3,
@@ -1949,13 +1965,15 @@ tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* X, const v
   TPMLP_TRY(check_ptr("db2", db2, true));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   void* const* db3_ = swiglu(plan) ? db3 : nullptr;
-  if (tz) {  // zero-filled gradients as in tpmlp_backward
-    TPMLP_TRY(bwd_dgrad(plan, di, W2, ckpt, H, dY, dact, dW2, db2, workspace, st));
-    return bwd_fsum(plan, di, X, W1, W3, dact, dX, dW1, dW3, db1, db3_, workspace, st);
-  }
-  TPMLP_TRY(bwd_dgrad(plan, di, W2, ckpt, H, dY, dact, dW2, db2, workspace, st, /*recompute=*/true, nullptr,
-                      /*ckpt8=*/true));
-  return bwd_fsum(plan, di, X, W1, W3, dact, dX, dW1, dW3, db1, db3_, workspace, st, H, dY, dW2);
+  TPMLP_NO_THROW(
+    if (tz) {  // zero-filled gradients as in tpmlp_backward
+      TPMLP_TRY(bwd_dgrad(plan, di, W2, ckpt, H, dY, dact, dW2, db2, workspace, st));
+      return bwd_fsum(plan, di, X, W1, W3, dact, dX, dW1, dW3, db1, db3_, workspace, st);
+    }
+    TPMLP_TRY(bwd_dgrad(plan, di, W2, ckpt, H, dY, dact, dW2, db2, workspace, st, /*recompute=*/true, nullptr,
+                        /*ckpt8=*/true));
+    return bwd_fsum(plan, di, X, W1, W3, dact, dX, dW1, dW3, db1, db3_, workspace, st, H, dY, dW2);
+  )
 }
 
 tpmlp_status tpmlp_plan_set_sequence_stripes(tpmlp_plan* plan, int32_t nstripes, const int64_t* stripe_rows) {

@@ -131,6 +131,8 @@ def test_forward_refusals(lib):
     assert status_of(lambda: fwd(p, QK=(A + 16, B))) == 1            # overlaps its own input without being it
     assert status_of(lambda: fwd(p, QK=(B, A))) == 1                 # another shard's input
     assert status_of(lambda: fwd(p, QK=(A - 16 * 192 * 2 + 16, B))) == 1  # its last bytes reach into QKV[0]
+    assert status_of(lambda: fwd(p, QK=(B, B))) == 1                 # two shards' outputs on one another
+    assert status_of(lambda: fwd(p, QK=(B, B + 6128))) == 1
 
 
 def test_backward_refusals(lib):
@@ -141,6 +143,8 @@ def test_backward_refusals(lib):
     assert status_of(lambda: bwd(p, dQKV=(B + 16, 2 * B))) == 1      # over dQK without being it
     assert status_of(lambda: bwd(p, dV=[2 * B + 64, B + (1 << 21)])) == 1
     assert status_of(lambda: bwd(p, dgq=FAKE)) == 1                  # needs a workspace
+    assert status_of(lambda: bwd(p, dgq=FAKE, dgk=FAKE, ws=FAKE)) == 1
+    assert status_of(lambda: bwd(p, dQKV=(2 * B, 2 * B + 64))) == 1
     assert status_of(lambda: bwd(p, dgk=FAKE + 8, ws=FAKE)) == 3
     assert status_of(lambda: bwd(_plan(norm=False), dgq=FAKE, ws=FAKE)) == 1
 
@@ -170,6 +174,7 @@ def test_checkpoint_sizes(lib):
     (("bf16", 4, 16, A, 8, B), 2), (("bf16", 4, 12, A, 16, B), 3), (("bf16", 4, 16, A, 20, B), 3),
     (("fp32", 4, 6, A, 8, B), 3), (("bf16", 1 << 31, 16, A, 16, B), 4), (("bf16", 4, 16, None, 16, B), 1),
     (("bf16", 4, 16, A, 16, None), 1), (("bf16", 4, 16, A + 8, 16, B), 3), (("bf16", 4, 16, A, 16, B + 4), 3),
+    (("bf16", 1 << 30, 16, A, 1 << 30, B), 4),
     (("bf16", 4, 16, A, 16, A), 1), (("bf16", 4, 16, A, 1024, A + 3 * 2048 + 16), 1),
 ])
 def test_pack_refusals(lib, args, status):
