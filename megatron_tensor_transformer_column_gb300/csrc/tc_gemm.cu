@@ -7,8 +7,6 @@
 
 namespace tpmlp {
 
-#define TPMLP_TC_KERNELS(name, EW) TPMLP_TC_KERNEL_PAIR(name, EW, false)
-
 // Launch kinds whose epilogues carry the activation (the column GEMM, the
 // dgrad GEMM) also exist with 16 epilogue warps (suffix _w16).  The host
 // takes them where the tiles' K is short (tc_epi_warps_for): there the
@@ -18,16 +16,16 @@ namespace tpmlp {
 // extra warps only compete with the producer and the MMA issuer for issue
 // slots (measured on GB300: C2's column and dgrad launches -7 % and -5 % with
 // 16 warps; C3 to C5's +1 to +3 %).
-TPMLP_TC_KERNELS(tpmlp_fwd_column_gemm_act, 8)
-TPMLP_TC_KERNELS(tpmlp_fwd_column_gemm_act_w16, 16)
-TPMLP_TC_KERNELS(tpmlp_fwd_row_gemm_gsum, 8)
-TPMLP_TC_KERNELS(tpmlp_bwd_dgrad_act_wgrad2, 8)
-TPMLP_TC_KERNELS(tpmlp_bwd_dgrad_act_wgrad2_w16, 16)
-TPMLP_TC_KERNELS(tpmlp_bwd_dx_fsum_wgrad1, 8)
-TPMLP_TC_KERNELS(tpmlp_attn_qkv_proj, 8)
-TPMLP_TC_KERNELS(tpmlp_attn_out_proj_gsum, 8)
-TPMLP_TC_KERNELS(tpmlp_attn_out_proj_bwd, 8)
-TPMLP_TC_KERNELS(tpmlp_attn_qkv_bwd_dx_fsum, 8)
+TPMLP_TC_KERNELS(tpmlp_fwd_column_gemm_act, 8, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_fwd_column_gemm_act_w16, 16, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_fwd_row_gemm_gsum, 8, EPIS_STORE)
+TPMLP_TC_KERNELS(tpmlp_bwd_dgrad_act_wgrad2, 8, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_bwd_dgrad_act_wgrad2_w16, 16, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_bwd_dx_fsum_wgrad1, 8, EPIS_STORE)
+TPMLP_TC_KERNELS(tpmlp_attn_qkv_proj, 8, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_attn_out_proj_gsum, 8, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_attn_out_proj_bwd, 8, EPIS_ALL)
+TPMLP_TC_KERNELS(tpmlp_attn_qkv_bwd_dx_fsum, 8, EPIS_ALL)
 
 int tc_gemm_max_smem_bytes() { return kSmemBytes; }
 

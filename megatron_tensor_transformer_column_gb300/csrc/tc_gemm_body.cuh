@@ -477,10 +477,19 @@ __device__ __forceinline__ void sk_fold(const GemmParams& p, const Prob& P, cons
 }
 
 // ------------------------------------------------------------------ the kernel body
-// kCk8: the saved pre-activations are 8-bit checkpoints (out0 / out1 of the
-// forward epilogues, aux0 / aux1 of the backward ones), and the backward
-// epilogues recompute H.
-template <bool kSK, int kEW, bool kCk8>
+// The epilogues a kernel has.  A body with fewer of them is faster where tiles
+// are short (measured on GB300 on the GPT-2-small block: the row launch with
+// plain stores only 40.6 -> 37.9 us, the f-sum launch 83 -> 80 us, the launches
+// with 8-bit checkpoints 53 -> 49 and 61 -> 57 us), so a launch kind that uses
+// one kind of epilogue has no other in its kernel.
+enum EpiSet : int {
+  EPIS_ALL = 0,
+  EPIS_STORE = 1,    // EPI_STORE only
+  EPIS_CK8_FWD = 2,  // the column GEMM that writes 8-bit checkpoints (out0, out1)
+  EPIS_CK8_BWD = 3,  // the dgrad GEMM that reads them (aux0, aux1) and recomputes H
+};
+
+template <bool kSK, int kEW, int kEpis>
 __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_raw) {
   constexpr int N = chunk_cols(kEW);  // accumulator columns per epilogue chunk
   constexpr int kParts = kEW / 4;      // epilogue warps per TMEM lane quarter
@@ -687,7 +696,7 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
       const int64_t grow = static_cast<int64_t>(ti.m0) + kBM * static_cast<int>(rank) + row;
       const int wrow = ti.m0 + kBM * static_cast<int>(rank) + q * 32;  // this warp's first row
       es.rows = P.M;
-      if (kCk8) {
+      if (kEpis == EPIS_CK8_FWD || kEpis == EPIS_CK8_BWD) {
         const int64_t blk = static_cast<int64_t>(wrow >> 5) * ck::groups(P.N);
         es.ck_codes = blk * ck::kBlockBytes + lane * ck::kGroup;
         es.ck_scales = ck::scale_offset(P.M, P.N) + blk * ck::kRows + lane;
@@ -696,12 +705,13 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
         es.sj = stripe_of(p.stripes, wrow);
         es.sy0 = static_cast<int>(p.stripes.row0[es.sj]);
       }
-      if (row_ok && (P.epi == EPI_GELU_BWD || P.epi == EPI_SWIGLU_BWD)) {
+      if ((kEpis == EPIS_ALL || kEpis == EPIS_CK8_BWD) && row_ok &&
+          (P.epi == EPI_GELU_BWD || P.epi == EPI_SWIGLU_BWD)) {
         // Pull this thread's row of the saved pre-activation(s) into L2
         // while the accumulator is still being computed.
         const int c0 = part * kCols;
         const int cn = min(kCols, ti.valid_n - c0);
-        if (kCk8 && cn > 0) {
+        if (kEpis == EPIS_CK8_BWD && cn > 0) {
           // of 8-bit checkpoints, this warp's blocks: contiguous, a 128-byte line per lane
           const int64_t nb = (cn + ck::kGroup - 1) / ck::kGroup;
           const int64_t blk = static_cast<int64_t>(wrow >> 5) * ck::groups(P.N) + (ti.n0 + c0) / ck::kGroup;
@@ -715,7 +725,7 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
             ptx::prefetch_l2(static_cast<const char*>(P.aux0) + sc + lane * ck::kRows);
             if (P.epi == EPI_SWIGLU_BWD) ptx::prefetch_l2(static_cast<const char*>(P.aux1) + sc + lane * ck::kRows);
           }
-        } else if (!kCk8 && cn > 0) {
+        } else if (kEpis == EPIS_ALL && cn > 0) {
           const int64_t off = grow * P.ldo + ti.n0 + c0;
           const __nv_bfloat16* a0 = static_cast<const __nv_bfloat16*>(P.aux0) + off;
           for (int b = 0; b < 2 * cn; b += 128) ptx::prefetch_l2(reinterpret_cast<const char*>(a0) + b);
@@ -744,7 +754,7 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
         if (finish && vm > 0) sk_fold<N>(p, P, it, s.r, q0, tacc, part, kParts, wi, lane);
       }
       if (finish && vm > 0) {
-        if (P.epi == EPI_SWIGLU_FWD) {
+        if ((kEpis == EPIS_ALL || kEpis == EPIS_CK8_FWD) && P.epi == EPI_SWIGLU_FWD) {
           const bool merged = swiglu_merged(ti, P);
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -766,7 +776,7 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
             add_bias<N>(P.aux0, ti.n0 + oc, nvalid, g);
             add_bias<N>(P.aux1, ti.n0 + oc, nvalid, u);
             act::x2::swiglu_xn(g, u, h);
-            if constexpr (kCk8) {
+            if constexpr (kEpis == EPIS_CK8_FWD) {
               if (row_ok) {
                 store_ckpt8<N>(P.out0, es, ti.n0 + oc, nvalid, g);
                 store_ckpt8<N>(P.out1, es, ti.n0 + oc, nvalid, u);
@@ -785,7 +795,22 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
             uint32_t r[N];
             ptx::tmem_ld_32x32b(tacc + col, r);
             ptx::tmem_wait_ld();
-            epilogue_chunk<N, kCk8>(p, P, es, grow, row_ok, ti.n0 + col, wrow, min(N, ti.valid_n - col), r, lane);
+            const int nvalid = min(N, ti.valid_n - col);
+            if constexpr (kEpis == EPIS_ALL) {
+              epilogue_chunk<N>(p, P, es, grow, row_ok, ti.n0 + col, wrow, nvalid, r, lane);
+            } else {
+              float v[N];
+#pragma unroll
+              for (int j = 0; j < N; ++j) v[j] = __uint_as_float(r[j]);
+              if constexpr (kEpis == EPIS_STORE) {
+                add_bias<N>(P.aux0, ti.n0 + col, nvalid, v);
+                store_block<N>(es, p, P, 0, ti.n0 + col, wrow, nvalid, v, lane);
+              } else if constexpr (kEpis == EPIS_CK8_FWD) {
+                ckpt8_gelu_chunk<N>(p, P, es, row_ok, ti.n0 + col, wrow, nvalid, v, lane);
+              } else {
+                ckpt8_bwd_chunk<N>(p, P, es, row_ok, ti.n0 + col, wrow, nvalid, v, lane);
+              }
+            }
           }
         }
       }
@@ -814,16 +839,15 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
 
 // Two kernel symbols per launch kind (same body): the data-parallel schedule
 // and, with the suffix _sk, the one with a stream-K tail; EW is the number
-// of epilogue warps (kernel_for), CK8 whether the pre-activations are 8-bit
-// checkpoints.
-#define TPMLP_TC_KERNEL_PAIR(name, EW, CK8)                                                              \
+// of epilogue warps (kernel_for), EPIS the epilogues (EpiSet).
+#define TPMLP_TC_KERNELS(name, EW, EPIS)                                                                 \
   __global__ void __launch_bounds__(threads_for(EW), 1) name(const __grid_constant__ GemmParams p) {     \
     extern __shared__ __align__(1024) uint8_t smem_raw[];                                                \
-    tc_gemm_body<false, EW, CK8>(p, smem_raw);                                                           \
+    tc_gemm_body<false, EW, EPIS>(p, smem_raw);                                                          \
   }                                                                                                      \
   __global__ void __launch_bounds__(threads_for(EW), 1) name##_sk(const __grid_constant__ GemmParams p) { \
     extern __shared__ __align__(1024) uint8_t smem_raw[];                                                \
-    tc_gemm_body<true, EW, CK8>(p, smem_raw);                                                            \
+    tc_gemm_body<true, EW, EPIS>(p, smem_raw);                                                           \
   }
 
 }  // namespace tpmlp

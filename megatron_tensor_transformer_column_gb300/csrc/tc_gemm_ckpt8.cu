@@ -10,21 +10,21 @@
 // row's largest magnitudes, scales and codes in about 35 instructions per 16
 // elements.  Measured on GB300 (device time of the launch, against the one with
 // bf16 pre-activations and, for dgrad, recomputed H):
-//   GeLU, 8192 x 768, 4 x 768:          column 54 against 51 us, dgrad 61 against 68
-//   GeLU, 8192 x 2048, 8192 hidden:     column 176 against 176 us, dgrad 192 against 200
-//   SwiGLU, 8192 x 4096, 8 x 1376:      column 820 against 849-875 us, dgrad 499 against 554
-// Where the checkpoint's rows lie is worked out once per tile (column of the
-// first shape 57 -> 54 us), dA and H leave behind one fence (dgrad 65 -> 63).
+//   GeLU, 8192 x 768, 4 x 768:          column 49 against 51 us, dgrad 57 against 68
+//   GeLU, 8192 x 2048, 8192 hidden:     column 176 against 176 us, dgrad 190 against 200
+//   SwiGLU, 8192 x 4096, 8 x 1376:      column 820 against 849-875 us, dgrad 495 against 554
+// Each launch has a body with its own epilogues only (column 53 -> 49 us, dgrad
+// 61 -> 57 on the first shape); where the checkpoint's rows lie is worked out
+// once per tile; dA and H leave behind one fence.  Fetching a chunk's bytes
+// while the one before is worked on was measured equal and is not done.
 #include "tc_gemm_body.cuh"
 
 namespace tpmlp {
 
-#define TPMLP_TC_CKPT8_KERNELS(name, EW) TPMLP_TC_KERNEL_PAIR(name, EW, true)
-
-TPMLP_TC_CKPT8_KERNELS(tpmlp_fwd_column_gemm_act_ckpt8, 8)
-TPMLP_TC_CKPT8_KERNELS(tpmlp_fwd_column_gemm_act_ckpt8_w16, 16)
-TPMLP_TC_CKPT8_KERNELS(tpmlp_bwd_dgrad_act_ckpt8, 8)
-TPMLP_TC_CKPT8_KERNELS(tpmlp_bwd_dgrad_act_ckpt8_w16, 16)
+TPMLP_TC_KERNELS(tpmlp_fwd_column_gemm_act_ckpt8, 8, EPIS_CK8_FWD)
+TPMLP_TC_KERNELS(tpmlp_fwd_column_gemm_act_ckpt8_w16, 16, EPIS_CK8_FWD)
+TPMLP_TC_KERNELS(tpmlp_bwd_dgrad_act_ckpt8, 8, EPIS_CK8_BWD)
+TPMLP_TC_KERNELS(tpmlp_bwd_dgrad_act_ckpt8_w16, 16, EPIS_CK8_BWD)
 
 TcKernelFn tc_ckpt8_kernel(int tag, bool stream_k, int epi_warps) {
   const bool w16 = epi_warps == 16;

@@ -443,8 +443,7 @@ __device__ __forceinline__ void load_ckpt8(const void* ckpt, const EpiStore& es,
 // Epilogue of one N-column chunk (columns x .. x+N-1 of rows y .. y+31, this
 // thread's row grow) of a single accumulator.  Every lane takes part (the
 // stores are per warp); inputs are read only for valid rows and columns.
-// kCk8: the pre-activations are 8-bit checkpoints and H is recomputed.
-template <int N, bool kCk8>
+template <int N>
 __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& P, EpiStore& es, int64_t grow,
                                                bool row_ok, int x, int y, int nvalid, const uint32_t (&r)[N],
                                                int lane) {
@@ -459,12 +458,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
       break;
     case EPI_GELU_FWD: {
       add_bias<N>(P.aux0, x, nvalid, acc);
-      if constexpr (kCk8) {
-        if (row_ok) store_ckpt8<N>(P.out0, es, x, nvalid, acc);
-        act::x2::gelu_xn(acc);
-        store_block<N>(es, p, P, 1, x, y, nvalid, acc, lane);
-        break;
-      }
       if (N == 16 && !P.out_striped) {  // A and H behind one fence
         float h[N];
 #pragma unroll
@@ -479,13 +472,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
       break;
     }
     case EPI_GELU_BWD: {
-      if constexpr (kCk8) {
-        float a[N], h[N];
-        load_ckpt8<N>(P.aux0, es, x, nload, a);
-        act::x2::gelu_bwd_xn<true>(acc, a, h);
-        store_pair<N>(es, p, P, 1, 0, x, y, h, a, lane);
-        break;
-      }
       if (N == 32 && !P.out1 && y < es.rows) {  // A staged through the output block, dA written over it
         const uint32_t b = es.buf + es.next * epi_block_bytes<N>();
         if (lane == 0) ptx::bulk_wait_group_read<1>();  // the store that last used block b has read it
@@ -518,15 +504,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
       break;
     }
     case EPI_SWIGLU_BWD: {
-      if constexpr (kCk8) {
-        float g[N], u[N], h[N];
-        load_ckpt8<N>(P.aux0, es, x, nload, g);
-        load_ckpt8<N>(P.aux1, es, x, nload, u);
-        act::x2::swiglu_bwd_xn<true>(acc, g, u, h);
-        store_block<N>(es, p, P, 2, x, y, nvalid, h, lane);
-        store_pair<N>(es, p, P, 0, 1, x, y, g, u, lane);
-        break;
-      }
       if (N == 32 && !P.out2 && y < es.rows) {  // G and U staged through both blocks, dG and dU written over them
         if (lane == 0) ptx::bulk_wait_group_read<0>();
         __syncwarp();
@@ -568,6 +545,37 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
     }
     default:
       break;
+  }
+}
+
+// The same with 8-bit checkpoints for pre-activations: the GeLU column GEMM's
+// chunk, and those of the dgrad GEMM, which recompute H.
+template <int N>
+__device__ __forceinline__ void ckpt8_gelu_chunk(const GemmParams& p, const Prob& P, EpiStore& es, bool row_ok, int x,
+                                                 int y, int nvalid, float (&acc)[N], int lane) {
+  add_bias<N>(P.aux0, x, nvalid, acc);
+  if (row_ok) store_ckpt8<N>(P.out0, es, x, nvalid, acc);
+  act::x2::gelu_xn(acc);
+  store_block<N>(es, p, P, 1, x, y, nvalid, acc, lane);
+}
+
+template <int N>
+__device__ __forceinline__ void ckpt8_bwd_chunk(const GemmParams& p, const Prob& P, EpiStore& es, bool row_ok, int x,
+                                                int y, int nvalid, const float (&acc)[N], int lane) {
+  const int nload = row_ok ? nvalid : 0;
+  float h[N];
+  if (P.epi == EPI_GELU_BWD) {
+    float a[N];
+    load_ckpt8<N>(P.aux0, es, x, nload, a);
+    act::x2::gelu_bwd_xn<true>(acc, a, h);
+    store_pair<N>(es, p, P, 1, 0, x, y, h, a, lane);
+  } else {
+    float g[N], u[N];
+    load_ckpt8<N>(P.aux0, es, x, nload, g);
+    load_ckpt8<N>(P.aux1, es, x, nload, u);
+    act::x2::swiglu_bwd_xn<true>(acc, g, u, h);
+    store_block<N>(es, p, P, 2, x, y, nvalid, h, lane);
+    store_pair<N>(es, p, P, 0, 1, x, y, g, u, lane);
   }
 }
 
