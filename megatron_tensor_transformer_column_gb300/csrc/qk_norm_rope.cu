@@ -83,6 +83,10 @@ __device__ __forceinline__ void load_vec(const E* p, float (&v)[V]) {
       v[1] = __uint_as_float(q.x & 0xffff0000u);
       v[2] = __uint_as_float(q.y << 16);
       v[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else if constexpr (V == 2) {
+      const uint32_t q = *reinterpret_cast<const uint32_t*>(p);
+      v[0] = __uint_as_float(q << 16);
+      v[1] = __uint_as_float(q & 0xffff0000u);
     } else {
       v[0] = __bfloat162float(*p);
     }
@@ -93,6 +97,10 @@ __device__ __forceinline__ void load_vec(const E* p, float (&v)[V]) {
       v[1] = q.y;
       v[2] = q.z;
       v[3] = q.w;
+    } else if constexpr (V == 2) {
+      const float2 q = *reinterpret_cast<const float2*>(p);
+      v[0] = q.x;
+      v[1] = q.y;
     } else {
       v[0] = *p;
     }
@@ -112,12 +120,16 @@ __device__ __forceinline__ void store_vec(E* p, const float (&v)[V]) {
           make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
     } else if constexpr (V == 4) {
       *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    } else if constexpr (V == 2) {
+      *reinterpret_cast<uint32_t*>(p) = pack2(v[0], v[1]);
     } else {
       *p = __float2bfloat16_rn(v[0]);
     }
   } else {
     if constexpr (V == 4) {
       *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if constexpr (V == 2) {
+      *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
     } else {
       *p = v[0];
     }
@@ -352,9 +364,11 @@ __device__ __forceinline__ P row_of(P base, uint32_t tok, uint32_t ld) {
 }
 template <int V>
 constexpr bool kQueue = V > 1;  // single elements are loaded when they are needed
+// Units of a lane: heads of up to kMaxHeadDim elements on 32 lanes.
+__host__ __device__ constexpr int units_of_lane(int V) { return V >= 4 ? 1 : V == 2 ? 2 : 4; }
 // Bytes of a warp's queue.
 __host__ __device__ constexpr int queue_bytes(int V, int elem, bool bwd) {
-  return V > 1 ? kStages * (bwd ? 4 : 2) * 32 * V * elem : 0;
+  return V > 1 ? kStages * units_of_lane(V) * (bwd ? 4 : 2) * 32 * V * elem : 0;
 }
 __host__ __device__ constexpr int round16(int n) { return (n + 15) / 16 * 16; }
 struct Place {
@@ -387,7 +401,9 @@ template <typename E, int V, int NU, bool kPairs, bool kBwd>
 __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int nw, uint8_t* smem) {
   constexpr int kVecBytes = V * int(sizeof(E));
   constexpr int kQueueBytes = queue_bytes(V, sizeof(E), kBwd);
-  constexpr int kHeadVecs = kBwd ? 4 : 2;  // a head's vectors in the queue
+  constexpr int kUnitVecs = kBwd ? 4 : 2;          // a unit's vectors in the queue
+  constexpr int kRoundVecs = NU * kUnitVecs;       // a round's
+  static_assert(NU == units_of_lane(V), "units of a lane");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = p.lanes, G = p.groups;  // lanes of a head, heads of a round
   const int grp = lane / n, li = lane - grp * n, leader = grp * n;
@@ -467,16 +483,20 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     if constexpr (kQueue<V>) {
       if (get.tok < T) {
         const int h = get.h0 + grp;
-        const bool ok = on[0] && h < heads;  // else zeros, which add nothing to any sum
-        const Head<kBwd>& H = head[ok ? h : 0];
-        const uint32_t q = queue + slot * kHeadVecs * 32 * kVecBytes;
+        const Head<kBwd>& H = head[h < heads && grp < G ? h : 0];
         const E* x = reinterpret_cast<const E*>(row_of(H.x, get.tok, H.ldx));
-        copy_async<kVecBytes>(q, x + o1[0], ok);
-        copy_async<kVecBytes>(q + 32 * kVecBytes, x + o2[0], ok);
-        if constexpr (kBwd) {
-          const E* y = reinterpret_cast<const E*>(row_of(H.dy, get.tok, H.lddy));
-          copy_async<kVecBytes>(q + 64 * kVecBytes, y + o1[0], ok);
-          copy_async<kVecBytes>(q + 96 * kVecBytes, y + o2[0], ok);
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          if (i > 0 && i * n >= units) break;  // no lane has a unit there
+          const bool ok = on[i] && h < heads;  // else zeros, which add nothing to any sum
+          const uint32_t q = queue + (slot * kRoundVecs + i * kUnitVecs) * 32 * kVecBytes;
+          copy_async<kVecBytes>(q, x + o1[i], ok);
+          copy_async<kVecBytes>(q + 32 * kVecBytes, x + o2[i], ok);
+          if constexpr (kBwd) {
+            const E* y = reinterpret_cast<const E*>(row_of(H.dy, get.tok, H.lddy));
+            copy_async<kVecBytes>(q + 64 * kVecBytes, y + o1[i], ok);
+            copy_async<kVecBytes>(q + 96 * kVecBytes, y + o2[i], ok);
+          }
         }
         cursor_next(get, first, step, heads, rows);
       }
@@ -505,10 +525,10 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     for (int k = 0; k < V; ++k) c3[i][k] = c4[i][k] = 0.0f;
   }
 
-  // Vector 0 of a round in the queue.
-  auto queued = [&](int slot) {
-    return reinterpret_cast<const E*>(smem + at.queue + warp * kQueueBytes + slot * kHeadVecs * 32 * kVecBytes +
-                                      lane * kVecBytes);
+  // Vector 0 of a round's unit i in the queue.
+  auto queued = [&](int slot, int i) {
+    return reinterpret_cast<const E*>(smem + at.queue + warp * kQueueBytes +
+                                      (slot * kRoundVecs + i * kUnitVecs) * 32 * kVecBytes + lane * kVecBytes);
   };
 
   auto forward_head = [&](const Cursor& run, int slot) {
@@ -518,12 +538,14 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
     float a[NU][V], b[NU][V], ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      if constexpr (kQueue<V>) {
-        const E* q = queued(slot);
-        load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
-      } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = 0.0f;
+      for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = 0.0f;
+      if constexpr (kQueue<V>) {
+        if (i == 0 || i * n < units) {
+          const E* q = queued(slot, i);
+          load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
+        }
+      } else {
         if (ok && on[i]) {
           const E* x = reinterpret_cast<const E*>(row_of(H.x, run.tok, H.ldx));
           load_unit<E, V, kPairs>(x + o1[i], x + o2[i], a[i], b[i]);
@@ -559,13 +581,15 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       float ya[V], yb[V], sa[V], sb[V], t[V];
-      if constexpr (kQueue<V>) {
-        const E* q = queued(slot);
-        load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
-        load_unit<E, V, kPairs>(q + 64 * V, q + 96 * V, ya, yb);
-      } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = ya[k] = yb[k] = 0.0f;
+      for (int k = 0; k < V; ++k) a[i][k] = b[i][k] = ya[k] = yb[k] = 0.0f;
+      if constexpr (kQueue<V>) {
+        if (i == 0 || i * n < units) {
+          const E* q = queued(slot, i);
+          load_unit<E, V, kPairs>(q, q + 32 * V, a[i], b[i]);
+          load_unit<E, V, kPairs>(q + 64 * V, q + 96 * V, ya, yb);
+        }
+      } else {
         if constexpr (kBwd) {
           if (ok && on[i]) {
             const E* x = reinterpret_cast<const E*>(row_of(H.x, run.tok, H.ldx));
@@ -764,29 +788,33 @@ __global__ void __launch_bounds__(1024) tpmlp_attn_qk_gain_grad(const float* par
 
 using QkKernel = void (*)(QkParams);
 
-template <typename E, int V, int NU>
+template <typename E, int V>
 QkKernel pick(bool pairs, bool bwd) {
+  constexpr int NU = units_of_lane(V);
   if (bwd) return pairs ? tpmlp_attn_qk_norm_rope_bwd<E, V, NU, true> : tpmlp_attn_qk_norm_rope_bwd<E, V, NU, false>;
   return pairs ? tpmlp_attn_qk_norm_rope_fwd<E, V, NU, true> : tpmlp_attn_qk_norm_rope_fwd<E, V, NU, false>;
 }
 
 // The widest vector (in elements) that every part of a head is a whole number
-// of: 16 bytes, 8 bytes (bf16), or one element.
+// of, up to 16 bytes.  8192 tokens of 32 + 8 heads of 80, bf16, on GB300: 24 us
+// in 8-element vectors (all 80 rotated), 26 us in 4 (40), and, before 2 was
+// added, 134 us in single elements (20; 71 us with 2).
 int vector_width(bool bf16, int D, int R, bool pairs) {
-  const int most = bf16 ? 8 : 4;
-  for (int V = most; V >= 4; V /= 2)
+  for (int V = bf16 ? 8 : 4; V >= 2; V /= 2)
     if (D % (2 * V) == 0 && (pairs || R % (2 * V) == 0)) return V;
   return 1;
 }
 
 QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
   if (bf16) {
-    if (V == 8) return pick<__nv_bfloat16, 8, 1>(pairs, bwd);
-    if (V == 4) return pick<__nv_bfloat16, 4, 1>(pairs, bwd);
-    return pick<__nv_bfloat16, 1, 4>(pairs, bwd);
+    if (V == 8) return pick<__nv_bfloat16, 8>(pairs, bwd);
+    if (V == 4) return pick<__nv_bfloat16, 4>(pairs, bwd);
+    if (V == 2) return pick<__nv_bfloat16, 2>(pairs, bwd);
+    return pick<__nv_bfloat16, 1>(pairs, bwd);
   }
-  if (V == 4) return pick<float, 4, 1>(pairs, bwd);
-  return pick<float, 1, 4>(pairs, bwd);
+  if (V == 4) return pick<float, 4>(pairs, bwd);
+  if (V == 2) return pick<float, 2>(pairs, bwd);
+  return pick<float, 1>(pairs, bwd);
 }
 
 }  // namespace

@@ -95,6 +95,7 @@ SHAPES = [  # D, R, layout
     (128, 128, "halves"), (128, 128, "pairs"), (96, 96, "halves"), (96, 24, "halves"), (64, 32, "pairs"),
     (256, 256, "halves"), (256, 64, "pairs"), (80, 20, "halves"), (20, 10, "halves"), (20, 20, "pairs"),
     (8, 8, "halves"), (2, 2, "halves"), (2, 2, "pairs"), (64, 0, "halves"), (250, 126, "halves"), (254, 254, "pairs"),
+    (252, 252, "halves"), (252, 100, "pairs"), (244, 20, "halves"), (132, 132, "halves"), (4, 4, "pairs"),
 ]
 
 
