@@ -311,3 +311,33 @@ def test_empty(gpu_lib):
     assert Y.shape == (0, 64) and all(not x.any() for x in g["dW1"] + g["dW2"] + g["db1"] + [g["db2"]])
     x = torch.empty(0, 16, dtype=torch.bfloat16, device="cuda")
     assert tp.ckpt8_unpack(tp.ckpt8_pack(x), 0, 16).shape == (0, 16)
+
+
+def test_python_refusals(gpu_lib):
+    """Wrong shapes, types, strides and devices are refused before any launch."""
+    tp = gpu_lib
+    mlp, s = setup(tp, 40, 64, (32, 16), "swiglu", "bf16", bias=False)
+    _, ckpt = mlp.forward_ckpt8(s["X"], s["W1"], s["W2"], s["W3"])
+    ok = dict(X=s["X"], W1_i=s["W1"], W2_i=s["W2"], W3_i=s["W3"])
+    for kw in (dict(X=s["X"][:39]), dict(X=s["X"].float()), dict(X=s["X"].cpu()), dict(W1_i=s["W1"][:1]),
+               dict(W3_i=None), dict(W2_i=s["W1"]), dict(b1_i=[torch.zeros(32, device="cuda")] * 2),
+               dict(W1_i=[w.t().contiguous().t() for w in s["W1"]])):
+        with pytest.raises(ValueError):
+            mlp.forward_ckpt8(**{**ok, **kw})
+    for kw in (dict(ckpt=ckpt[:3]), dict(ckpt=[c[:-1] for c in ckpt]), dict(ckpt=[c.short() for c in ckpt]),
+               dict(dY=s["dY"][:3])):
+        with pytest.raises(ValueError):
+            mlp.backward_ckpt8(**{**ok, **dict(ckpt=ckpt, dY=s["dY"]), **kw})
+    x = torch.zeros(8, 32, dtype=torch.bfloat16, device="cuda")
+    for y in (x.t(), x.half(), x[0], x.expand(8, 32)[:, ::2]):
+        with pytest.raises(ValueError):
+            tp.ckpt8_pack(y)
+    with pytest.raises(tp.TpmlpError):
+        tp.ckpt8_pack(x[:1].expand(8, 32))  # rows on top of one another
+    with pytest.raises(tp.TpmlpError):
+        tp.ckpt8_pack(x[:, 1:17])  # not on a 16-byte boundary
+    buf = tp.ckpt8_pack(x)
+    # (9 rows have the same size as 8: nothing can tell those apart)
+    for kw in (dict(rows=33), dict(cols=48), dict(out=x[:, :16]), dict(out=x.float())):
+        with pytest.raises(ValueError):
+            tp.ckpt8_unpack(**{**dict(ckpt=buf, rows=8, cols=32), **kw})

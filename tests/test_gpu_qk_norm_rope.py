@@ -268,3 +268,57 @@ def test_empty(gpu_lib):
     assert p.qk_norm_rope_forward([e(192)], gq=g, gk=g)[0].shape == (0, 128)
     dQKV, dgq, dgk = p.qk_norm_rope_backward([e(192)], [e(128)], gq=g, gk=g, dV_i=[e(64)])
     assert dQKV[0].shape == (0, 192) and not dgq.any() and not dgk.any()
+
+
+def test_two_threads_on_two_streams(gpu_lib):
+    """Two host threads, each with its plan, workspace and stream, at the same time: the bits of one after the
+    other."""
+    import threading
+    jobs = []
+    for seed, (T, hq, hkv, D, layout) in enumerate([(700, [4, 2], [2, 1], 96, "halves"), (900, [8], [2], 64, "pairs")]):
+        s = make(T, hq, hkv, D, "bf16", seed=seed)
+        p = proj_of(gpu_lib, T, s, "bf16", D, layout=layout)
+        call = lambda p=p, s=s, **kw: p.qk_norm_rope_backward(s["QKV"], s["dQK"], s["pos"], s["gq"], s["gk"], s["dV"],
+                                                              **kw)
+        jobs.append((call, call()))
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            for _ in range(20):
+                got[i].append(jobs[i][0](stream=st))
+            st.synchronize()
+        except Exception as e:  # reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors, errors
+    for (_, (dQKV, dgq, dgk)), runs in zip(jobs, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(dQKV + [dgq, dgk], r[0] + [r[1], r[2]]))
+
+
+def test_python_refusals(gpu_lib):
+    """Wrong shapes, types, strides and devices are refused before any launch."""
+    s = make(20, [2], [2], 32, "bf16")
+    p = proj_of(gpu_lib, 20, s, "bf16", 32)
+    bad = [dict(QKV_i=[s["QKV"][0][:10]]), dict(QKV_i=[s["QKV"][0].float()]), dict(QKV_i=[s["QKV"][0].cpu()]),
+           dict(QKV_i=[s["QKV"][0].t().contiguous().t()]), dict(QKV_i=s["QKV"] * 2),
+           dict(positions=s["pos"].int()), dict(positions=s["pos"][:5]), dict(positions=s["pos"].cpu()),
+           dict(gq=s["gq"][:16]), dict(gk=s["gk"].float()), dict(out=[torch.empty_like(s["QKV"][0])]), dict(out=[])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            p.qk_norm_rope_forward(**{**dict(QKV_i=s["QKV"], positions=s["pos"], gq=s["gq"], gk=s["gk"]), **kw})
+    with pytest.raises(ValueError):  # nothing says where dV comes from
+        p.qk_norm_rope_backward(s["QKV"], s["dQK"], s["pos"], s["gq"], s["gk"])
+    with pytest.raises(ValueError):
+        gpu_lib.ShardedAttentionProj(20, 64, [64], [64]).qk_norm_rope_forward(s["QKV"])
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    f = proj_of(gpu_lib, 20, make(20, [2], [2], 32, "fp32"), "fp32", 32)
+    with pytest.raises(ValueError):  # a workspace from before the norm was described
+        gpu_lib.tpmlp_attn_qk_norm_rope_backward(f.plan, [1 << 20], None, None, None, [1 << 22], None, [1 << 24],
+                                                 1 << 26, None, small)
