@@ -41,8 +41,9 @@
 // A first version with the loads in registers and every lane computing its own
 // angles took 147 and 359 us on the former: it was bound by instruction issue
 // (250 instructions a round forward) and latency.  What bounds it now is issue
-// and the latency of a round's chain (load, sum, root, store) together: 60 % of
-// the issue slots taken with 16 warps an SM, which is what the registers allow.
+// and the latency of a round's chain (load, sum, root, store) together: 55 % of
+// the issue slots taken (190 instructions a round, backward 370) with 16 warps
+// an SM, which is what the registers allow.
 // Two heads a lane and round (4 % less time on the former shape, 1 to 30 %
 // more on small and 64-wide ones) and queues of four or six rounds (no gain)
 // were measured and not kept; a queue of two helps the latter shape (94 us) and
@@ -819,6 +820,8 @@ QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
 
 }  // namespace
 
+// A token's angles, in rounds of heads, for the deal of the CTAs to the kinds: 2
+// and 3 were measured equal to 3 % slower (8 shards of 16 + 1 heads).
 constexpr double kAngleWork = 1.0;
 
 // Lays the launch out (lanes, parts, CTAs of each kind) and launches it.
