@@ -961,7 +961,11 @@ def _make_checkpoint_function():
 
     class TPMLPCheckpointFunction(torch.autograd.Function):
         """TPMLPFunction with the pre-activations kept as 8-bit checkpoints between the passes: it saves X, the
-        weights and 1.0625 bytes per pre-activation."""
+        weights and 1.0625 bytes per pre-activation.
+
+        In a CUDA graph capture, capture forward and backward together, and let no eager autograd graph of the same
+        leaves be alive then: autograd accumulates a leaf's gradient on the stream of the first graph that used it,
+        which a capture cannot take in.  ShardedMLP.forward_ckpt8 and backward_ckpt8 know no such thing."""
 
         @staticmethod
         def forward(ctx, mlp: ShardedMLP, X, *weights):

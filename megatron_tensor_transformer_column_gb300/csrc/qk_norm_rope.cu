@@ -821,7 +821,7 @@ QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
 }  // namespace
 
 // A token's angles, in rounds of heads, for the deal of the CTAs to the kinds: 2
-// and 3 were measured equal to 3 % slower (8 shards of 16 + 1 heads).
+// and 3 were measured equal to 8 % slower (8 shards of 16 + 1 heads).
 constexpr double kAngleWork = 1.0;
 
 // Lays the launch out (lanes, parts, CTAs of each kind) and launches it.

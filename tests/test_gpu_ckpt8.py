@@ -341,3 +341,29 @@ def test_python_refusals(gpu_lib):
     for kw in (dict(rows=33), dict(cols=48), dict(out=x[:, :16]), dict(out=x.float())):
         with pytest.raises(ValueError):
             tp.ckpt8_unpack(**{**dict(ckpt=buf, rows=8, cols=32), **kw})
+
+
+def test_block_past_32_bits(gpu_lib):
+    """Checkpoints and activations of more than 2^32 bytes: the last tokens' Y, checkpoint and dX, against the same
+    tokens alone (a row's sums do not depend on how many rows there are; K of 36 blocks, no stream-K)."""
+    tp = gpu_lib
+    free, _ = torch.cuda.mem_get_info()
+    if free < 80 << 30:
+        pytest.skip("needs 80 GB of device memory")
+    T, d, w, last = 1 << 20, 64, 4608, 96
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device="cuda") * std).bfloat16()
+    X, dY, W1, W2 = rnd(T, d), rnd(T, d), [rnd(d, w, std=0.1)], [rnd(w, d, std=0.02)]
+    whole, part = tp.ShardedMLP(T, d, [w]), tp.ShardedMLP(last, d, [w])
+    for m in (whole, part):
+        tp.tpmlp_plan_set_stream_k(m.plan, tp.STREAM_K_OFF)
+    Y, ckpt = whole.forward_ckpt8(X, W1, W2)
+    Yp, cp = part.forward_ckpt8(X[-last:].contiguous(), W1, W2)
+    assert ckpt[0].numel() > 1 << 32
+    assert torch.equal(Y[-last:], Yp)
+    codes, tail = T * w, last * w  # whole blocks of rows and columns
+    assert torch.equal(ckpt[0][:codes][-tail:], cp[0][:tail])
+    assert torch.equal(ckpt[0][codes:][-tail // 16:], cp[0][tail:])
+    dX = whole.backward_ckpt8(X, W1, W2, ckpt, dY)["dX"]
+    assert torch.equal(dX[-last:], part.backward_ckpt8(X[-last:].contiguous(), W1, W2, cp, dY[-last:].contiguous())["dX"])
+    whole.check()

@@ -322,3 +322,26 @@ def test_python_refusals(gpu_lib):
     with pytest.raises(ValueError):  # a workspace from before the norm was described
         gpu_lib.tpmlp_attn_qk_norm_rope_backward(f.plan, [1 << 20], None, None, None, [1 << 22], None, [1 << 24],
                                                  1 << 26, None, small)
+
+
+def test_past_32_bits(gpu_lib):
+    """Buffers of more than 2^32 bytes: the last tokens, against the same tokens alone."""
+    T, n, last = 2_200_000, 1024, 70
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    big = lambda w: torch.randn(T, w, generator=gen, device="cuda", dtype=torch.bfloat16)
+    x, dy, dv = big(n), big(768), big(256)
+    pos = torch.arange(T, device="cuda")
+    g = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    whole = gpu_lib.ShardedAttentionProj(T, 64, [512], [256])
+    part = gpu_lib.ShardedAttentionProj(last, 64, [512], [256])
+    for p in (whole, part):
+        p.set_qk_norm_rope(128)
+    cut = lambda t: t[-last:].contiguous()
+    y = whole.qk_norm_rope_forward([x], pos, g, g)[0]
+    assert torch.equal(y[-last:], part.qk_norm_rope_forward([cut(x)], cut(pos), g, g)[0])
+    dx = whole.qk_norm_rope_backward([x], [dy], pos, g, g, [dv])[0][0]
+    want = part.qk_norm_rope_backward([cut(x)], [cut(dy)], cut(pos), g, g, [cut(dv)])[0][0]
+    assert torch.equal(dx[-last:], want)
