@@ -856,7 +856,7 @@ class ShardedAttentionProj:
         tpmlp_attn_plan_set_qk_norm_rope(self.plan, head_dim, rotary_dim, layout, norm, eps, base, inv_freq)
         n = tpmlp_workspace_size(self.plan)
         if n > self.workspace.numel():
-            self.workspace = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self.workspace = torch.zeros(n, dtype=torch.uint8, device=self.workspace.device)
 
     def _qk_args(self, QKV_i, positions, gq, gk):
         """Checked addresses of the inputs that both passes share."""
