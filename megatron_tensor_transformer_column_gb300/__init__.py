@@ -646,7 +646,13 @@ class ShardedMLP:
         self.device = torch.device(device or "cuda")
         self.tdtype = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
         self.workspace = torch.zeros(tpmlp_workspace_size(self.plan), dtype=torch.uint8, device=self.device)
-        self._ckpt8_sizes = None
+        # What the 8-bit calls check and make, worked out once: shapes of W1_i / W3_i, W2_i, biases, checkpoints; bytes
+        # of one [T, d_i] array per shard.
+        p = self.plan
+        self._col, self._row = [(p.d, w) for w in p.d_i], [(w, p.d) for w in p.d_i]
+        self._wide = [(w,) for w in p.d_i]
+        self._ckpt8 = [(tpmlp_ckpt8_size(p.T, w),) for w in p.d_i] * (2 if self.swiglu else 1)
+        self._act_bytes = [p.T * w * (2 if dtype == "bf16" else 4) for w in p.d_i]
 
     @property
     def swiglu(self) -> bool:
@@ -710,38 +716,34 @@ class ShardedMLP:
     # ---- 8-bit activation checkpoints: what backward needs of the pre-activations in 1.0625 bytes each
     def ckpt8_sizes(self):
         """Bytes of each checkpoint: one per shard (A_i), SwiGLU two (G_i, then U_i)."""
-        if self._ckpt8_sizes is None:
-            self._ckpt8_sizes = [tpmlp_ckpt8_size(self.plan.T, w) for w in self.plan.d_i] * (2 if self.swiglu else 1)
-        return self._ckpt8_sizes
+        return [n for n, in self._ckpt8]
 
     def _ckpt8_args(self, X, W1_i, W2_i, W3_i):
-        """Checked addresses of the inputs that both passes share, and the shapes they are checked by."""
+        """Checked addresses of the inputs that both passes share."""
         p, td, dev = self.plan, self.tdtype, self.workspace.device
-        col, row = [(p.d, w) for w in p.d_i], [(w, p.d) for w in p.d_i]
-        return (_ptr("X", X, (p.T, p.d), td, dev), _ptrs("W1_i", W1_i, col, td, dev),
-                _ptrs("W3_i", W3_i, col, td, dev) if self.swiglu else None, _ptrs("W2_i", W2_i, row, td, dev), col, row)
+        return (_ptr("X", X, (p.T, p.d), td, dev), _ptrs("W1_i", W1_i, self._col, td, dev),
+                _ptrs("W3_i", W3_i, self._col, td, dev) if self.swiglu else None,
+                _ptrs("W2_i", W2_i, self._row, td, dev))
 
     def forward_ckpt8(self, X, W1_i, W2_i, W3_i=None, stream=None, b1_i=None, b3_i=None, b2=None, out=None):
         """forward with the pre-activations kept as 8-bit checkpoints.  Returns (Y, ckpt); out: those two, to write
         to.  H is scratch of the call."""
         import torch
         p, td, dev = self.plan, self.tdtype, self.workspace.device
-        x, w1, w3, w2, _, _ = self._ckpt8_args(X, W1_i, W2_i, W3_i)
-        wide = [(w,) for w in p.d_i]
-        b1 = _ptrs("b1_i", b1_i, wide, td, dev) if b1_i is not None else None
-        b3 = _ptrs("b3_i", b3_i, wide, td, dev) if b3_i is not None and self.swiglu else None
+        x, w1, w3, w2 = self._ckpt8_args(X, W1_i, W2_i, W3_i)
+        b1 = _ptrs("b1_i", b1_i, self._wide, td, dev) if b1_i is not None else None
+        b3 = _ptrs("b3_i", b3_i, self._wide, td, dev) if b3_i is not None and self.swiglu else None
         b2 = _ptr("b2", b2, (p.d,), td, dev) if b2 is not None else None
-        sizes = self.ckpt8_sizes()
         with _on(dev, stream):
             if out is None:
                 Y = X.new_empty((p.T, p.d))
-                ckpt = [X.new_empty(n, dtype=torch.uint8) for n in sizes]
+                ckpt = [X.new_empty(n, dtype=torch.uint8) for n in self._ckpt8]
                 y, c = Y.data_ptr(), (ctypes.c_void_p * len(ckpt))(*[x.data_ptr() for x in ckpt])
             else:
                 Y, ckpt = out
                 y = _ptr("Y", Y, (p.T, p.d), td, dev)
-                c = _ptrs("ckpt", ckpt, [(n,) for n in sizes], torch.uint8, dev)
-            scratch, H = _pieces([p.T * w * X.element_size() for w in p.d_i], dev)
+                c = _ptrs("ckpt", ckpt, self._ckpt8, torch.uint8, dev)
+            scratch, H = _pieces(self._act_bytes, dev)
             tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, y, c, H, self.workspace.data_ptr(), _current(dev))
         return Y, ckpt
 
@@ -750,10 +752,10 @@ class ShardedMLP:
         (dX, dW1, dW3, dW2) to write to (dW3: None for GeLU)."""
         import torch
         p, td, dev = self.plan, self.tdtype, self.workspace.device
-        x, w1, w3, w2, col, row = self._ckpt8_args(X, W1_i, W2_i, W3_i)
+        x, w1, w3, w2 = self._ckpt8_args(X, W1_i, W2_i, W3_i)
         dy = _ptr("dY", dY, (p.T, p.d), td, dev)
-        c = _ptrs("ckpt", ckpt, [(n,) for n in self.ckpt8_sizes()], torch.uint8, dev)
-        es = X.element_size()
+        c = _ptrs("ckpt", ckpt, self._ckpt8, torch.uint8, dev)
+        col, row = self._col, self._row
         with _on(dev, stream):
             if out is None:
                 dX = X.new_empty((p.T, p.d))
@@ -768,11 +770,10 @@ class ShardedMLP:
             db = (None, None, None)
             if bias_grads:
                 db2 = X.new_empty(p.d)
-                db1, to1 = _new_list(X, p.d_i)
-                db3, to3 = _new_list(X, p.d_i) if self.swiglu else (None, None)
+                db1, to1 = _new_list(X, self._wide)
+                db3, to3 = _new_list(X, self._wide) if self.swiglu else (None, None)
                 db = to1, to3, db2.data_ptr()
-            wide = [p.T * w * es for w in p.d_i]
-            scratch, at = _pieces(wide * (3 if self.swiglu else 2), dev)  # H_i, then dact
+            scratch, at = _pieces(self._act_bytes * (3 if self.swiglu else 2), dev)  # H_i, then dact
             tpmlp_backward_ckpt8(p, x, w1, w3, w2, c, at[:p.t], dy, at[p.t:], *to, *db, self.workspace.data_ptr(),
                                  _current(dev))
         return {"dX": dX, "dW1": dW1, "dW3": dW3, "dW2": dW2, "db1": db1, "db3": db3, "db2": db2}
@@ -820,6 +821,9 @@ class ShardedAttentionProj:
         self.device = torch.device(device or "cuda")
         self.tdtype = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
         self.workspace = torch.zeros(tpmlp_workspace_size(self.plan), dtype=torch.uint8, device=self.device)
+        p = self.plan  # shapes of QKV_i, [Q_i | K_i] and V_i
+        self._fused, self._v = [(p.T, n) for n in p.d_i], [(p.T, k) for k in p.dkv_i]
+        self._qk = [(p.T, q + k) for q, k in zip(p.dq_i, p.dkv_i)]
 
     def _empty(self, *shape):
         import torch
@@ -865,7 +869,7 @@ class ShardedAttentionProj:
         if not D:
             raise ValueError("the heads are not described (set_qk_norm_rope)")
         import torch
-        return (_ptrs("QKV_i", QKV_i, [(p.T, n) for n in p.d_i], td, dev),
+        return (_ptrs("QKV_i", QKV_i, self._fused, td, dev),
                 _ptr("positions", positions, (p.T,), torch.int64, dev) if positions is not None else None,
                 _ptr("gq", gq, (D,), td, dev) if gq is not None else None,
                 _ptr("gk", gk, (D,), td, dev) if gk is not None else None)
@@ -875,8 +879,7 @@ class ShardedAttentionProj:
         p = self.plan
         if len(xs) != p.t:
             raise ValueError(f"{name}: expected {p.t} tensors, got {len(xs)}")
-        shapes = [(p.T, n if p.T and x.data_ptr() == f else q + k)
-                  for x, f, n, q, k in zip(xs, fused, p.d_i, p.dq_i, p.dkv_i)]
+        shapes = [n if p.T and x.data_ptr() == f else qk for x, f, n, qk in zip(xs, fused, self._fused, self._qk)]
         return _ptrs(name, xs, shapes, self.tdtype, self.workspace.device)
 
     def qk_norm_rope_forward(self, QKV_i, positions=None, gq=None, gk=None, out=None, stream=None):
@@ -886,7 +889,7 @@ class ShardedAttentionProj:
         qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk)
         with _on(self.workspace.device, stream):
             if out is None:
-                out, to = _new_list(QKV_i[0], [(p.T, q_ + k_) for q_, k_ in zip(p.dq_i, p.dkv_i)])
+                out, to = _new_list(QKV_i[0], self._qk)
             else:
                 to = self._in_place_or_dense("out", out, qkv)
             tpmlp_attn_qk_norm_rope_forward(p, qkv, pos, q, k, to, _current(self.workspace.device))
@@ -899,16 +902,16 @@ class ShardedAttentionProj:
         gain_grads: whether to compute dgq and dgk (None: if a gain is given)."""
         p, td, dev = self.plan, self.tdtype, self.workspace.device
         qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk)
-        dv = _ptrs("dV_i", dV_i, [(p.T, w) for w in p.dkv_i], td, dev) if dV_i is not None else None
+        dv = _ptrs("dV_i", dV_i, self._v, td, dev) if dV_i is not None else None
         if dV_i is None and out is None:
             raise ValueError("dV_i, or dQKV_i that hold dV already (out), must be given")
         if gain_grads is None:
             gain_grads = gq is not None or gk is not None
         with _on(dev, stream):
             if out is None:
-                out, dqkv = _new_list(QKV_i[0], [(p.T, n) for n in p.d_i])
+                out, dqkv = _new_list(QKV_i[0], self._fused)
             else:
-                dqkv = _ptrs("out", out, [(p.T, n) for n in p.d_i], td, dev)
+                dqkv = _ptrs("out", out, self._fused, td, dev)
             dgq = dgk = None
             if gain_grads:
                 dgq, dgk = QKV_i[0].new_empty(p.head_dim), QKV_i[0].new_empty(p.head_dim)
