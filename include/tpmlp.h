@@ -336,7 +336,8 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * included; its error in turns is at most |p f_j| 2^-53 + 2^-25.
  * Backward, from dy: w = dy rotated back, n = x r, s = w g:
  *   dx = r (s - n mean(s n)),   dg = sum over tokens, shards and heads of w n
- * (norm = 0: dx = w).  x is the QKV buffer as the projection wrote it: keep it.
+ * (norm = 0: dx = w).  x is the QKV buffer as the projection wrote it: keep it
+ * (norm = 0: it is not read, QKV may be NULL in the backward call).
  * A head with a NaN or an infinity spoils itself and the gain's gradient only;
  * so does one whose sum of squares passes the fp32 range (elements above about
  * 10^18).

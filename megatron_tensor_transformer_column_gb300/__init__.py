@@ -862,14 +862,14 @@ class ShardedAttentionProj:
         if n > self.workspace.numel():
             self.workspace = torch.zeros(n, dtype=torch.uint8, device=self.workspace.device)
 
-    def _qk_args(self, QKV_i, positions, gq, gk):
+    def _qk_args(self, QKV_i, positions, gq, gk, may_lack_x=False):
         """Checked addresses of the inputs that both passes share."""
         p, td, dev = self.plan, self.tdtype, self.workspace.device
         D = getattr(p, "head_dim", 0)
         if not D:
             raise ValueError("the heads are not described (set_qk_norm_rope)")
         import torch
-        return (_ptrs("QKV_i", QKV_i, self._fused, td, dev),
+        return (_ptrs("QKV_i", QKV_i, self._fused, td, dev) if QKV_i is not None or not may_lack_x else None,
                 _ptr("positions", positions, (p.T,), torch.int64, dev) if positions is not None else None,
                 _ptr("gq", gq, (D,), td, dev) if gq is not None else None,
                 _ptr("gk", gk, (D,), td, dev) if gk is not None else None)
@@ -899,22 +899,24 @@ class ShardedAttentionProj:
                               gain_grads=None):
         """(dQKV_i, dgq, dgk) from the core's [dQ_i | dK_i] and, optionally, dV_i [T, dkv_i].  out: the dQKV_i to
         write to; their value columns stay as they are without dV_i.  dQK_i may be those tensors themselves.
-        gain_grads: whether to compute dgq and dgk (None: if a gain is given)."""
+        gain_grads: whether to compute dgq and dgk (None: if a gain is given).  Without a norm QKV_i is not read and may
+        be None."""
         p, td, dev = self.plan, self.tdtype, self.workspace.device
-        qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk)
+        qkv, pos, q, k = self._qk_args(QKV_i, positions, gq, gk, may_lack_x=not getattr(p, "qk_norm", True))
         dv = _ptrs("dV_i", dV_i, self._v, td, dev) if dV_i is not None else None
         if dV_i is None and out is None:
             raise ValueError("dV_i, or dQKV_i that hold dV already (out), must be given")
         if gain_grads is None:
             gain_grads = gq is not None or gk is not None
         with _on(dev, stream):
+            like = QKV_i[0] if QKV_i is not None else self.workspace.new_empty(0, dtype=td)
             if out is None:
-                out, dqkv = _new_list(QKV_i[0], self._fused)
+                out, dqkv = _new_list(like, self._fused)
             else:
                 dqkv = _ptrs("out", out, self._fused, td, dev)
             dgq = dgk = None
             if gain_grads:
-                dgq, dgk = QKV_i[0].new_empty(p.head_dim), QKV_i[0].new_empty(p.head_dim)
+                dgq, dgk = like.new_empty(p.head_dim), like.new_empty(p.head_dim)
             tpmlp_attn_qk_norm_rope_backward(p, qkv, pos, q, k, self._in_place_or_dense("dQK_i", dQK_i, dqkv), dv,
                                              dqkv, dgq, dgk, self.workspace, _current(dev))
         return out, dgq, dgk

@@ -10,6 +10,8 @@
 //   elements past R are stored as u.  A pair is (j, j + R/2) or (2j, 2j + 1).
 // Backward, from dy: w = dy rotated back, n = x r, s = w g:
 //   dx = r (s - n mean(s n)),  dg = sum over tokens and heads of w n.
+// Without a norm dx = w: that is the forward pass of dy with the angles
+// negated, and the forward kernel runs it (x is not read).
 //
 // The angle.  f_j is held as a 64-bit fraction of a turn, F_j = 2^64 f_j / 2 pi,
 // and p F_j is taken modulo 2^64, which drops whole turns exactly; the top 32
@@ -611,12 +613,9 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
       mul_v<V>(wb[i], c2[i], sb);
       sx += dot_v<V>(sa, a[i], sb, b[i]);
     }
-    float r = 1.0f, m = 0.0f;
-    if (p.norm) {
-      group_sum<true>(ss, sx, n, li, leader);
-      r = rsqrtf(fmaf(ss, inv_d, p.eps));
-      m = -(r * (sx * inv_d));  // - mean(s n)
-    }
+    group_sum<true>(ss, sx, n, li, leader);
+    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    const float m = -(r * (sx * inv_d));  // - mean(s n)
     E* out = reinterpret_cast<E*>(row_of(H.out, run.tok, H.ldo));
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
@@ -644,7 +643,7 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
         float c, s;
         sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
         cosines[j] = c;
-        sines[j] = s;
+        sines[j] = kBwd ? s : s * p.turn;
       }
       pos = position(run.tok + rows);
       __syncwarp();
@@ -747,7 +746,7 @@ template <typename E, int V, int NU, bool kPairs, bool kBwd>
 __device__ __forceinline__ void qk_body(const QkParams& p) {
   extern __shared__ __align__(16) uint8_t qk_smem[];
   const int cta = blockIdx.x, warp = threadIdx.x >> 5;
-  if (kBwd && p.values) copy_values<E>(p, cta * kWarps + warp, gridDim.x * kWarps);
+  if (p.values) copy_values<E>(p, cta * kWarps + warp, gridDim.x * kWarps);
   const int kind = cta < p.cta_end[0] ? 0 : 1;
   const int c0 = kind ? p.cta_end[0] : 0;
   qk_kind<E, V, NU, kPairs, kBwd>(p, kind, (cta - c0) * kWarps + warp, (p.cta_end[kind] - c0) * kWarps, qk_smem);

@@ -1235,15 +1235,16 @@ tpmlp_status check_overlap(const char* na, int i, const void* a, int64_t bytes_a
   return fail(TPMLP_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", na, i, nb, j);
 }
 
-// The checks both passes share, before any device query.
+// The checks both passes share, before any device query.  backward: without a
+// norm it has no use for QKV, which may be NULL then.
 tpmlp_status qk_checks(const tpmlp_plan* pl, const void* const* QKV, const int64_t* positions, const void* gq,
-                       const void* gk) {
+                       const void* gk, bool backward) {
   g_last_error[0] = 0;
   if (!pl) return fail(TPMLP_ERR_INVALID_ARG, "plan is NULL");
   TPMLP_TRY(check_kind(pl, PLAN_ATTN));
   if (!pl->head_dim)
     return fail(TPMLP_ERR_INVALID_ARG, "the heads are not described (tpmlp_attn_plan_set_qk_norm_rope)");
-  TPMLP_TRY(check_array("QKV", QKV, pl->t, pl->T == 0));
+  if (QKV || !backward || pl->qk_norm) TPMLP_TRY(check_array("QKV", QKV, pl->t, pl->T == 0));
   if (reinterpret_cast<uintptr_t>(positions) & 7u)
     return fail(TPMLP_ERR_ALIGNMENT, "positions (%p) is not 8-byte aligned", static_cast<const void*>(positions));
   TPMLP_TRY(check_ptr("gq", gq, true));
@@ -1263,6 +1264,7 @@ QkParams qk_params(const tpmlp_plan* pl, const int64_t* positions, const void* g
   p.R = pl->rotary_dim;
   p.norm = pl->qk_norm;
   p.eps = pl->qk_eps;
+  p.turn = 1.0f;
   p.pos = positions;
   p.gain[0] = gq;
   p.gain[1] = gk;
@@ -1757,7 +1759,7 @@ tpmlp_status tpmlp_attn_qk_norm_rope_forward(const tpmlp_plan* plan, const void*
                                              const void* gq, const void* gk, void* const* QK,
                                              tpmlp_stream_t stream) {
   g_last_launches = 0;
-  TPMLP_TRY(qk_checks(plan, QKV, positions, gq, gk));
+  TPMLP_TRY(qk_checks(plan, QKV, positions, gq, gk, /*backward=*/false));
   TPMLP_TRY(check_array("QK", QK, plan->t, plan->T == 0));
   if (plan->T == 0) return TPMLP_OK;
   QkParams p = qk_params(plan, positions, gq, gk);
@@ -1788,7 +1790,7 @@ tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void
                                               const void* const* dQK, const void* const* dV, void* const* dQKV,
                                               void* dgq, void* dgk, void* workspace, tpmlp_stream_t stream) {
   g_last_launches = 0;
-  TPMLP_TRY(qk_checks(plan, QKV, positions, gq, gk));
+  TPMLP_TRY(qk_checks(plan, QKV, positions, gq, gk, /*backward=*/true));
   const bool tz = plan->T == 0;
   TPMLP_TRY(check_array("dQK", dQK, plan->t, tz));
   if (dV) TPMLP_TRY(check_array("dV", dV, plan->t, tz));
@@ -1819,17 +1821,23 @@ tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void
     const bool in_place = dQK[i] == dQKV[i];
     for (int j = 0; j < plan->t; ++j) {
       const int64_t qk = plan->T * (plan->dq_i[j] + plan->dkv_i[j]) * es, v = plan->T * plan->dkv_i[j] * es;
-      TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "QKV", j, QKV[j], plan->T * plan->d_i[j] * es));
+      if (QKV) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "QKV", j, QKV[j], plan->T * plan->d_i[j] * es));
       if (!(in_place && j == i)) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dQK", j, dQK[j], qk));
       if (dV) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dV", j, dV[j], v));
       if (j < i) TPMLP_TRY(check_overlap("dQKV", i, dQKV[i], n, "dQKV", j, dQKV[j], plan->T * plan->d_i[j] * es));
     }
     QkShard& S = p.shards[i];
-    S.x = QKV[i];
-    S.dy = dQK[i];
     S.dv = dV ? dV[i] : nullptr;
     S.out = dQKV[i];
-    S.lddy = in_place ? plan->d_i[i] : plan->dq_i[i] + plan->dkv_i[i];
+    const int64_t lddy = in_place ? plan->d_i[i] : plan->dq_i[i] + plan->dkv_i[i];
+    if (plan->qk_norm) {
+      S.x = QKV[i];
+      S.dy = dQK[i];
+      S.lddy = lddy;
+    } else {
+      S.x = dQK[i];
+      S.ldx = lddy;
+    }
     S.ldo = plan->d_i[i];
     if (dV) p.values += plan->dkv_i[i];
   }
@@ -1838,7 +1846,8 @@ tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void
                                          (plan->dtype == TPMLP_BF16 ? kSkSlotsOffset : kStatusBytes));
   TPMLP_TRY(device_info(&di));
   const bool bf16 = plan->dtype == TPMLP_BF16;
-  cudaError_t e = launch_qk_norm_rope(p, bf16, plan->rope_pairs, true, di.sms, st);
+  if (!plan->qk_norm) p.turn = -1.0f;
+  cudaError_t e = launch_qk_norm_rope(p, bf16, plan->rope_pairs, plan->qk_norm != 0, di.sms, st);
   if (e != cudaSuccess) return cuda_fail(e);
   ++g_last_launches;
   if (gains) {

@@ -299,6 +299,7 @@ struct QkParams {
   int64_t T, values;                  // tokens; value columns to copy
   int32_t t, D, R, norm;
   float eps;
+  float turn;                         // 1, or -1: rotated back by the forward kernel
   int32_t heads[2];
   int32_t lanes, groups, parts[2], cta_end[2];  // set by the launcher
 };

@@ -1,0 +1,48 @@
+"""Calls of the head norm with rotation and of the 8-bit checkpoints that need no GPU: what is accepted, what is
+refused, and what the Python layer keeps."""
+import pytest
+import torch
+
+import megatron_tensor_transformer_column_gb300 as tp
+
+A = 1 << 24  # addresses that are never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from megatron_tensor_transformer_column_gb300 import _build
+    _build.build()
+    return tp.load()
+
+
+def status_of(call):
+    with pytest.raises(tp.TpmlpError) as e:
+        call()
+    return e.value.status
+
+
+def heads_plan(T, norm=True, dtype="bf16"):
+    p = tp.AttnPlan(T, 64, [128, 64], [64, 64], dtype)
+    tp.tpmlp_attn_plan_set_qk_norm_rope(p, 64, norm=norm)
+    return p
+
+
+def test_backward_of_the_rotation_alone_takes_no_x(lib):
+    """QKV may be missing in the backward call without a norm, and in no other (no tokens: nothing is launched)."""
+    n = [None, None]
+    tp.tpmlp_attn_qk_norm_rope_backward(heads_plan(0, False), None, None, None, None, n, n, n, None, None, None, stream=0)
+    assert status_of(lambda: tp.tpmlp_attn_qk_norm_rope_backward(heads_plan(0), None, None, None, None, n, n, n, None,
+                                                                 None, None, stream=0)) == 1
+    assert status_of(lambda: tp.tpmlp_attn_qk_norm_rope_forward(heads_plan(0, False), None, None, None, None, n,
+                                                                stream=0)) == 1
+    # what is given is still looked at
+    far = [A + (i << 22) for i in range(8)]
+    p = heads_plan(16, False)
+    call = lambda **kw: tp.tpmlp_attn_qk_norm_rope_backward(
+        p, *{**dict(QKV=None, pos=None, gq=None, gk=None, dQK=far[:2], dV=far[2:4], dQKV=far[4:6], dgq=None, dgk=None,
+                    workspace=None), **kw}.values(), stream=0)
+    assert status_of(lambda: call(QKV=[far[6], None])) == 1
+    assert status_of(lambda: call(QKV=[far[6], far[4]])) == 1       # over an output
+    assert status_of(lambda: call(QKV=[far[6] + 8, far[7]])) == 3
+    assert status_of(lambda: call(dQK=[far[0], far[4]])) == 1       # another shard's output
+    assert status_of(lambda: call(dQK=[far[0], None])) == 1
