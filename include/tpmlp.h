@@ -340,7 +340,7 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * (norm = 0: it is not read, QKV may be NULL in the backward call).
  * A head with a NaN or an infinity spoils itself and the gain's gradient only;
  * so does one whose sum of squares passes the fp32 range (elements above about
- * 10^18).
+ * 10^18).  Without a norm it spoils its pair only, or itself from rotary_dim on.
  *
  * tpmlp_attn_plan_set_qk_norm_rope describes the heads (copied into the plan,
  * inv_freq included; may not run while another call uses the plan).  Every

@@ -11,7 +11,7 @@
 // Backward, from dy: w = dy rotated back, n = x r, s = w g:
 //   dx = r (s - n mean(s n)),  dg = sum over tokens and heads of w n.
 // Without a norm dx = w: that is the forward pass of dy with the angles
-// negated, and the forward kernel runs it (x is not read).
+// negated, and the kernel without a norm runs both (x is not read).
 //
 // The angle.  f_j is held as a 64-bit fraction of a turn, F_j = 2^64 f_j / 2 pi,
 // and p F_j is taken modulo 2^64, which drops whole turns exactly; the top 32
@@ -299,6 +299,13 @@ __device__ __forceinline__ void read_pairs(const float* table, int u, int D, flo
   }
 }
 
+// The pair in that table of element k of unit u's a's and b's.
+template <int V, bool kPairs>
+__device__ __forceinline__ int pair_at(int u, int k, int D) {
+  if (kPairs && V > 1) return V / 2 * u + (k < V / 2 ? k : D / 4 + k - V / 2);
+  return V * u + k;
+}
+
 // The sums of s (and t) over the n lanes of a group, to all of them (the same
 // bits): a tree to the group's first lane and back for an n that is no power of
 // two.  n is the same for the whole warp.
@@ -400,8 +407,13 @@ __device__ __forceinline__ void cursor_next(Cursor& c, int first, int step, int 
   }
 }
 
-template <typename E, int V, int NU, bool kPairs, bool kBwd>
+// What a kernel computes.  Without a norm it is a kernel of its own: as a branch
+// of the normed one it took that from 92 to 103 registers, a CTA less an SM.
+enum Pass { kNormFwd, kNormBwd, kRotate };
+
+template <typename E, int V, int NU, bool kPairs, Pass kPass>
 __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int nw, uint8_t* smem) {
+  constexpr bool kBwd = kPass == kNormBwd, kNorm = kPass != kRotate;
   constexpr int kVecBytes = V * int(sizeof(E));
   constexpr int kQueueBytes = queue_bytes(V, sizeof(E), kBwd);
   constexpr int kUnitVecs = kBwd ? 4 : 2;          // a unit's vectors in the queue
@@ -411,7 +423,6 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
   const int n = p.lanes, G = p.groups;  // lanes of a head, heads of a round
   const int grp = lane / n, li = lane - grp * n, leader = grp * n;
   const int units = p.D / (2 * V), heads = p.heads[kind], parts = p.parts[kind];
-  const float inv_d = 1.0f / static_cast<float>(p.D);
   const uint32_t T = static_cast<uint32_t>(p.T);
   const Place at = place(max(p.heads[0], p.heads[1]), p.D, kQueueBytes, kBwd);
   Head<kBwd>* head = reinterpret_cast<Head<kBwd>*>(smem);
@@ -517,8 +528,8 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
   };
   uint64_t pos = position(run.tok);
 
-  // Forward: the coefficients of a and b in a' and b'; backward: the cosines,
-  // sines and gains.
+  // Forward: the coefficients of a and b in a' and b'; else the cosines and
+  // sines (c3, c4) and, backward, the gains.
   float c1[NU][V], c2[NU][V], c3[NU][V], c4[NU][V];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
@@ -532,6 +543,15 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
   auto queued = [&](int slot, int i) {
     return reinterpret_cast<const E*>(smem + at.queue + warp * kQueueBytes +
                                       (slot * kRoundVecs + i * kUnitVecs) * 32 * kVecBytes + lane * kVecBytes);
+  };
+
+  // Past R the partner's part is nothing, not 0 times the partner, which is a NaN if that is infinite.  (With a norm an
+  // infinity spoils the whole head.)
+  auto drop_unrotated = [&](int i, float (&t)[V]) {
+    if (p.R == p.D) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (pair_at<V, kPairs>(un[i], k, p.D) >= p.R / 2) t[k] = 0.0f;
   };
 
   auto forward_head = [&](const Cursor& run, int slot) {
@@ -554,23 +574,33 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
           load_unit<E, V, kPairs>(x + o1[i], x + o2[i], a[i], b[i]);
         }
       }
-      ss += dot_v<V>(a[i], a[i], b[i], b[i]);
+      if constexpr (kNorm) ss += dot_v<V>(a[i], a[i], b[i], b[i]);
     }
     float r = 1.0f, none = 0.0f;
-    if (p.norm) {
+    if constexpr (kNorm) {
       group_sum<false>(ss, none, n, li, leader);
-      r = rsqrtf(fmaf(ss, inv_d, p.eps));
+      r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
     }
     E* out = reinterpret_cast<E*>(row_of(H.out, run.tok, H.ldo));
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       float oa[V], ob[V], t[V];
-      mul_v<V>(b[i], c2[i], t);
-      fma_v<V>(a[i], c1[i], t, oa);
-      mul_v<V>(a[i], c4[i], t);
-      fma_v<V>(b[i], c3[i], t, ob);
-      scale_v<V>(oa, r, oa);
-      scale_v<V>(ob, r, ob);
+      if constexpr (kNorm) {
+        mul_v<V>(b[i], c2[i], t);
+        fma_v<V>(a[i], c1[i], t, oa);
+        mul_v<V>(a[i], c4[i], t);
+        fma_v<V>(b[i], c3[i], t, ob);
+        scale_v<V>(oa, r, oa);
+        scale_v<V>(ob, r, ob);
+      } else {
+        mul_v<V>(b[i], c4[i], t);
+        scale_v<V>(t, -1.0f, t);
+        drop_unrotated(i, t);
+        fma_v<V>(a[i], c3[i], t, oa);
+        mul_v<V>(a[i], c4[i], t);
+        drop_unrotated(i, t);
+        fma_v<V>(b[i], c3[i], t, ob);
+      }
       if (ok && on[i]) store_unit<E, V, kPairs>(out, o1[i], o2[i], oa, ob);
     }
   };
@@ -614,8 +644,8 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
       sx += dot_v<V>(sa, a[i], sb, b[i]);
     }
     group_sum<true>(ss, sx, n, li, leader);
-    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-    const float m = -(r * (sx * inv_d));  // - mean(s n)
+    const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+    const float m = -(r * (sx * p.inv_d));  // - mean(s n)
     E* out = reinterpret_cast<E*>(row_of(H.out, run.tok, H.ldo));
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
@@ -643,13 +673,13 @@ __device__ __forceinline__ void qk_kind(const QkParams& p, int kind, int w, int 
         float c, s;
         sincospif(static_cast<float>(turn) * 0x1p-31f, &s, &c);
         cosines[j] = c;
-        sines[j] = kBwd ? s : s * p.turn;
+        sines[j] = kNorm ? s : s * p.turn;
       }
       pos = position(run.tok + rows);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
-        if (kBwd) {
+        if (kPass != kNormFwd) {
           read_pairs<V, kPairs>(cosines, un[i], p.D, c3[i]);
           read_pairs<V, kPairs>(sines, un[i], p.D, c4[i]);
         } else {
@@ -742,24 +772,29 @@ __device__ __forceinline__ void copy_values(const QkParams& p, int w, int nw) {
   }
 }
 
-template <typename E, int V, int NU, bool kPairs, bool kBwd>
+template <typename E, int V, int NU, bool kPairs, Pass kPass>
 __device__ __forceinline__ void qk_body(const QkParams& p) {
   extern __shared__ __align__(16) uint8_t qk_smem[];
   const int cta = blockIdx.x, warp = threadIdx.x >> 5;
-  if (p.values) copy_values<E>(p, cta * kWarps + warp, gridDim.x * kWarps);
+  if (kPass != kNormFwd && p.values) copy_values<E>(p, cta * kWarps + warp, gridDim.x * kWarps);
   const int kind = cta < p.cta_end[0] ? 0 : 1;
   const int c0 = kind ? p.cta_end[0] : 0;
-  qk_kind<E, V, NU, kPairs, kBwd>(p, kind, (cta - c0) * kWarps + warp, (p.cta_end[kind] - c0) * kWarps, qk_smem);
+  qk_kind<E, V, NU, kPairs, kPass>(p, kind, (cta - c0) * kWarps + warp, (p.cta_end[kind] - c0) * kWarps, qk_smem);
 }
 
 template <typename E, int V, int NU, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) tpmlp_attn_qk_norm_rope_fwd(const __grid_constant__ QkParams p) {
-  qk_body<E, V, NU, kPairs, false>(p);
+  qk_body<E, V, NU, kPairs, kNormFwd>(p);
+}
+
+template <typename E, int V, int NU, bool kPairs>
+__global__ void __launch_bounds__(kThreads, 4) tpmlp_attn_qk_rope(const __grid_constant__ QkParams p) {
+  qk_body<E, V, NU, kPairs, kRotate>(p);
 }
 
 template <typename E, int V, int NU, bool kPairs>
 __global__ void __launch_bounds__(kThreads, 4) tpmlp_attn_qk_norm_rope_bwd(const __grid_constant__ QkParams p) {
-  qk_body<E, V, NU, kPairs, true>(p);
+  qk_body<E, V, NU, kPairs, kNormBwd>(p);
 }
 
 // dg of one kind (blockIdx.y) for 32 elements: the CTAs' sums added in a
@@ -789,9 +824,11 @@ __global__ void __launch_bounds__(1024) tpmlp_attn_qk_gain_grad(const float* par
 using QkKernel = void (*)(QkParams);
 
 template <typename E, int V>
-QkKernel pick(bool pairs, bool bwd) {
+QkKernel pick(bool pairs, Pass pass) {
   constexpr int NU = units_of_lane(V);
-  if (bwd) return pairs ? tpmlp_attn_qk_norm_rope_bwd<E, V, NU, true> : tpmlp_attn_qk_norm_rope_bwd<E, V, NU, false>;
+  if (pass == kRotate) return pairs ? tpmlp_attn_qk_rope<E, V, NU, true> : tpmlp_attn_qk_rope<E, V, NU, false>;
+  if (pass == kNormBwd)
+    return pairs ? tpmlp_attn_qk_norm_rope_bwd<E, V, NU, true> : tpmlp_attn_qk_norm_rope_bwd<E, V, NU, false>;
   return pairs ? tpmlp_attn_qk_norm_rope_fwd<E, V, NU, true> : tpmlp_attn_qk_norm_rope_fwd<E, V, NU, false>;
 }
 
@@ -805,16 +842,16 @@ int vector_width(bool bf16, int D, int R, bool pairs) {
   return 1;
 }
 
-QkKernel kernel_for(bool bf16, int V, bool pairs, bool bwd) {
+QkKernel kernel_for(bool bf16, int V, bool pairs, Pass pass) {
   if (bf16) {
-    if (V == 8) return pick<__nv_bfloat16, 8>(pairs, bwd);
-    if (V == 4) return pick<__nv_bfloat16, 4>(pairs, bwd);
-    if (V == 2) return pick<__nv_bfloat16, 2>(pairs, bwd);
-    return pick<__nv_bfloat16, 1>(pairs, bwd);
+    if (V == 8) return pick<__nv_bfloat16, 8>(pairs, pass);
+    if (V == 4) return pick<__nv_bfloat16, 4>(pairs, pass);
+    if (V == 2) return pick<__nv_bfloat16, 2>(pairs, pass);
+    return pick<__nv_bfloat16, 1>(pairs, pass);
   }
-  if (V == 4) return pick<float, 4>(pairs, bwd);
-  if (V == 2) return pick<float, 2>(pairs, bwd);
-  return pick<float, 1>(pairs, bwd);
+  if (V == 4) return pick<float, 4>(pairs, pass);
+  if (V == 2) return pick<float, 2>(pairs, pass);
+  return pick<float, 1>(pairs, pass);
 }
 
 }  // namespace
@@ -831,14 +868,16 @@ cudaError_t launch_qk_norm_rope(QkParams& p, bool bf16, bool pairs, bool bwd, in
   p.lanes = std::min(units, 32);
   p.groups = 32 / p.lanes;
   const int G = p.groups;
-  const QkKernel k = kernel_for(bf16, V, pairs, bwd);
-  int bytes = place(std::max(p.heads[0], p.heads[1]), p.D, queue_bytes(V, bf16 ? 2 : 4, bwd), bwd).total;
-  if (bwd) bytes = std::max(bytes, kWarps * G * p.D * 4);  // the sums of the gain's gradient
+  const Pass pass = !p.norm ? kRotate : bwd ? kNormBwd : kNormFwd;
+  const bool sums = pass == kNormBwd;  // of the gain's gradient
+  const QkKernel k = kernel_for(bf16, V, pairs, pass);
+  int bytes = place(std::max(p.heads[0], p.heads[1]), p.D, queue_bytes(V, bf16 ? 2 : 4, sums), sums).total;
+  if (sums) bytes = std::max(bytes, kWarps * G * p.D * 4);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
   // CTAs that an SM holds: by registers (asked once per kernel) and by shared memory.
-  static std::atomic<int> by_registers[2][9][2][2];
-  std::atomic<int>& known = by_registers[bf16][V][pairs][bwd];
+  static std::atomic<int> by_registers[2][9][2][3];
+  std::atomic<int>& known = by_registers[bf16][V][pairs][pass];
   int per_sm = known.load(std::memory_order_relaxed);
   if (per_sm == 0) {
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, kThreads, 0);

@@ -1264,6 +1264,7 @@ QkParams qk_params(const tpmlp_plan* pl, const int64_t* positions, const void* g
   p.R = pl->rotary_dim;
   p.norm = pl->qk_norm;
   p.eps = pl->qk_eps;
+  p.inv_d = 1.0f / static_cast<float>(p.D);
   p.turn = 1.0f;
   p.pos = positions;
   p.gain[0] = gq;
@@ -1847,7 +1848,7 @@ tpmlp_status tpmlp_attn_qk_norm_rope_backward(const tpmlp_plan* plan, const void
   TPMLP_TRY(device_info(&di));
   const bool bf16 = plan->dtype == TPMLP_BF16;
   if (!plan->qk_norm) p.turn = -1.0f;
-  cudaError_t e = launch_qk_norm_rope(p, bf16, plan->rope_pairs, plan->qk_norm != 0, di.sms, st);
+  cudaError_t e = launch_qk_norm_rope(p, bf16, plan->rope_pairs, true, di.sms, st);
   if (e != cudaSuccess) return cuda_fail(e);
   ++g_last_launches;
   if (gains) {

@@ -298,8 +298,8 @@ struct QkParams {
   float* partial;                     // [CTAs x D] sums of the gain's gradient (backward), or null
   int64_t T, values;                  // tokens; value columns to copy
   int32_t t, D, R, norm;
-  float eps;
-  float turn;                         // 1, or -1: rotated back by the forward kernel
+  float eps, inv_d;                   // inv_d: 1 / D
+  float turn;                         // without a norm: 1, or -1 to rotate back
   int32_t heads[2];
   int32_t lanes, groups, parts[2], cta_end[2];  // set by the launcher
 };
