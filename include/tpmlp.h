@@ -331,9 +331,10 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * and the elements from rotary_dim on are u.  The partners (a, b) of pair j are
  * the elements (j, j + rotary_dim / 2) (TPMLP_ROPE_HALVES) or (2j, 2j + 1)
  * (TPMLP_ROPE_PAIRS); f_j = base^(-2j / rotary_dim), or inv_freq[j].  All in
- * fp32, rounded once to the plan's dtype.  The angle is p f_j taken modulo a
- * turn exactly, with f_j to 53 bits, for any 64-bit position, negative ones
- * included; its error in turns is at most |p f_j| 2^-53 + 2^-25.
+ * fp32, rounded once to the plan's dtype.  The angle is p f_j (f_j a double)
+ * taken modulo a turn exactly, for any 64-bit position, negative ones
+ * included; its error in turns is at most |p f_j| 2^-53 + |p| 2^-65 + 2^-25:
+ * positions beyond about 2^40 cost accuracy whatever the frequency.
  * Backward, from dy: w = dy rotated back, n = x r, s = w g:
  *   dx = r (s - n mean(s n)),   dg = sum over tokens, shards and heads of w n
  * (norm = 0: dx = w).  x is the QKV buffer as the projection wrote it: keep it

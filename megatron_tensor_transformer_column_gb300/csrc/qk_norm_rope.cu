@@ -15,9 +15,10 @@
 //
 // The angle.  f_j is held as a 64-bit fraction of a turn, F_j = 2^64 f_j / 2 pi,
 // and p F_j is taken modulo 2^64, which drops whole turns exactly; the top 32
-// bits are the angle in units of 2^-32 turn.  Its error is the rounding of
-// F_j (below 2^-53 f_j) times p, as that of the product in 64-bit floating
-// point, without 64-bit floating-point instructions.
+// bits are the angle in units of 2^-32 turn.  Its error is that of F_j times p:
+// |p f_j| 2^-53 turns, as that of the product in 64-bit floating point, and
+// |p| 2^-65 for the fraction's last bit (2^-25 turns at p = 2^40), without
+// 64-bit floating-point instructions.
 //
 // Layout of the work.  HBM-bound: a head is read and written once.  A lane
 // holds a unit: V pairs, i.e. two vectors of V elements, both partners of each

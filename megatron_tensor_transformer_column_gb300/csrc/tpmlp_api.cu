@@ -1737,11 +1737,11 @@ tpmlp_status tpmlp_attn_plan_set_qk_norm_rope(tpmlp_plan* plan, const tpmlp_qk_d
   for (int j = 0; j < R / 2; ++j) {
     const double f = desc->inv_freq ? desc->inv_freq[j] : std::pow(desc->base, -2.0 * j / R);
     if (!std::isfinite(f)) return fail(TPMLP_ERR_INVALID_ARG, "inv_freq[%d] is not finite", j);
-    // The fraction of a turn per position; whole turns do not count.
-    const double turns = f / 6.283185307179586476925286766559;
-    double frac = turns - std::floor(turns);
-    if (!(frac < 1.0)) frac = 0.0;  // a tiny negative frequency, rounded up to a whole turn
-    freq[j] = static_cast<uint64_t>(std::ldexp(frac, 64));
+    // The fraction of a turn per position, to the nearest 2^-64; whole turns do not count.  Of a negative frequency that
+    // of its magnitude, negated modulo 2^64: 1 - frac would lose the digits of a small one.
+    const double turns = std::fabs(f) / 6.283185307179586476925286766559;
+    const uint64_t frac = static_cast<uint64_t>(std::nearbyint(std::ldexp(turns - std::floor(turns), 64)));
+    freq[j] = f < 0 ? 0 - frac : frac;
   }
   try {
     plan->rope_freq.assign(freq, freq + R / 2);
