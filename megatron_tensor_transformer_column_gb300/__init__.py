@@ -807,6 +807,10 @@ class ShardedMLP:
                 "db2": db2}
 
 
+# Partial sums of the gains' gradients in an fp32 plan's workspace at most: CTAs of a launch x head_dim.
+_GAIN_SUMS_BYTES = 4096 * 256 * 4
+
+
 class ShardedAttentionProj:
     """Attention plan + workspace + output allocation for one shape.
 
@@ -820,7 +824,10 @@ class ShardedAttentionProj:
         self.plan = AttnPlan(T, d, dq_i, dkv_i, dtype)
         self.device = torch.device(device or "cuda")
         self.tdtype = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
-        self.workspace = torch.zeros(tpmlp_workspace_size(self.plan), dtype=torch.uint8, device=self.device)
+        # Of the size that the largest head_dim asks for, so that set_qk_norm_rope never replaces it: kernels in flight
+        # and captured graphs keep its address.
+        n = tpmlp_workspace_size(self.plan)
+        self.workspace = torch.zeros(max(n, 256 + _GAIN_SUMS_BYTES), dtype=torch.uint8, device=self.device)
         p = self.plan  # shapes of QKV_i, [Q_i | K_i] and V_i
         self._fused, self._v = [(p.T, n) for n in p.d_i], [(p.T, k) for k in p.dkv_i]
         self._qk = [(p.T, q + k) for q, k in zip(p.dq_i, p.dkv_i)]
@@ -856,11 +863,7 @@ class ShardedAttentionProj:
     # ---- norm of the query and key heads with the position rotation
     def set_qk_norm_rope(self, head_dim, rotary_dim=None, layout="halves", norm=True, eps=1e-6, base=10000.0,
                          inv_freq=None):
-        import torch
         tpmlp_attn_plan_set_qk_norm_rope(self.plan, head_dim, rotary_dim, layout, norm, eps, base, inv_freq)
-        n = tpmlp_workspace_size(self.plan)
-        if n > self.workspace.numel():
-            self.workspace = torch.zeros(n, dtype=torch.uint8, device=self.workspace.device)
 
     def _qk_args(self, QKV_i, positions, gq, gk, may_lack_x=False):
         """Checked addresses of the inputs that both passes share."""

@@ -46,3 +46,13 @@ def test_backward_of_the_rotation_alone_takes_no_x(lib):
     assert status_of(lambda: call(QKV=[far[6] + 8, far[7]])) == 3
     assert status_of(lambda: call(dQK=[far[0], far[4]])) == 1       # another shard's output
     assert status_of(lambda: call(dQK=[far[0], None])) == 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_describing_the_heads_keeps_the_workspace(lib, dtype):
+    """Kernels in flight and captured graphs hold its address, and its status word."""
+    proj = tp.ShardedAttentionProj(16, 64, [256], [256], dtype, device="cpu")
+    ws, at = proj.workspace, proj.workspace.data_ptr()
+    for D in (2, 64, 256):
+        proj.set_qk_norm_rope(D)
+        assert proj.workspace is ws and ws.data_ptr() == at and ws.numel() >= tp.tpmlp_workspace_size(proj.plan)
