@@ -1000,16 +1000,21 @@ def _make_checkpoint_function():
 
 
 class _LazyFunction:
-    """An autograd function that is made, and torch imported, on its first use."""
+    """An autograd function that is made, and torch imported, on its first use.  What was made stays with the class, so
+    that a copy of the object, or one that was pickled, is as good as the object."""
 
-    def __init__(self, make=_make_function):
-        self._make, self._fn = make, None
+    _make, _fn = staticmethod(_make_function), None
 
     def __getattr__(self, name):
-        if self._fn is None:
-            self._fn = self._make()
-        return getattr(self._fn, name)
+        cls = type(self)
+        if cls._fn is None:
+            cls._fn = cls._make()
+        return getattr(cls._fn, name)
+
+
+class _LazyCheckpointFunction(_LazyFunction):
+    _make, _fn = staticmethod(_make_checkpoint_function), None
 
 
 TPMLPFunction = _LazyFunction()
-TPMLPCheckpointFunction = _LazyFunction(_make_checkpoint_function)
+TPMLPCheckpointFunction = _LazyCheckpointFunction()

@@ -1,7 +1,9 @@
 """Calls of the head norm with rotation and of the 8-bit checkpoints that need no GPU: what is accepted, what is
 refused, and what the Python layer keeps."""
+import copy
+import pickle
+
 import pytest
-import torch
 
 import megatron_tensor_transformer_column_gb300 as tp
 
@@ -56,3 +58,14 @@ def test_describing_the_heads_keeps_the_workspace(lib, dtype):
     for D in (2, 64, 256):
         proj.set_qk_norm_rope(D)
         assert proj.workspace is ws and ws.data_ptr() == at and ws.numel() >= tp.tpmlp_workspace_size(proj.plan)
+
+
+@pytest.mark.parametrize("name", ["TPMLPFunction", "TPMLPCheckpointFunction"])
+def test_autograd_functions_can_be_copied_and_pickled(name):
+    fn = getattr(tp, name)
+    for used in (False, True):
+        if used:
+            assert fn.__name__ == name
+        for other in (copy.copy(fn), copy.deepcopy(fn), copy.deepcopy([fn])[0], pickle.loads(pickle.dumps(fn))):
+            assert other.__name__ == name and other.apply == fn.apply
+    assert tp.TPMLPFunction.__name__ != tp.TPMLPCheckpointFunction.__name__
