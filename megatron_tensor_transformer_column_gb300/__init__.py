@@ -215,7 +215,7 @@ def _addr(x) -> Optional[int]:
 
 
 def _arr(xs) -> Optional[ctypes.Array]:
-    if xs is None or isinstance(xs, ctypes.Array):
+    if xs is None or (isinstance(xs, ctypes.Array) and xs._type_ is ctypes.c_void_p):
         return xs
     return (ctypes.c_void_p * len(xs))(*[_addr(x) for x in xs])
 

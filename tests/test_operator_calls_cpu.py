@@ -1,6 +1,7 @@
 """Calls of the head norm with rotation and of the 8-bit checkpoints that need no GPU: what is accepted, what is
 refused, and what the Python layer keeps."""
 import copy
+import ctypes
 import pickle
 
 import pytest
@@ -69,3 +70,19 @@ def test_autograd_functions_can_be_copied_and_pickled(name):
         for other in (copy.copy(fn), copy.deepcopy(fn), copy.deepcopy([fn])[0], pickle.loads(pickle.dumps(fn))):
             assert other.__name__ == name and other.apply == fn.apply
     assert tp.TPMLPFunction.__name__ != tp.TPMLPCheckpointFunction.__name__
+
+
+@pytest.mark.parametrize("element", [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int64])
+def test_arrays_of_addresses_of_any_integer_type(lib, element):
+    """A ctypes array counts as a sequence of addresses, whatever its elements' type."""
+    both = lambda *xs: (element * 2)(*xs)
+    n = both(0, 0)
+    p = heads_plan(0)  # no tokens: accepted, and nothing is launched
+    tp.tpmlp_attn_qk_norm_rope_forward(p, n, None, None, None, n, stream=0)
+    p = heads_plan(16)
+    call = lambda QK: tp.tpmlp_attn_qk_norm_rope_forward(p, both(A, A + (1 << 22)), None, None, None, QK, stream=0)
+    assert status_of(lambda: call(both(A + (1 << 24), A + (1 << 26) + 8))) == 3
+    assert status_of(lambda: call(both(A + (1 << 24), 0))) == 1
+    m = tp.AttnPlan(16, 64, [128, 64], [64, 64])
+    with pytest.raises(tp.TpmlpError):  # a misaligned entry, or no device
+        tp.tpmlp_attn_qkv_forward(m, A, both(A + 8, A + 8), both(A, A), A, stream=0)
