@@ -214,7 +214,10 @@ def _addr(x) -> Optional[int]:
     raise TypeError(f"expected a tensor or an int device pointer, got {type(x)}")
 
 
-def _arr(xs) -> Optional[ctypes.Array]:
+def _arr(xs, n=0) -> Optional[ctypes.Array]:
+    """A host array of addresses; n: how many of them the call reads."""
+    if xs is not None and len(xs) < n:
+        raise ValueError(f"expected {n} tensors or addresses, got {len(xs)}")
     if xs is None or (isinstance(xs, ctypes.Array) and xs._type_ is ctypes.c_void_p):
         return xs
     return (ctypes.c_void_p * len(xs))(*[_addr(x) for x in xs])
@@ -347,17 +350,19 @@ def tpmlp_attn_plan_set_qk_norm_rope(plan, head_dim, rotary_dim=None, layout="ha
 
 
 def tpmlp_attn_qk_norm_rope_forward(plan, QKV, positions, gq, gk, QK, stream=None):
-    _ok(load().tpmlp_attn_qk_norm_rope_forward(plan.handle, _arr(QKV), _positions(plan, positions), _addr(gq),
-                                               _addr(gk), _arr(QK), _stream(stream)),
+    t = plan.t
+    _ok(load().tpmlp_attn_qk_norm_rope_forward(plan.handle, _arr(QKV, t), _positions(plan, positions), _addr(gq),
+                                               _addr(gk), _arr(QK, t), _stream(stream)),
         "tpmlp_attn_qk_norm_rope_forward")
 
 
 def tpmlp_attn_qk_norm_rope_backward(plan, QKV, positions, gq, gk, dQK, dV, dQKV, dgq, dgk, workspace, stream=None):
     if hasattr(workspace, "numel") and workspace.numel() * workspace.element_size() < tpmlp_workspace_size(plan):
         raise ValueError("workspace is smaller than tpmlp_workspace_size(plan)")
-    _ok(load().tpmlp_attn_qk_norm_rope_backward(plan.handle, _arr(QKV), _positions(plan, positions), _addr(gq),
-                                                _addr(gk), _arr(dQK), _arr(dV), _arr(dQKV), _addr(dgq), _addr(dgk),
-                                                _addr(workspace), _stream(stream)),
+    t = plan.t
+    _ok(load().tpmlp_attn_qk_norm_rope_backward(plan.handle, _arr(QKV, t), _positions(plan, positions), _addr(gq),
+                                                _addr(gk), _arr(dQK, t), _arr(dV, t), _arr(dQKV, t), _addr(dgq),
+                                                _addr(dgk), _addr(workspace), _stream(stream)),
         "tpmlp_attn_qk_norm_rope_backward")
 
 
@@ -376,17 +381,27 @@ def tpmlp_ckpt8_unpack(dtype, rows, cols, ckpt, dst, ld, stream=None):
                                   _addr(ckpt), _addr(dst), int(ld), _stream(stream)), "tpmlp_ckpt8_unpack")
 
 
+def _shards(plan):
+    """Shards, those that have a W3, and activation tensors of an MLP plan."""
+    t3 = plan.t if getattr(plan, "act", None) in ("swiglu", ACT["swiglu"]) else 0
+    return plan.t, t3, plan.t + t3
+
+
 def tpmlp_forward_ckpt8(plan, X, W1, W3, W2, b1, b3, b2, Y, ckpt, H, workspace, stream=None):
-    _ok(load().tpmlp_forward_ckpt8(plan.handle, _addr(X), _arr(W1), _arr(W3), _arr(W2), _arr(b1), _arr(b3), _addr(b2),
-                                   _addr(Y), _arr(ckpt), _arr(H), _addr(workspace), _stream(stream)),
+    t, t3, n = _shards(plan)
+    _ok(load().tpmlp_forward_ckpt8(plan.handle, _addr(X), _arr(W1, t), _arr(W3, t3), _arr(W2, t), _arr(b1, t),
+                                   _arr(b3, t3), _addr(b2), _addr(Y), _arr(ckpt, n), _arr(H, t), _addr(workspace),
+                                   _stream(stream)),
         "tpmlp_forward_ckpt8")
 
 
 def tpmlp_backward_ckpt8(plan, X, W1, W3, W2, ckpt, H, dY, dact, dX, dW1, dW3, dW2, db1, db3, db2, workspace,
                          stream=None):
-    _ok(load().tpmlp_backward_ckpt8(plan.handle, _addr(X), _arr(W1), _arr(W3), _arr(W2), _arr(ckpt), _arr(H),
-                                    _addr(dY), _arr(dact), _addr(dX), _arr(dW1), _arr(dW3), _arr(dW2), _arr(db1),
-                                    _arr(db3), _addr(db2), _addr(workspace), _stream(stream)),
+    t, t3, n = _shards(plan)
+    _ok(load().tpmlp_backward_ckpt8(plan.handle, _addr(X), _arr(W1, t), _arr(W3, t3), _arr(W2, t), _arr(ckpt, n),
+                                    _arr(H, t), _addr(dY), _arr(dact, n), _addr(dX), _arr(dW1, t), _arr(dW3, t3),
+                                    _arr(dW2, t), _arr(db1, t), _arr(db3, t3), _addr(db2), _addr(workspace),
+                                    _stream(stream)),
         "tpmlp_backward_ckpt8")
 
 

@@ -86,3 +86,28 @@ def test_arrays_of_addresses_of_any_integer_type(lib, element):
     m = tp.AttnPlan(16, 64, [128, 64], [64, 64])
     with pytest.raises(tp.TpmlpError):  # a misaligned entry, or no device
         tp.tpmlp_attn_qkv_forward(m, A, both(A + 8, A + 8), both(A, A), A, stream=0)
+
+
+def test_lists_shorter_than_the_shards_are_refused(lib):
+    """The library would read addresses past the end of the host array."""
+    p, n = heads_plan(0), [None, None]
+    fwd = dict(QKV=n, pos=None, gq=None, gk=None, QK=n)
+    bwd = dict(QKV=n, pos=None, gq=None, gk=None, dQK=n, dV=n, dQKV=n, dgq=None, dgk=None, workspace=None)
+    calls = [(tp.tpmlp_attn_qk_norm_rope_forward, p, fwd), (tp.tpmlp_attn_qk_norm_rope_backward, p, bwd)]
+    for act in ("gelu", "swiglu"):
+        m, sw = tp.Plan(0, 64, [64, 32], act), act == "swiglu"
+        a, w, w3 = [None] * (4 if sw else 2), [A, A], [A, A] if sw else None
+        calls += [(tp.tpmlp_forward_ckpt8, m, dict(X=None, W1=w, W3=w3, W2=w, b1=w, b3=w3, b2=None, Y=None, ckpt=a, H=n,
+                                                   workspace=A)),
+                  (tp.tpmlp_backward_ckpt8, m, dict(X=None, W1=w, W3=w3, W2=w, ckpt=a, H=n, dY=None, dact=a, dX=None,
+                                                    dW1=w, dW3=w3, dW2=w, db1=w, db3=w3, db2=None, workspace=A))]
+    for f, plan, args in calls:
+        for name, xs in args.items():
+            if not isinstance(xs, list):
+                continue
+            for short in (xs[:-1], (ctypes.c_void_p * (len(xs) - 1))()):
+                with pytest.raises(ValueError):
+                    f(plan, *{**args, name: short}.values(), stream=0)
+    for f, plan, args in calls[:2]:  # whole ones, and longer ones, are taken
+        f(plan, *args.values(), stream=0)
+        f(plan, *{**args, "QKV": [None] * 3}.values(), stream=0)
