@@ -984,7 +984,8 @@ def _make_checkpoint_function():
 
     class TPMLPCheckpointFunction(torch.autograd.Function):
         """TPMLPFunction with the pre-activations kept as 8-bit checkpoints between the passes: it saves X, the
-        weights and 1.0625 bytes per pre-activation.
+        weights and 1.0625 bytes per pre-activation.  Without biases, as TPMLPFunction; any other number of weights is
+        refused.
 
         In a CUDA graph capture, capture forward and backward together, and let no eager autograd graph of the same
         leaves be alive then: autograd accumulates a leaf's gradient on the stream of the first graph that used it,
@@ -993,6 +994,9 @@ def _make_checkpoint_function():
         @staticmethod
         def forward(ctx, mlp: ShardedMLP, X, *weights):
             t = mlp.plan.t
+            n = (3 if mlp.swiglu else 2) * t
+            if len(weights) != n:  # no biases here: a longer list would be computed without its rest
+                raise ValueError(f"expected {n} weights (W1_i, W2_i{', W3_i' if mlp.swiglu else ''}), got {len(weights)}")
             X = X.contiguous()
             W3_i = list(weights[2 * t:3 * t]) if mlp.swiglu else None
             Y, ckpt = mlp.forward_ckpt8(X, list(weights[:t]), list(weights[t:2 * t]), W3_i)

@@ -5,6 +5,7 @@ import ctypes
 import pickle
 
 import pytest
+import torch
 
 import megatron_tensor_transformer_column_gb300 as tp
 
@@ -111,3 +112,14 @@ def test_lists_shorter_than_the_shards_are_refused(lib):
     for f, plan, args in calls[:2]:  # whole ones, and longer ones, are taken
         f(plan, *args.values(), stream=0)
         f(plan, *{**args, "QKV": [None] * 3}.values(), stream=0)
+
+
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_checkpoint_function_refuses_what_it_would_leave_out(lib, act):
+    """Biases behind the weights, or W3 with GeLU: the forward pass ignored them."""
+    mlp = tp.ShardedMLP(8, 16, [16, 8], act, device="cpu")
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    ws = [z(16, 16), z(16, 8), z(16, 16), z(8, 16)] + ([z(16, 16), z(16, 8)] if act == "swiglu" else [])
+    for weights in (ws + [z(16), z(8)], ws[:-1], ws[:2], []):
+        with pytest.raises(ValueError, match="weights"):
+            tp.TPMLPCheckpointFunction.apply(mlp, z(8, 16), *weights)
