@@ -106,8 +106,10 @@ TPMLP_API void tpmlp_plan_destroy(tpmlp_plan* plan);
 
 /* Bytes of device workspace every call needs.  fp32 plans: a 256-byte block
  * holding the device status word (and, once a norm of the heads is set,
- * tpmlp_attn_plan_set_qk_norm_rope, the partial sums of its gains' gradients).  bf16 plans: that block, then the ticket
- * counters and fp32 partial accumulators of the stream-K schedules (16 KB +
+ * tpmlp_attn_plan_set_qk_norm_rope, the partial sums of its gains' gradients:
+ * 256 bytes and 4 MB with the largest head_dim, which a program that describes the
+ * heads more than once takes from the start).  bf16 plans: that block, then
+ * the ticket counters and fp32 partial accumulators of the stream-K schedules (16 KB +
  * 160 x 256 KB, about 42 MB; see tpmlp_plan_set_stream_k).  The caller allocates it once,
  * zero-filled, and passes it to every call of this plan; calls that share it
  * must be ordered on the device.                                             */
@@ -351,7 +353,7 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * norm = 1 tpmlp_workspace_size grows: query it after this call.  Errors:
  * TPMLP_ERR_INVALID_ARG (NULL, an MLP plan, unknown layout, norm not 0 or 1,
  * eps, base or inv_freq not usable), TPMLP_ERR_SHAPE, TPMLP_ERR_UNSUPPORTED
- * (head_dim above 256).
+ * (head_dim above 256, or more heads).
  *
  * Forward: QK[i] = [Q_i | K_i] normed and rotated, dense [T x (dq_i + dkv_i)];
  * or in place, QK[i] == QKV[i]: then the query and key columns of the
@@ -367,8 +369,8 @@ TPMLP_API tpmlp_status tpmlp_attn_qkv_backward(const tpmlp_plan* plan, const voi
  * a gain's gradient is asked for, which is also when workspace is needed (the
  * plan's, zero-filled or used).  Other overlaps of the [T x ...] arrays, of
  * outputs with inputs or with each other, are refused (TPMLP_ERR_INVALID_ARG).
- * A gain's gradient is added in an order that depends on the device's SM count.  With T = 0 the gradients of the gains are
- * zero-filled.                                                               */
+ * A gain's gradient is added in an order that depends on the device's SM
+ * count.  With T = 0 the gradients of the gains are zero-filled.              */
 typedef enum { TPMLP_ROPE_HALVES = 0, TPMLP_ROPE_PAIRS = 1 } tpmlp_rope_layout;
 typedef struct {
   int32_t head_dim;

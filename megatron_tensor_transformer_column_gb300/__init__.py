@@ -996,7 +996,8 @@ def _make_checkpoint_function():
             t = mlp.plan.t
             n = (3 if mlp.swiglu else 2) * t
             if len(weights) != n:  # no biases here: a longer list would be computed without its rest
-                raise ValueError(f"expected {n} weights (W1_i, W2_i{', W3_i' if mlp.swiglu else ''}), got {len(weights)}")
+                names = "W1_i, W2_i, W3_i" if mlp.swiglu else "W1_i, W2_i"
+                raise ValueError(f"expected {n} weights ({names}), got {len(weights)}")
             X = X.contiguous()
             W3_i = list(weights[2 * t:3 * t]) if mlp.swiglu else None
             Y, ckpt = mlp.forward_ckpt8(X, list(weights[:t]), list(weights[t:2 * t]), W3_i)

@@ -39,14 +39,16 @@
 // of 8 shards of 16 + 1 heads of 128).
 //
 // Measured on GB300, bf16, device time and share of the copy bandwidth:
-//   16384 tokens, 8 shards of 4 + 4 heads of 96:   68 us (0.87), backward 141 us (0.84)
-//   8192 tokens, 8 shards of 16 + 1 heads of 128: 102 us (0.82), backward 158 us (0.83)
+//   16384 tokens, 8 shards of 4 + 4 heads of 96:   68 us (0.87), backward 141 us (0.84);
+//     without a norm 73 (0.81) and 100 us (0.89)
+//   8192 tokens, 8 shards of 16 + 1 heads of 128: 102 us (0.82), backward 158 us (0.83);
+//     without a norm 96 (0.88) and 100 us (0.89)
 // A first version with the loads in registers and every lane computing its own
 // angles took 147 and 359 us on the former: it was bound by instruction issue
 // (250 instructions a round forward) and latency.  What bounds it now is issue
 // and the latency of a round's chain (load, sum, root, store) together: 55 % of
-// the issue slots taken (190 instructions a round, backward 370) with 16 warps
-// an SM, which is what the registers allow.
+// the issue slots taken (190 instructions a round, backward 370) with the warps
+// an SM that the registers allow: 20 forward (92 registers), 16 backward (128).
 // Two heads a lane and round (4 % less time on the former shape, 1 to 30 %
 // more on small and 64-wide ones) and queues of four or six rounds (no gain)
 // were measured and not kept; a queue of two helps the latter shape (94 us) and

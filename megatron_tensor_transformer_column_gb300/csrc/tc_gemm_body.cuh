@@ -480,8 +480,10 @@ __device__ __forceinline__ void sk_fold(const GemmParams& p, const Prob& P, cons
 // The epilogues a kernel has.  A body with fewer of them is faster where tiles
 // are short (measured on GB300 on the GPT-2-small block: the row launch with
 // plain stores only 40.6 -> 37.9 us, the f-sum launch 83 -> 80 us, the launches
-// with 8-bit checkpoints 53 -> 49 and 61 -> 57 us), so a launch kind that uses
-// one kind of epilogue has no other in its kernel.
+// with 8-bit checkpoints 53 -> 49 and 61 -> 57 us), so the block's row and f-sum
+// launches and those with checkpoints have no other epilogue in their kernels.
+// The attention projections' launches, which store plainly too, have all of
+// them: EPIS_STORE was not measured there.
 enum EpiSet : int {
   EPIS_ALL = 0,
   EPIS_STORE = 1,    // EPI_STORE only

@@ -64,8 +64,8 @@ def test_backward_without_x(gpu_lib):
 
 
 def test_backward_turns_the_forward_pass_back(gpu_lib):
-    """<rotate(x), dy> = <x, rotate back(dy)>, in fp32: both sums from the kernels' outputs, off by 33 u (32, and the last rounding) of every
-    term's magnitude |a||c| + |b||c| each."""
+    """<rotate(x), dy> = <x, rotate back(dy)>, in fp32: both sums from the kernels' outputs, each off by 33 u (32, and
+    the last rounding) of every term's magnitude |a||c| + |b||c|."""
     s, p = shape(gpu_lib, 400, 64, 32, "halves", "fp32")
     y = p.qk_norm_rope_forward(s["QKV"], s["pos"])
     dx = p.qk_norm_rope_backward(None, s["dQK"], s["pos"], dV_i=s["dV"])[0]
