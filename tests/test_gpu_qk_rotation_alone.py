@@ -99,3 +99,61 @@ def test_special_values_with_the_norm(gpu_lib, layout):
     assert np.isnan(b[6, 1]).all() and np.isnan(b[7, 0]).any() and np.isnan(b[8, 0]).all()
     assert dgq2.isnan().any() and torch.equal(dgk, dgk2)
     assert torch.equal(got[0][:, 256:], s["dV"][0])
+
+
+@pytest.mark.parametrize("T", [1, 3, 640])
+def test_many_shards_and_heads(gpu_lib, T):
+    """The largest numbers of heads and shards; the same bits on another stream."""
+    s = make(T, [64] * 16, [64] * 16, 32, "bf16")
+    p = proj_of(gpu_lib, T, s, "bf16", 32, rotary_dim=16, layout="pairs", norm=False)
+    check_forward(s, p.qk_norm_rope_forward(s["QKV"], s["pos"]), 32, 16, "pairs", "bf16", norm=False, gains=False)
+    dQKV = p.qk_norm_rope_backward(None, s["dQK"], s["pos"], dV_i=s["dV"])[0]
+    check_backward(s, dQKV, None, None, 32, 16, "pairs", "bf16", norm=False, gains=False)
+    assert all(torch.equal(x[:, 4096:], v) for x, v in zip(dQKV, s["dV"]))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    again = p.qk_norm_rope_backward(None, s["dQK"], s["pos"], dV_i=s["dV"], stream=st)[0]
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(dQKV, again))
+
+
+def test_no_tokens(gpu_lib):
+    p = gpu_lib.ShardedAttentionProj(0, 64, [64], [64], "bf16")
+    p.set_qk_norm_rope(64, norm=False)
+    e = lambda n: torch.empty(0, n, dtype=torch.bfloat16, device="cuda")
+    assert p.qk_norm_rope_forward([e(192)])[0].shape == (0, 128)
+    assert p.qk_norm_rope_backward(None, [e(128)], dV_i=[e(64)])[0][0].shape == (0, 192)
+
+
+def test_gains_are_refused(gpu_lib):
+    s, p = shape(gpu_lib, 20, 64, 64, "halves", "bf16")
+    with pytest.raises(gpu_lib.TpmlpError):
+        p.qk_norm_rope_forward(s["QKV"], s["pos"], s["gq"], s["gk"])
+    with pytest.raises(gpu_lib.TpmlpError):
+        p.qk_norm_rope_backward(None, s["dQK"], s["pos"], s["gq"], s["gk"], s["dV"])
+    with pytest.raises(gpu_lib.TpmlpError):
+        p.qk_norm_rope_backward(None, s["dQK"], s["pos"], dV_i=s["dV"], gain_grads=True)
+    with pytest.raises(ValueError):  # with a norm x has to be there
+        proj_of(gpu_lib, 20, s, "bf16", 64).qk_norm_rope_backward(None, s["dQK"], s["pos"], dV_i=s["dV"])
+    with pytest.raises(ValueError):
+        p.qk_norm_rope_forward(None, s["pos"])
+
+
+def test_past_32_bits(gpu_lib):
+    """Buffers of more than 2^32 bytes: the last tokens, against the same tokens alone."""
+    T, n, last = 2_200_000, 1024, 70
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    big = lambda w: torch.randn(T, w, generator=gen, device="cuda", dtype=torch.bfloat16)
+    x, dy, dv, pos = big(n), big(768), big(256), torch.arange(T, device="cuda")
+    whole = gpu_lib.ShardedAttentionProj(T, 64, [512], [256])
+    part = gpu_lib.ShardedAttentionProj(last, 64, [512], [256])
+    for p in (whole, part):
+        p.set_qk_norm_rope(128, rotary_dim=64, norm=False)
+    cut = lambda t: t[-last:].contiguous()
+    y = whole.qk_norm_rope_forward([x], pos)[0]
+    assert torch.equal(y[-last:], part.qk_norm_rope_forward([cut(x)], cut(pos))[0])
+    dx = whole.qk_norm_rope_backward(None, [dy], pos, dV_i=[dv])[0][0]
+    assert torch.equal(dx[-last:], part.qk_norm_rope_backward(None, [cut(dy)], cut(pos), dV_i=[cut(dv)])[0][0])
