@@ -442,6 +442,56 @@ TPMLP_API tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* 
                                             void* const* dW1, void* const* dW3, void* const* dW2, void* const* db1,
                                             void* const* db3, void* db2, void* workspace, tpmlp_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Norm of the tokens in front of a block, with the residual stream's sum.
+ *
+ * Every token x of cols elements:
+ *   s = x + residual              (residual NULL: s = x; the sum is kept in the
+ *                                 storage type, and what is kept is normed)
+ *   mu = mean(s), r = (mean((s - mu)^2) + eps)^(-1/2)   (TPMLP_NORM_RMS: mu = 0)
+ *   n = (s - mu) r,  y = n gain + bias      (gain NULL: ones, bias NULL: zeros)
+ * Backward, from dy and dsum, the gradient that reaches s past the norm (the
+ * residual stream's; NULL: none):
+ *   w = dy gain,  dx = r (w - mean(w) - n mean(w n)) + dsum   (RMS: without mean(w))
+ *   dgain = sum over tokens of dy n,  dbias = sum over tokens of dy
+ * All in fp32, each output rounded once to the storage type.  dx is the gradient
+ * of x and of the residual alike.  A token with a NaN or an infinity spoils its
+ * own outputs and the gradients of gain and bias only; so does one whose squares
+ * pass the fp32 range (elements above about 10^17).
+ *
+ * Arrays are [rows x cols] with row strides ld* >= cols in elements; cols and
+ * every ld a multiple of 8 (bf16) / 4 (fp32), cols at most 16384.  gain, bias,
+ * dgain, dbias: [cols] in the storage type.  stats: [rows x 2] fp32, mu and r of
+ * each token; forward may be given NULL, backward reads what forward wrote.
+ * Forward: with a residual, sum receives s, which is the x of the backward call.
+ * Backward: dgain and dbias are optional (NULL: not computed); workspace,
+ * tpmlp_norm_workspace_size bytes, is needed if one of them is asked for (no
+ * contents are expected).  One launch each, backward a second one for dgain and
+ * dbias.
+ * In place: sum may be x or residual, y may be x or residual (where sum is not that
+ * array), dx may be x, dy or dsum, each with the same row stride.  Other overlaps
+ * of an output with another array are refused (TPMLP_ERR_INVALID_ARG), but for
+ * column slices of one buffer that share no element.  The sums over tokens are
+ * added in an order that depends on the device's SM count.  With rows = 0 dgain
+ * and dbias are zero-filled.                                                 */
+typedef enum { TPMLP_NORM_LAYER = 0, TPMLP_NORM_RMS = 1 } tpmlp_norm_kind;
+typedef struct {
+  int64_t rows, cols;
+  tpmlp_norm_kind kind;
+  tpmlp_dtype dtype;
+  float eps;            /* > 0 */
+} tpmlp_norm_desc;
+/* 0 for a desc that is not usable. */
+TPMLP_API size_t tpmlp_norm_workspace_size(const tpmlp_norm_desc* desc);
+TPMLP_API tpmlp_status tpmlp_norm_forward(const tpmlp_norm_desc* desc, const void* x, int64_t ldx,
+                                          const void* residual, int64_t ldr, const void* gain, const void* bias,
+                                          void* sum, int64_t lds, void* y, int64_t ldy, float* stats,
+                                          tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const void* x, int64_t ldx,
+                                           const float* stats, const void* gain, const void* dy, int64_t lddy,
+                                           const void* dsum, int64_t ldds, void* dx, int64_t lddx, void* dgain,
+                                           void* dbias, void* workspace, tpmlp_stream_t stream);
+
 /* Watchdog controls, for testing the failure path without faulting a GPU.
  * Neither may run while another call uses the plan.
  *   tpmlp_plan_set_timeout: bound, in milliseconds (>= 1), of every wait

@@ -11,7 +11,8 @@ CPU or PyTorch fallback, and :func:`load` raises if the library is missing.
 PyTorch (device memory and streams are all PyTorch provides here) and
 ``TPMLPFunction`` wraps forward/backward as a ``torch.autograd.Function``.
 ``ShardedAttentionProj`` does the same for the attention block's QKV and
-output projections (``tpmlp_attn_*``).
+output projections (``tpmlp_attn_*``), ``TokenNorm`` for the norm in front of
+a block (``tpmlp_norm_*``, ``TPMLPNormFunction``).
 """
 from __future__ import annotations
 
@@ -37,12 +38,14 @@ __all__ = [
     "ACT_EVAL", "tpmlp_attn_plan_set_qk_norm_rope", "tpmlp_attn_qk_norm_rope_forward",
     "tpmlp_attn_qk_norm_rope_backward", "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack",
     "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8", "ckpt8_pack", "ckpt8_unpack", "TPMLPCheckpointFunction",
-    "ROPE_LAYOUT",
+    "ROPE_LAYOUT", "NORM", "NormDesc", "tpmlp_norm_workspace_size", "tpmlp_norm_forward", "tpmlp_norm_backward",
+    "TokenNorm", "TPMLPNormFunction",
 ]
 
 ACT = {"gelu": 0, "swiglu": 1}
 DTYPE = {"bf16": 0, "fp32": 1}
 ROPE_LAYOUT = {"halves": 0, "pairs": 1}
+NORM = {"layer": 0, "rms": 1}
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_INVALID_ARG", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_ALIGNMENT",
           4: "TPMLP_ERR_UNSUPPORTED", 5: "TPMLP_ERR_CUDA", 6: "TPMLP_ERR_DEVICE_TIMEOUT",
           7: "TPMLP_ERR_NOT_IMPLEMENTED"}
@@ -58,6 +61,7 @@ EXPORTED_SYMBOLS = (
     "tpmlp_backward_sp", "tpmlp_plan_set_stream_k", "tpmlp_last_split_tiles", "tpmlp_eval_activation",
     "tpmlp_attn_plan_set_qk_norm_rope", "tpmlp_attn_qk_norm_rope_forward", "tpmlp_attn_qk_norm_rope_backward",
     "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack", "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8",
+    "tpmlp_norm_workspace_size", "tpmlp_norm_forward", "tpmlp_norm_backward",
 )
 
 # forms of tpmlp_eval_activation
@@ -95,6 +99,16 @@ class _QkDesc(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int),
                 ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("base", ctypes.c_double),
                 ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class NormDesc(ctypes.Structure):
+    """The ``tpmlp_norm_desc`` of [rows x cols] tokens; kind: a key of NORM, dtype: a key of DTYPE."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("kind", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+    def __init__(self, rows, cols, kind="layer", dtype="bf16", eps=1e-5):
+        super().__init__(int(rows), int(cols), NORM[kind] if isinstance(kind, str) else int(kind),
+                         DTYPE[dtype] if isinstance(dtype, str) else int(dtype), float(eps))
 
 
 _lib = None
@@ -194,6 +208,13 @@ def load():
         lib.tpmlp_forward_ckpt8.restype = st
         lib.tpmlp_backward_ckpt8.argtypes = lib.tpmlp_backward_recompute.argtypes
         lib.tpmlp_backward_ckpt8.restype = st
+        nd = ctypes.POINTER(NormDesc)
+        lib.tpmlp_norm_workspace_size.argtypes = [nd]
+        lib.tpmlp_norm_workspace_size.restype = ctypes.c_size_t
+        lib.tpmlp_norm_forward.argtypes = [nd, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp]
+        lib.tpmlp_norm_forward.restype = st
+        lib.tpmlp_norm_backward.argtypes = [nd, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+        lib.tpmlp_norm_backward.restype = st
         _lib = lib
         return lib
 
@@ -403,6 +424,26 @@ def tpmlp_backward_ckpt8(plan, X, W1, W3, W2, ckpt, H, dY, dact, dX, dW1, dW3, d
                                     _arr(dW2, t), _arr(db1, t), _arr(db3, t3), _addr(db2), _addr(workspace),
                                     _stream(stream)),
         "tpmlp_backward_ckpt8")
+
+
+def tpmlp_norm_workspace_size(desc: NormDesc) -> int:
+    """Bytes of workspace that tpmlp_norm_backward needs for the gradients of gain and bias."""
+    return int(load().tpmlp_norm_workspace_size(ctypes.byref(desc)))
+
+
+def tpmlp_norm_forward(desc, x, ldx, residual, ldr, gain, bias, sum, lds, y, ldy, stats, stream=None):
+    _ok(load().tpmlp_norm_forward(ctypes.byref(desc), _addr(x), ldx, _addr(residual), ldr, _addr(gain), _addr(bias),
+                                  _addr(sum), lds, _addr(y), ldy, _addr(stats), _stream(stream)),
+        "tpmlp_norm_forward")
+
+
+def tpmlp_norm_backward(desc, x, ldx, stats, gain, dy, lddy, dsum, ldds, dx, lddx, dgain, dbias, workspace,
+                        stream=None):
+    if hasattr(workspace, "numel") and workspace.numel() * workspace.element_size() < tpmlp_norm_workspace_size(desc):
+        raise ValueError("workspace is smaller than tpmlp_norm_workspace_size(desc)")
+    _ok(load().tpmlp_norm_backward(ctypes.byref(desc), _addr(x), ldx, _addr(stats), _addr(gain), _addr(dy), lddy,
+                                   _addr(dsum), ldds, _addr(dx), lddx, _addr(dgain), _addr(dbias), _addr(workspace),
+                                   _stream(stream)), "tpmlp_norm_backward")
 
 
 def tpmlp_plan_set_sequence_stripes(plan: Plan, stripe_rows: Sequence[int]):
@@ -943,6 +984,80 @@ class ShardedAttentionProj:
         tpmlp_check(self.plan, self.workspace, stream)
 
 
+class TokenNorm:
+    """Layer norm or RMS norm of T tokens of d elements in front of a block, with the workspace of its backward pass.
+
+    x, residual, sum, y, dy, dsum, dx: [T, d] in the norm's dtype, rows contiguous but possibly further apart than they
+    are long (a column slice); gain, bias: [d]; stats: [T, 2] fp32."""
+
+    def __init__(self, T: int, d: int, kind: str = "layer", dtype: str = "bf16", eps: float = 1e-5, device=None):
+        import torch
+        self.T, self.d, self.kind, self.dtype = int(T), int(d), kind, dtype
+        self.desc = NormDesc(T, d, kind, dtype, eps)
+        self.tdtype = _tdtype(dtype)
+        n = tpmlp_norm_workspace_size(self.desc)
+        if not n:
+            raise ValueError(_lib.tpmlp_last_error().decode(errors="replace"))
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        self._shape = torch.Size((self.T, self.d))
+
+    def _rows(self, name, x):
+        """(address, row stride) of a [T, d] argument."""
+        if x.shape != self._shape or x.dtype != self.tdtype or x.device != self.workspace.device:
+            raise ValueError(f"{name}: expected {tuple(self._shape)} of {self.tdtype} on {self.workspace.device}, got "
+                             f"{tuple(x.shape)} of {x.dtype} on {x.device}")
+        return _rows_apart(name, x)
+
+    def _vector(self, name, x):
+        return None if x is None else _ptr(name, x, (self.d,), self.tdtype, self.workspace.device)
+
+    def forward(self, x, gain=None, bias=None, residual=None, out=None, stream=None):
+        """(y, stats, s): s = x + residual (x itself without one) normed to y; s and stats are what backward takes.
+        out: (y, s) to write to; s may be x or residual, y may be x or residual where s is not."""
+        import torch
+        dev = self.workspace.device
+        xp, ldx = self._rows("x", x)
+        rp, ldr = self._rows("residual", residual) if residual is not None else (None, 0)
+        g, b = self._vector("gain", gain), self._vector("bias", bias)
+        with _on(dev, stream):
+            if out is None:
+                y = torch.empty(self._shape, dtype=self.tdtype, device=dev)
+                s = torch.empty(self._shape, dtype=self.tdtype, device=dev) if residual is not None else x
+            else:
+                y, s = out
+                if residual is None and s is not None and s is not x:
+                    raise ValueError("out: a sum without a residual")
+                s = x if residual is None else s
+            yp, ldy = self._rows("y", y)
+            sp, lds = self._rows("sum", s) if residual is not None else (None, 0)
+            stats = torch.empty((self.T, 2), dtype=torch.float32, device=dev)
+            tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr() or None,
+                               _current(dev))
+        return y, stats, s
+
+    def backward(self, x, stats, dy, gain=None, dsum=None, out=None, stream=None, gain_grad=None, bias_grad=False):
+        """(dx, dgain, dbias) from the s and stats of forward and the gradients of y and (dsum, optional) of s itself.
+        out: the dx to write to, which may be dy, dsum or x.  gain_grad: whether to compute dgain (None: if a gain is
+        given)."""
+        import torch
+        dev = self.workspace.device
+        xp, ldx = self._rows("x", x)
+        dyp, lddy = self._rows("dy", dy)
+        dsp, ldds = self._rows("dsum", dsum) if dsum is not None else (None, 0)
+        g, st = self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), torch.float32, dev)
+        if gain_grad is None:
+            gain_grad = gain is not None
+        with _on(dev, stream):
+            dx = torch.empty(self._shape, dtype=self.tdtype, device=dev) if out is None else out
+            dxp, lddx = self._rows("out", dx)
+            dgain = torch.empty(self.d, dtype=self.tdtype, device=dev) if gain_grad else None
+            dbias = torch.empty(self.d, dtype=self.tdtype, device=dev) if bias_grad else None
+            tpmlp_norm_backward(self.desc, xp, ldx, st or None, g, dyp, lddy, dsp, ldds, dxp, lddx,
+                                dgain.data_ptr() if gain_grad else None, dbias.data_ptr() if bias_grad else None,
+                                self.workspace.data_ptr(), _current(dev))
+        return dx, dgain, dbias
+
+
 def _make_function():
     import torch
 
@@ -1019,6 +1134,38 @@ def _make_checkpoint_function():
     return TPMLPCheckpointFunction
 
 
+def _make_norm_function():
+    import torch
+
+    def rows(x):
+        return x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+
+    class TPMLPNormFunction(torch.autograd.Function):
+        """y = TPMLPNormFunction.apply(norm, x, gain, bias), or (y, x + residual) = TPMLPNormFunction.apply(norm, x,
+        gain, bias, residual), with the library's backward; gain and bias may be None.  What TPMLPCheckpointFunction
+        says of captures holds here as well."""
+
+        @staticmethod
+        def forward(ctx, norm: TokenNorm, x, gain, bias, residual=None):
+            y, stats, s = norm.forward(rows(x), gain, bias, None if residual is None else rows(residual))
+            ctx.norm, ctx.has_bias, ctx.n = norm, bias is not None, 4 if residual is None else 5
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(s, stats, gain)
+            return y if residual is None else (y, s)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy, ds=None):
+            s, stats, gain = ctx.saved_tensors
+            if dy is None:  # y was not used
+                dy = torch.zeros_like(s)
+            dx, dgain, dbias = ctx.norm.backward(s, stats, rows(dy), gain, None if ds is None else rows(ds),
+                                                 bias_grad=ctx.has_bias)
+            return (None, dx, dgain, dbias, dx)[:ctx.n]
+
+    return TPMLPNormFunction
+
+
 class _LazyFunction:
     """An autograd function that is made, and torch imported, on its first use.  What was made stays with the class, so
     that a copy of the object, or one that was pickled, is as good as the object."""
@@ -1036,5 +1183,10 @@ class _LazyCheckpointFunction(_LazyFunction):
     _make, _fn = staticmethod(_make_checkpoint_function), None
 
 
+class _LazyNormFunction(_LazyFunction):
+    _make, _fn = staticmethod(_make_norm_function), None
+
+
 TPMLPFunction = _LazyFunction()
 TPMLPCheckpointFunction = _LazyCheckpointFunction()
+TPMLPNormFunction = _LazyNormFunction()

@@ -1986,6 +1986,215 @@ tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* X, const v
   )
 }
 
+namespace {
+
+// A [rows x cols] argument of the norm: an array of the caller, its row stride in elements.
+struct NormArray {
+  const char* name;
+  const void* p;
+  int64_t ld;
+  bool out;
+};
+
+// Whether two such arrays share an element: by their byte ranges, or, with one row stride, by their columns.
+bool share(const tpmlp_norm_desc& d, const NormArray& a, const NormArray& b) {
+  if (!a.p || !b.p || !d.rows) return false;
+  const int64_t es = d.dtype == TPMLP_BF16 ? 2 : 4;
+  if (!overlap(a.p, ((d.rows - 1) * a.ld + d.cols) * es, b.p, ((d.rows - 1) * b.ld + d.cols) * es)) return false;
+  if (a.ld != b.ld) return true;
+  const int64_t ld = a.ld * es, w = d.cols * es;
+  int64_t delta = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % ld;
+  if (delta < 0) delta += ld;
+  return delta < w || ld - delta < w;
+}
+
+tpmlp_status norm_desc_checks(const tpmlp_norm_desc* d) {
+  g_last_error[0] = 0;
+  if (!d) return fail(TPMLP_ERR_INVALID_ARG, "desc is NULL");
+  if (d->kind != TPMLP_NORM_LAYER && d->kind != TPMLP_NORM_RMS)
+    return fail(TPMLP_ERR_INVALID_ARG, "unknown norm %d", static_cast<int>(d->kind));
+  if (d->dtype != TPMLP_BF16 && d->dtype != TPMLP_FP32)
+    return fail(TPMLP_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(d->dtype));
+  if (!(d->eps > 0.0f && std::isfinite(d->eps)))
+    return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive number", static_cast<double>(d->eps));
+  if (d->rows < 0 || d->cols < 1)
+    return fail(TPMLP_ERR_SHAPE, "need rows >= 0, cols >= 1 (got rows=%lld cols=%lld)",
+                static_cast<long long>(d->rows), static_cast<long long>(d->cols));
+  const int64_t mult = d->dtype == TPMLP_BF16 ? 8 : 4;
+  if (d->cols % mult)
+    return fail(TPMLP_ERR_ALIGNMENT, "cols = %lld must be a multiple of %lld", static_cast<long long>(d->cols),
+                static_cast<long long>(mult));
+  if (d->cols > kNormMaxCols)
+    return fail(TPMLP_ERR_UNSUPPORTED, "cols = %lld is above %d", static_cast<long long>(d->cols), kNormMaxCols);
+  return TPMLP_OK;
+}
+
+tpmlp_status norm_array_checks(const tpmlp_norm_desc* d, const NormArray* arrays, int n) {
+  const int64_t mult = d->dtype == TPMLP_BF16 ? 8 : 4;
+  for (int i = 0; i < n; ++i) {
+    const NormArray& a = arrays[i];
+    if (!a.p) continue;
+    if (a.ld < d->cols)
+      return fail(TPMLP_ERR_SHAPE, "the row stride of %s, %lld, is below cols = %lld", a.name,
+                  static_cast<long long>(a.ld), static_cast<long long>(d->cols));
+    if (a.ld % mult)
+      return fail(TPMLP_ERR_ALIGNMENT, "the row stride of %s, %lld, must be a multiple of %lld", a.name,
+                  static_cast<long long>(a.ld), static_cast<long long>(mult));
+    if (d->rows && a.ld > (int64_t(1) << 48) / d->rows)  // past any memory; the products stay within 64 bits
+      return fail(TPMLP_ERR_UNSUPPORTED, "rows times the row stride of %s is above 2^48", a.name);
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j) {
+      const NormArray &a = arrays[i], &b = arrays[j];
+      if (!a.out || i == j || (b.out && j > i) || !share(*d, a, b)) continue;
+      if (b.out || a.p != b.p || a.ld != b.ld)
+        return fail(TPMLP_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    }
+  return TPMLP_OK;
+}
+
+// Vectors (gain, bias, statistics, their gradients) against each output.
+tpmlp_status norm_vector_checks(const tpmlp_norm_desc* d, const NormArray* arrays, int n, const NormArray* vectors,
+                                int m) {
+  const int64_t es = d->dtype == TPMLP_BF16 ? 2 : 4;
+  for (int j = 0; j < m; ++j) {  // a vector's ld: its bytes
+    for (int i = 0; i < n; ++i)
+      if ((arrays[i].out || vectors[j].out) && arrays[i].p && d->rows &&
+          overlap(arrays[i].p, ((d->rows - 1) * arrays[i].ld + d->cols) * es, vectors[j].p,
+                  vectors[j].p ? vectors[j].ld : 0))
+        return fail(TPMLP_ERR_INVALID_ARG, "%s overlaps %s", arrays[i].name, vectors[j].name);
+    for (int i = 0; i < j; ++i)
+      if ((vectors[i].out || vectors[j].out) && vectors[i].p && vectors[j].p &&
+          overlap(vectors[i].p, vectors[i].ld, vectors[j].p, vectors[j].ld))
+        return fail(TPMLP_ERR_INVALID_ARG, "%s overlaps %s", vectors[j].name, vectors[i].name);
+  }
+  return TPMLP_OK;
+}
+
+NormParams norm_params(const tpmlp_norm_desc* d) {
+  NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rows = d->rows;
+  p.cols = static_cast<int32_t>(d->cols);
+  p.rms = d->kind == TPMLP_NORM_RMS;
+  p.eps = d->eps;
+  p.inv_cols = 1.0f / static_cast<float>(d->cols);
+  return p;
+}
+
+}  // namespace
+
+size_t tpmlp_norm_workspace_size(const tpmlp_norm_desc* desc) {
+  if (norm_desc_checks(desc) != TPMLP_OK) return 0;
+  return static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(desc->rows, 1), kNormMaxCtas)) * 2 *
+         static_cast<size_t>(desc->cols) * sizeof(float);
+}
+
+tpmlp_status tpmlp_norm_forward(const tpmlp_norm_desc* desc, const void* x, int64_t ldx, const void* residual,
+                                int64_t ldr, const void* gain, const void* bias, void* sum, int64_t lds, void* y,
+                                int64_t ldy, float* stats, tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(norm_desc_checks(desc));
+  const bool none = desc->rows == 0;
+  TPMLP_TRY(check_ptr("x", x, none));
+  TPMLP_TRY(check_ptr("residual", residual, true));
+  TPMLP_TRY(check_ptr("gain", gain, true));
+  TPMLP_TRY(check_ptr("bias", bias, true));
+  TPMLP_TRY(check_ptr("sum", sum, none || !residual));
+  TPMLP_TRY(check_ptr("y", y, none));
+  TPMLP_TRY(check_ptr("stats", stats, true));
+  if (sum && !residual && !none) return fail(TPMLP_ERR_INVALID_ARG, "sum without a residual");
+  const NormArray arrays[] = {{"x", x, ldx, false}, {"residual", residual, ldr, false}, {"sum", sum, lds, true},
+                              {"y", y, ldy, true}};
+  TPMLP_TRY(norm_array_checks(desc, arrays, 4));
+  const int64_t vec = desc->cols * (desc->dtype == TPMLP_BF16 ? 2 : 4);
+  const NormArray vectors[] = {{"gain", gain, vec, false}, {"bias", bias, vec, false},
+                               {"stats", stats, desc->rows * 8, true}};
+  TPMLP_TRY(norm_vector_checks(desc, arrays, 4, vectors, 3));
+  if (none) return TPMLP_OK;
+  DeviceInfo di;
+  TPMLP_TRY(device_info(&di));
+  const int64_t es = desc->dtype == TPMLP_BF16 ? 2 : 4;
+  NormParams p = norm_params(desc);
+  p.x = x;
+  p.res = residual;
+  p.sum = sum;
+  p.y = y;
+  p.gain = gain;
+  p.bias = bias;
+  p.stats = stats;
+  p.ldx = ldx * es;
+  p.ldr = ldr * es;
+  p.lds = lds * es;
+  p.ldy = ldy * es;
+  cudaError_t e = launch_norm(p, desc->dtype == TPMLP_BF16, false, di.sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  ++g_last_launches;
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const void* x, int64_t ldx, const float* stats,
+                                 const void* gain, const void* dy, int64_t lddy, const void* dsum, int64_t ldds,
+                                 void* dx, int64_t lddx, void* dgain, void* dbias, void* workspace,
+                                 tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(norm_desc_checks(desc));
+  const bool none = desc->rows == 0, sums = dgain || dbias;
+  TPMLP_TRY(check_ptr("x", x, none));
+  TPMLP_TRY(check_ptr("stats", stats, none));
+  TPMLP_TRY(check_ptr("gain", gain, true));
+  TPMLP_TRY(check_ptr("dy", dy, none));
+  TPMLP_TRY(check_ptr("dsum", dsum, true));
+  TPMLP_TRY(check_ptr("dx", dx, none));
+  TPMLP_TRY(check_ptr("dgain", dgain, true));
+  TPMLP_TRY(check_ptr("dbias", dbias, true));
+  TPMLP_TRY(check_ptr("workspace", workspace, none || !sums));
+  const NormArray arrays[] = {{"x", x, ldx, false}, {"dy", dy, lddy, false}, {"dsum", dsum, ldds, false},
+                              {"dx", dx, lddx, true}};
+  TPMLP_TRY(norm_array_checks(desc, arrays, 4));
+  const int64_t es = desc->dtype == TPMLP_BF16 ? 2 : 4, vec = desc->cols * es;
+  const int64_t ws = sums ? static_cast<int64_t>(tpmlp_norm_workspace_size(desc)) : 0;
+  const NormArray vectors[] = {{"gain", gain, vec, false}, {"stats", stats, desc->rows * 8, false},
+                               {"dgain", dgain, vec, true}, {"dbias", dbias, vec, true},
+                               {"workspace", workspace, ws, true}};
+  TPMLP_TRY(norm_vector_checks(desc, arrays, 4, vectors, 5));
+  if (none && !sums) return TPMLP_OK;
+  DeviceInfo di;
+  TPMLP_TRY(device_info(&di));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (none) {
+    for (void* g : {dgain, dbias})
+      if (g) {
+        cudaError_t e = cudaMemsetAsync(g, 0, static_cast<size_t>(vec), st);
+        if (e != cudaSuccess) return cuda_fail(e);
+      }
+    return TPMLP_OK;
+  }
+  const bool bf16 = desc->dtype == TPMLP_BF16;
+  NormParams p = norm_params(desc);
+  p.x = x;
+  p.gain = gain;
+  p.stats = const_cast<float*>(stats);
+  p.dy = dy;
+  p.dsum = dsum;
+  p.dx = dx;
+  p.ldx = ldx * es;
+  p.lddy = lddy * es;
+  p.ldds = ldds * es;
+  p.lddx = lddx * es;
+  p.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  p.want_bias = dbias != nullptr;
+  cudaError_t e = launch_norm(p, bf16, true, di.sms, st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  ++g_last_launches;
+  if (sums) {
+    e = launch_norm_gain_grad(p, bf16, dgain, dbias, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+    ++g_last_launches;
+  }
+  return TPMLP_OK;
+}
+
 tpmlp_status tpmlp_plan_set_sequence_stripes(tpmlp_plan* plan, int32_t nstripes, const int64_t* stripe_rows) {
   g_last_error[0] = 0;
   if (!plan) return fail(TPMLP_ERR_INVALID_ARG, "plan is NULL");

@@ -312,6 +312,30 @@ cudaError_t launch_ckpt8_pack(bool bf16, int64_t rows, int64_t cols, const void*
 cudaError_t launch_ckpt8_unpack(bool bf16, int64_t rows, int64_t cols, const void* ckpt, void* dst, int64_t ld,
                                 cudaStream_t stream);
 
+// Norm of the tokens (token_norm.cu).  Row strides are in bytes.
+constexpr int kNormMaxCols = 16384;
+constexpr int kNormMaxCtas = 160;  // bound of a launch's CTAs: rows of its partial sums of dgain and dbias
+struct NormParams {
+  const void* x;
+  const void* res;   // forward: the residual stream, or null
+  void* sum;         // forward, with res
+  void* y;
+  const void* gain;  // null: ones
+  const void* bias;  // null: zeros
+  float* stats;      // [rows] pairs (mean, 1 / deviation); forward: may be null
+  const void* dy;
+  const void* dsum;  // backward: may be null
+  void* dx;
+  float* partial;    // backward: [2][CTAs][cols] sums of dgain and dbias, or null
+  int64_t rows, ldx, ldr, lds, ldy, lddy, ldds, lddx;
+  int32_t cols, rms;
+  float eps, inv_cols;
+  int32_t want_bias;    // backward: the bias's sums are asked for
+  int32_t stages, ctas;  // set by the launcher
+};
+cudaError_t launch_norm(NormParams& p, bool bf16, bool bwd, int sms, cudaStream_t stream);
+cudaError_t launch_norm_gain_grad(const NormParams& p, bool bf16, void* dgain, void* dbias, cudaStream_t stream);
+
 // Kernel parameters live in the 32 KB parameter space (__grid_constant__).
 static_assert(sizeof(GemmParams) <= 32000, "kernel parameter block too large");
 

@@ -1,0 +1,116 @@
+"""Argument checks of the operators around the GEMM launches of a step, and their references, without a GPU: no kernel
+is launched here."""
+import ctypes
+
+import pytest
+import torch
+
+import megatron_tensor_transformer_column_gb300 as tp
+import step_reference as ref
+
+FAKE = 1 << 20  # never dereferenced
+INVALID, SHAPE, ALIGN, UNSUPPORTED, CUDA = 1, 2, 3, 4, 5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from megatron_tensor_transformer_column_gb300 import _build
+    _build.build()
+    return tp.load()
+
+
+def status_of(call):
+    with pytest.raises(tp.TpmlpError) as e:
+        call()
+    return e.value.status
+
+
+# ---------------------------------------------------------------- the tokens' norm
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_norm_reference_gradient_against_differences(kind):
+    gen = torch.Generator().manual_seed(0)
+    x, dy, ds, v = (torch.randn(3, 24, generator=gen, dtype=torch.float64) for _ in range(4))
+    g, b, w = (torch.randn(24, generator=gen, dtype=torch.float64) for _ in range(3))
+    f = lambda x, g, b: (ref.norm_forward(x, g, b, kind, 1e-3)[0] * dy).sum() + (x * ds).sum()
+    _, mu, r = ref.norm_forward(x, g, b, kind, 1e-3)
+    dx, dg, db = ref.norm_backward(x, mu, r, dy, ds, g, kind)
+    h = 1e-6
+    assert abs((f(x + h * v, g, b) - f(x - h * v, g, b)) / (2 * h) - (dx * v).sum()) < 1e-7
+    assert abs((f(x, g + h * w, b) - f(x, g - h * w, b)) / (2 * h) - (dg * w).sum()) < 1e-7
+    assert abs((f(x, g, b + h * w) - f(x, g, b - h * w)) / (2 * h) - (db * w).sum()) < 1e-7
+
+
+def norm_fwd(rows=4, cols=64, kind="layer", dtype="bf16", eps=1e-5, **kw):
+    a = {"x": FAKE, "ldx": cols, "residual": None, "ldr": cols, "gain": None, "bias": None, "sum": None, "lds": cols,
+         "y": 2 * FAKE, "ldy": cols, "stats": None} | kw
+    tp.tpmlp_norm_forward(tp.NormDesc(rows, cols, kind, dtype, eps), *a.values(), stream=0)
+
+
+def norm_bwd(rows=4, cols=64, kind="layer", dtype="bf16", eps=1e-5, **kw):
+    a = {"x": FAKE, "ldx": cols, "stats": 3 * FAKE, "gain": None, "dy": 4 * FAKE, "lddy": cols, "dsum": None,
+         "ldds": cols, "dx": 5 * FAKE, "lddx": cols, "dgain": None, "dbias": None, "workspace": None} | kw
+    tp.tpmlp_norm_backward(tp.NormDesc(rows, cols, kind, dtype, eps), *a.values(), stream=0)
+
+
+@pytest.mark.parametrize("call", [norm_fwd, norm_bwd])
+def test_norm_descriptions(lib, call):
+    assert status_of(lambda: call(kind=2)) == INVALID
+    assert status_of(lambda: call(dtype=2)) == INVALID
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        assert status_of(lambda: call(eps=eps)) == INVALID
+    assert status_of(lambda: call(rows=-1)) == SHAPE
+    assert status_of(lambda: call(cols=0)) == SHAPE
+    assert status_of(lambda: call(cols=60)) == ALIGN
+    assert status_of(lambda: call(cols=62, dtype="fp32")) == ALIGN
+    assert status_of(lambda: call(cols=16392)) == UNSUPPORTED
+    assert status_of(lambda: call(ldx=56)) == SHAPE
+    assert status_of(lambda: call(ldx=68)) == ALIGN
+    assert status_of(lambda: call(rows=1 << 40, ldx=1 << 20)) == UNSUPPORTED
+    assert status_of(lambda: call(x=None)) == INVALID
+    assert status_of(lambda: call(x=FAKE + 8)) == ALIGN
+    assert lib.tpmlp_norm_forward(None, *[0] * 12) == INVALID  # no desc at all
+    if not torch.cuda.is_available():
+        assert status_of(call) == CUDA  # the arguments are good
+
+
+def test_norm_forward_refusals(lib):
+    assert status_of(lambda: norm_fwd(y=None)) == INVALID
+    assert status_of(lambda: norm_fwd(residual=3 * FAKE)) == INVALID  # no sum
+    assert status_of(lambda: norm_fwd(sum=3 * FAKE)) == INVALID      # no residual
+    assert status_of(lambda: norm_fwd(residual=3 * FAKE, sum=2 * FAKE)) == INVALID  # sum is y
+    assert status_of(lambda: norm_fwd(y=FAKE + 16)) == INVALID  # y overlaps x
+    assert status_of(lambda: norm_fwd(y=FAKE, ldy=72)) == INVALID  # in place with another stride
+    assert status_of(lambda: norm_fwd(ldx=128, y=FAKE + 112, ldy=128)) == INVALID  # columns in common
+    assert status_of(lambda: norm_fwd(gain=2 * FAKE)) == INVALID
+    assert status_of(lambda: norm_fwd(stats=2 * FAKE + 256)) == INVALID
+    assert status_of(lambda: norm_fwd(stats=FAKE)) == INVALID
+    assert status_of(lambda: norm_fwd(gain=3 * FAKE, stats=3 * FAKE)) == INVALID
+    assert status_of(lambda: norm_fwd(gain=3 * FAKE + 2)) == ALIGN
+    norm_fwd(rows=0, x=None, y=None)
+
+
+def test_norm_backward_refusals(lib):
+    for name in ("stats", "dy", "dx"):
+        assert status_of(lambda: norm_bwd(**{name: None})) == INVALID
+    assert status_of(lambda: norm_bwd(dgain=6 * FAKE)) == INVALID  # no workspace
+    ws = 8 * FAKE
+    assert status_of(lambda: norm_bwd(dgain=6 * FAKE, dbias=6 * FAKE, workspace=ws)) == INVALID
+    assert status_of(lambda: norm_bwd(dgain=5 * FAKE, workspace=ws)) == INVALID  # dgain in dx
+    assert status_of(lambda: norm_bwd(dgain=ws, workspace=ws)) == INVALID
+    assert status_of(lambda: norm_bwd(dgain=6 * FAKE, workspace=4 * FAKE)) == INVALID  # the workspace in dy
+    assert status_of(lambda: norm_bwd(dx=3 * FAKE)) == INVALID  # dx in stats
+    assert status_of(lambda: norm_bwd(dx=4 * FAKE + 128)) == INVALID
+    norm_bwd(rows=0, x=None, stats=None, dy=None, dx=None)
+
+
+def test_norm_workspace(lib):
+    size = tp.tpmlp_norm_workspace_size
+    assert size(tp.NormDesc(5, 64)) == 5 * 2 * 64 * 4
+    assert size(tp.NormDesc(100000, 64)) == size(tp.NormDesc(160, 64)) == 160 * 2 * 64 * 4
+    assert size(tp.NormDesc(5, 60)) == size(tp.NormDesc(5, 16392)) == 0
+    small = torch.empty(16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="smaller"):
+        norm_bwd(dgain=6 * FAKE, workspace=small)
+    with pytest.raises(ValueError):
+        tp.TokenNorm(4, 60)
