@@ -443,6 +443,35 @@ TPMLP_API tpmlp_status tpmlp_backward_ckpt8(const tpmlp_plan* plan, const void* 
                                             void* const* db3, void* db2, void* workspace, tpmlp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The residual stream in the epilogue of the row-parallel products.
+ *
+ * The calls of the same name without _residual, with residual [T x d] added to
+ * the product:
+ *   Y = residual + sum_i H_i W2_i + b2        Z = residual + sum_i O_i WO_i
+ * taken of the fp32 accumulator (after b2) and rounded once.  Y (Z) may be the
+ * residual itself; an overlap of the two in any other way is refused
+ * (TPMLP_ERR_INVALID_ARG).  As many launches, the same workspace and schedules.
+ * The residual's gradient is dY (dZ); the other gradients are those of the calls
+ * without it, so the backward passes are the same.  Not for the token-striped
+ * layout.                                                                    */
+TPMLP_API tpmlp_status tpmlp_forward_row_residual(const tpmlp_plan* plan, const void* const* W2, const void* b2,
+                                                  const void* residual, void* const* H, void* Y, void* workspace,
+                                                  tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_attn_out_forward_residual(const tpmlp_plan* plan, const void* const* WO,
+                                                       const void* const* O, const void* residual, void* Z,
+                                                       void* workspace, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_forward_residual(const tpmlp_plan* plan, const void* X, const void* const* W1,
+                                              const void* const* W3, const void* const* W2, const void* const* b1,
+                                              const void* const* b3, const void* b2, const void* residual, void* Y,
+                                              void* const* saved, void* const* H, void* workspace,
+                                              tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_forward_ckpt8_residual(const tpmlp_plan* plan, const void* X, const void* const* W1,
+                                                    const void* const* W3, const void* const* W2,
+                                                    const void* const* b1, const void* const* b3, const void* b2,
+                                                    const void* residual, void* Y, void* const* ckpt,
+                                                    void* const* H, void* workspace, tpmlp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Norm of the tokens in front of a block, with the residual stream's sum.
  *
  * Every token x of cols elements:

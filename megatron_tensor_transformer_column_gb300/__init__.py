@@ -39,7 +39,8 @@ __all__ = [
     "tpmlp_attn_qk_norm_rope_backward", "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack",
     "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8", "ckpt8_pack", "ckpt8_unpack", "TPMLPCheckpointFunction",
     "ROPE_LAYOUT", "NORM", "NormDesc", "tpmlp_norm_workspace_size", "tpmlp_norm_forward", "tpmlp_norm_backward",
-    "TokenNorm", "TPMLPNormFunction",
+    "TokenNorm", "TPMLPNormFunction", "tpmlp_forward_row_residual", "tpmlp_attn_out_forward_residual",
+    "tpmlp_forward_residual", "tpmlp_forward_ckpt8_residual", "TPMLPResidualFunction",
 ]
 
 ACT = {"gelu": 0, "swiglu": 1}
@@ -62,6 +63,8 @@ EXPORTED_SYMBOLS = (
     "tpmlp_attn_plan_set_qk_norm_rope", "tpmlp_attn_qk_norm_rope_forward", "tpmlp_attn_qk_norm_rope_backward",
     "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack", "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8",
     "tpmlp_norm_workspace_size", "tpmlp_norm_forward", "tpmlp_norm_backward",
+    "tpmlp_forward_row_residual", "tpmlp_attn_out_forward_residual", "tpmlp_forward_residual",
+    "tpmlp_forward_ckpt8_residual",
 )
 
 # forms of tpmlp_eval_activation
@@ -208,6 +211,14 @@ def load():
         lib.tpmlp_forward_ckpt8.restype = st
         lib.tpmlp_backward_ckpt8.argtypes = lib.tpmlp_backward_recompute.argtypes
         lib.tpmlp_backward_ckpt8.restype = st
+        lib.tpmlp_forward_row_residual.argtypes = [vp, pp, vp, vp, pp, vp, vp, vp]
+        lib.tpmlp_forward_row_residual.restype = st
+        lib.tpmlp_attn_out_forward_residual.argtypes = [vp, pp, pp, vp, vp, vp, vp]
+        lib.tpmlp_attn_out_forward_residual.restype = st
+        lib.tpmlp_forward_residual.argtypes = [vp, vp, pp, pp, pp, pp, pp, vp, vp, vp, pp, pp, vp, vp]
+        lib.tpmlp_forward_residual.restype = st
+        lib.tpmlp_forward_ckpt8_residual.argtypes = lib.tpmlp_forward_residual.argtypes
+        lib.tpmlp_forward_ckpt8_residual.restype = st
         nd = ctypes.POINTER(NormDesc)
         lib.tpmlp_norm_workspace_size.argtypes = [nd]
         lib.tpmlp_norm_workspace_size.restype = ctypes.c_size_t
@@ -424,6 +435,34 @@ def tpmlp_backward_ckpt8(plan, X, W1, W3, W2, ckpt, H, dY, dact, dX, dW1, dW3, d
                                     _arr(dW2, t), _arr(db1, t), _arr(db3, t3), _addr(db2), _addr(workspace),
                                     _stream(stream)),
         "tpmlp_backward_ckpt8")
+
+
+def tpmlp_forward_row_residual(plan, W2, b2, residual, H, Y, workspace, stream=None):
+    t = _shards(plan)[0]
+    _ok(load().tpmlp_forward_row_residual(plan.handle, _arr(W2, t), _addr(b2), _addr(residual), _arr(H, t), _addr(Y),
+                                          _addr(workspace), _stream(stream)), "tpmlp_forward_row_residual")
+
+
+def tpmlp_attn_out_forward_residual(plan, WO, O, residual, Z, workspace, stream=None):
+    t = plan.t
+    _ok(load().tpmlp_attn_out_forward_residual(plan.handle, _arr(WO, t), _arr(O, t), _addr(residual), _addr(Z),
+                                               _addr(workspace), _stream(stream)), "tpmlp_attn_out_forward_residual")
+
+
+def tpmlp_forward_residual(plan, X, W1, W3, W2, b1, b3, b2, residual, Y, saved, H, workspace, stream=None):
+    t, t3, n = _shards(plan)
+    _ok(load().tpmlp_forward_residual(plan.handle, _addr(X), _arr(W1, t), _arr(W3, t3), _arr(W2, t), _arr(b1, t),
+                                      _arr(b3, t3), _addr(b2), _addr(residual), _addr(Y), _arr(saved, n), _arr(H, t),
+                                      _addr(workspace), _stream(stream)),
+        "tpmlp_forward_residual")
+
+
+def tpmlp_forward_ckpt8_residual(plan, X, W1, W3, W2, b1, b3, b2, residual, Y, ckpt, H, workspace, stream=None):
+    t, t3, n = _shards(plan)
+    _ok(load().tpmlp_forward_ckpt8_residual(plan.handle, _addr(X), _arr(W1, t), _arr(W3, t3), _arr(W2, t), _arr(b1, t),
+                                            _arr(b3, t3), _addr(b2), _addr(residual), _addr(Y), _arr(ckpt, n),
+                                            _arr(H, t), _addr(workspace), _stream(stream)),
+        "tpmlp_forward_ckpt8_residual")
 
 
 def tpmlp_norm_workspace_size(desc: NormDesc) -> int:
@@ -707,6 +746,7 @@ class ShardedMLP:
         p = self.plan
         self._col, self._row = [(p.d, w) for w in p.d_i], [(w, p.d) for w in p.d_i]
         self._wide = [(w,) for w in p.d_i]
+        self._act = [(p.T, w) for w in p.d_i]
         self._ckpt8 = [(tpmlp_ckpt8_size(p.T, w),) for w in p.d_i] * (2 if self.swiglu else 1)
         self._act_bytes = [p.T * w * (2 if dtype == "bf16" else 4) for w in p.d_i]
 
@@ -745,12 +785,37 @@ class ShardedMLP:
         dW2 = [self._empty(w, p.d) for w in p.d_i]
         return dact, dX, dW1, dW3, dW2
 
-    def forward(self, X, W1_i, W2_i, W3_i=None, out=None, stream=None, b1_i=None, b3_i=None, b2=None):
-        """Y = sum_i act(X W1_i + b1_i) W2_i + b2 (biases optional).  Returns (Y, saved, H)."""
+    def forward(self, X, W1_i, W2_i, W3_i=None, out=None, stream=None, b1_i=None, b3_i=None, b2=None,
+                residual=None):
+        """Y = sum_i act(X W1_i + b1_i) W2_i + b2 (biases optional), plus residual [T, d] (optional, may be Y).
+        Returns (Y, saved, H)."""
         self.check_inputs(X, W1_i, W2_i, W3_i)
         Y, saved, H = out if out is not None else self.alloc_forward()
+        if residual is not None:
+            r = _ptr("residual", residual, (self.plan.T, self.plan.d), self.tdtype, self.workspace.device)
+            tpmlp_forward_residual(self.plan, X, W1_i, W3_i, W2_i, b1_i, b3_i, b2, r, Y, saved, H, self.workspace,
+                                   stream)
+            return Y, saved, H
         tpmlp_forward(self.plan, X, W1_i, W3_i, W2_i, b1_i, b3_i, b2, Y, saved, H, self.workspace, stream)
         return Y, saved, H
+
+    def row_forward(self, H_i, W2_i, b2=None, residual=None, out=None, stream=None):
+        """The block's second product alone: sum_i H_i W2_i + b2, plus residual [T, d] (optional); out: the [T, d]
+        tensor to write to, which may be residual."""
+        import torch
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        h, w2 = _ptrs("H_i", H_i, self._act, td, dev), _ptrs("W2_i", W2_i, self._row, td, dev)
+        b2 = _ptr("b2", b2, (p.d,), td, dev) if b2 is not None else None
+        r = _ptr("residual", residual, (p.T, p.d), td, dev) if residual is not None else None
+        with _on(dev, stream):
+            if out is None:
+                out = torch.empty((p.T, p.d), dtype=td, device=dev)
+            y, ws, st = _ptr("out", out, (p.T, p.d), td, dev), self.workspace.data_ptr(), _current(dev)
+            if residual is None:
+                tpmlp_forward_row(p, w2, b2, h, y, ws, st)
+            else:
+                tpmlp_forward_row_residual(p, w2, b2, r, h, y, ws, st)
+        return out
 
     def alloc_bias_grads(self):
         p = self.plan
@@ -781,7 +846,8 @@ class ShardedMLP:
                 _ptrs("W3_i", W3_i, self._col, td, dev) if self.swiglu else None,
                 _ptrs("W2_i", W2_i, self._row, td, dev))
 
-    def forward_ckpt8(self, X, W1_i, W2_i, W3_i=None, stream=None, b1_i=None, b3_i=None, b2=None, out=None):
+    def forward_ckpt8(self, X, W1_i, W2_i, W3_i=None, stream=None, b1_i=None, b3_i=None, b2=None, out=None,
+                      residual=None):
         """forward with the pre-activations kept as 8-bit checkpoints.  Returns (Y, ckpt); out: those two, to write
         to.  H is scratch of the call."""
         import torch
@@ -790,6 +856,7 @@ class ShardedMLP:
         b1 = _ptrs("b1_i", b1_i, self._wide, td, dev) if b1_i is not None else None
         b3 = _ptrs("b3_i", b3_i, self._wide, td, dev) if b3_i is not None and self.swiglu else None
         b2 = _ptr("b2", b2, (p.d,), td, dev) if b2 is not None else None
+        r = _ptr("residual", residual, (p.T, p.d), td, dev) if residual is not None else None
         with _on(dev, stream):
             if out is None:
                 Y = X.new_empty((p.T, p.d))
@@ -800,7 +867,11 @@ class ShardedMLP:
                 y = _ptr("Y", Y, (p.T, p.d), td, dev)
                 c = _ptrs("ckpt", ckpt, self._ckpt8, torch.uint8, dev)
             scratch, H = _pieces(self._act_bytes, dev)
-            tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, y, c, H, self.workspace.data_ptr(), _current(dev))
+            if residual is None:
+                tpmlp_forward_ckpt8(p, x, w1, w3, w2, b1, b3, b2, y, c, H, self.workspace.data_ptr(), _current(dev))
+            else:
+                tpmlp_forward_ckpt8_residual(p, x, w1, w3, w2, b1, b3, b2, r, y, c, H, self.workspace.data_ptr(),
+                                             _current(dev))
         return Y, ckpt
 
     def backward_ckpt8(self, X, W1_i, W2_i, ckpt, dY, W3_i=None, stream=None, bias_grads=False, out=None):
@@ -887,6 +958,7 @@ class ShardedAttentionProj:
         p = self.plan  # shapes of QKV_i, [Q_i | K_i] and V_i
         self._fused, self._v = [(p.T, n) for n in p.d_i], [(p.T, k) for k in p.dkv_i]
         self._qk = [(p.T, q + k) for q, k in zip(p.dq_i, p.dkv_i)]
+        self._o, self._wo = [(p.T, q) for q in p.dq_i], [(q, p.d) for q in p.dq_i]
 
     def _empty(self, *shape):
         import torch
@@ -898,10 +970,26 @@ class ShardedAttentionProj:
         tpmlp_attn_qkv_forward(p, X, Wqkv_i, QKV, self.workspace, stream)
         return QKV
 
-    def out_forward(self, WO_i, O_i, out=None, stream=None):
+    def out_forward(self, WO_i, O_i, out=None, stream=None, residual=None):
+        """Z = sum_i O_i WO_i, plus residual [T, d] (optional, may be out)."""
+        if residual is not None:
+            return self._out_forward_residual(WO_i, O_i, residual, out, stream)
         Z = out if out is not None else self._empty(self.plan.T, self.plan.d)
         tpmlp_attn_out_forward(self.plan, WO_i, O_i, Z, self.workspace, stream)
         return Z
+
+    def _out_forward_residual(self, WO_i, O_i, residual, out, stream):
+        import torch
+        p, td, dev = self.plan, self.tdtype, self.workspace.device
+        shape = (p.T, p.d)
+        wo, o = _ptrs("WO_i", WO_i, self._wo, td, dev), _ptrs("O_i", O_i, self._o, td, dev)
+        r = _ptr("residual", residual, shape, td, dev)
+        with _on(dev, stream):
+            if out is None:
+                out = torch.empty(shape, dtype=td, device=dev)
+            tpmlp_attn_out_forward_residual(p, wo, o, r, _ptr("out", out, shape, td, dev), self.workspace.data_ptr(),
+                                            _current(dev))
+        return out
 
     def out_backward(self, WO_i, O_i, dZ, out=None, stream=None):
         p = self.plan
@@ -1134,6 +1222,43 @@ def _make_checkpoint_function():
     return TPMLPCheckpointFunction
 
 
+def _make_residual_function():
+    import torch
+
+    class TPMLPResidualFunction(torch.autograd.Function):
+        """Y = TPMLPResidualFunction.apply(mlp, X, residual, *W1_i, *W2_i[, *W3_i]): the block's output with the
+        residual stream added in its epilogue, the pre-activations kept as 8-bit checkpoints as by
+        TPMLPCheckpointFunction, with the library's backward.  What that function says of captures holds here too."""
+
+        @staticmethod
+        def forward(ctx, mlp: ShardedMLP, X, residual, *weights):
+            t = mlp.plan.t
+            n = (3 if mlp.swiglu else 2) * t
+            if len(weights) != n:
+                names = "W1_i, W2_i, W3_i" if mlp.swiglu else "W1_i, W2_i"
+                raise ValueError(f"expected {n} weights ({names}), got {len(weights)}")
+            X = X.contiguous()
+            W3_i = list(weights[2 * t:]) if mlp.swiglu else None
+            Y, ckpt = mlp.forward_ckpt8(X, list(weights[:t]), list(weights[t:2 * t]), W3_i,
+                                        residual=residual.contiguous())
+            ctx.mlp, ctx.nw = mlp, n
+            ctx.save_for_backward(X, *weights, *ckpt)
+            return Y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dY):
+            mlp, nw = ctx.mlp, ctx.nw
+            t = mlp.plan.t
+            X, *rest = ctx.saved_tensors
+            weights, ckpt = rest[:nw], rest[nw:]
+            W3_i = weights[2 * t:] if mlp.swiglu else None
+            g = mlp.backward_ckpt8(X, weights[:t], weights[t:2 * t], ckpt, dY.contiguous(), W3_i)
+            return (None, g["dX"], dY, *g["dW1"], *g["dW2"], *(g["dW3"] if mlp.swiglu else []))
+
+    return TPMLPResidualFunction
+
+
 def _make_norm_function():
     import torch
 
@@ -1183,6 +1308,10 @@ class _LazyCheckpointFunction(_LazyFunction):
     _make, _fn = staticmethod(_make_checkpoint_function), None
 
 
+class _LazyResidualFunction(_LazyFunction):
+    _make, _fn = staticmethod(_make_residual_function), None
+
+
 class _LazyNormFunction(_LazyFunction):
     _make, _fn = staticmethod(_make_norm_function), None
 
@@ -1190,3 +1319,4 @@ class _LazyNormFunction(_LazyFunction):
 TPMLPFunction = _LazyFunction()
 TPMLPCheckpointFunction = _LazyCheckpointFunction()
 TPMLPNormFunction = _LazyNormFunction()
+TPMLPResidualFunction = _LazyResidualFunction()

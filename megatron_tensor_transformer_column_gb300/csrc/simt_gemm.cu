@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads) tpmlp_fp32_simt_gemm(const __grid_co
     switch (P.epi) {
       case EPI_STORE:
         if (P.aux0) v += static_cast<const float*>(P.aux0)[col];
+        if (P.aux1) v += static_cast<const float*>(P.aux1)[o];  // the residual stream
         if (P.out_striped) {  // token stripes of the sequence-parallel layout
           const Stripes& st = p.stripes;
           int j = 0;

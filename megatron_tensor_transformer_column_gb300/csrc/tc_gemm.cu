@@ -95,8 +95,9 @@ int tc_gemm_grid_pairs(const GemmParams& p, int kernel_tag, int max_pairs_hint) 
 
 cudaError_t launch_tc_gemm(const GemmParams& p, int kernel_tag, int epi_warps, int max_pairs_hint,
                            cudaStream_t stream) {
-  KernelFn k = p.ckpt8 ? tc_ckpt8_kernel(kernel_tag, p.sk.on != 0, epi_warps)
-                       : kernel_for(kernel_tag, p.sk.on != 0, epi_warps);
+  KernelFn k = p.ckpt8      ? tc_ckpt8_kernel(kernel_tag, p.sk.on != 0, epi_warps)
+               : p.residual ? tc_residual_kernel(kernel_tag, p.sk.on != 0)
+                            : kernel_for(kernel_tag, p.sk.on != 0, epi_warps);
   if (!k) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;

@@ -276,7 +276,9 @@ __device__ __forceinline__ uint32_t stage_off(int r, int g) {
 // Rows grow0 .. grow0 + 31 (valid_rows of them), columns x .. x + N - 1
 // (nvalid of them) of a row-major bf16 array into staging block blk,
 // coalesced: a warp instruction covers 32 / (N / 8) whole rows.
-template <int N>
+// kOnce: of an array that this launch may write as well (each element after its
+// reading, by the same warp): loads that keep nothing in L1.
+template <int N, bool kOnce = false>
 __device__ __forceinline__ void stage_rows(const void* src, int64_t ld, int64_t grow0, int valid_rows, int x,
                                            int nvalid, uint32_t blk, int lane) {
   constexpr int P = N / 8;
@@ -286,8 +288,11 @@ __device__ __forceinline__ void stage_rows(const void* src, int64_t ld, int64_t 
   for (int i = 0; i < P; ++i) {
     const int r = i * RPI + lane / P;
     uint4 q = make_uint4(0, 0, 0, 0);
-    if (r < valid_rows && 8 * g < nvalid)
-      q = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + (grow0 + r) * ld + x + 8 * g));
+    if (r < valid_rows && 8 * g < nvalid) {
+      const uint4* s =
+          reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + (grow0 + r) * ld + x + 8 * g);
+      q = kOnce ? __ldcg(s) : __ldg(s);
+    }
     ptx::st_shared_v4(blk + stage_off<N>(r, g), q);
   }
 }
@@ -546,6 +551,32 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
     default:
       break;
   }
+}
+
+// The plain store of a chunk with the residual stream's block added: it comes in
+// through the block that the sum leaves by.
+template <int N>
+__device__ __forceinline__ void residual_chunk(const GemmParams& p, const Prob& P, EpiStore& es, int64_t grow, int x,
+                                               int y, int nvalid, float (&acc)[N], int lane) {
+  if (y >= es.rows) return;
+  add_bias<N>(P.aux0, x, nvalid, acc);
+  const uint32_t b = es.buf + es.next * epi_block_bytes<N>();
+  if (lane == 0) ptx::bulk_wait_group_read<1>();  // the store that last used block b has read it
+  __syncwarp();
+  stage_rows<N, true>(P.aux1, P.ldo, grow - lane, es.rows - y, x, nvalid, b, lane);
+  __syncwarp();
+  float r[N];
+  read_row<N>(b, lane, r);
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] += r[j];
+  write_row<N>(b, lane, acc);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_2d(&p.maps[P.out_map[0]], b, x, y);
+    ptx::bulk_commit_group();
+  }
+  es.next ^= 1u;
 }
 
 // The same with 8-bit checkpoints for pre-activations: the GeLU column GEMM's

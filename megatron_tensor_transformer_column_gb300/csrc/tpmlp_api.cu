@@ -908,7 +908,7 @@ tpmlp_status fwd_column(const tpmlp_plan* pl, const DeviceInfo& di, const void* 
 
 tpmlp_status fwd_row(const tpmlp_plan* pl, const DeviceInfo& di, const void* const* W2, const void* b2, void* Y,
                      void* const* H, void* ws, cudaStream_t st, void* const* Y_stripes = nullptr,
-                     bool sk_workspace = true) {
+                     bool sk_workspace = true, const void* residual = nullptr) {
   if (pl->T == 0) return TPMLP_OK;
   Builder B(scratch_params(), pl->dtype == TPMLP_BF16);
   if (Y_stripes) {  // reduce-scatter: the summed rows of stripe j go to Y_j
@@ -919,6 +919,8 @@ tpmlp_status fwd_row(const tpmlp_plan* pl, const DeviceInfo& di, const void* con
   Prob& P = B.add_prob(pl->T, pl->d, 256, MAJOR_K, MAJOR_MN, EPI_STORE, pl->d);
   P.out0 = Y;
   P.aux0 = b2;  // added once, after the whole g-sum
+  P.aux1 = residual;
+  B.p->residual = residual != nullptr;
   // g operator: every shard's H_i W2_i accumulates into the same tile.
   for (int i = 0; i < pl->t; ++i) B.add_seg(P, H[i], pl->T, pl->d_i[i], W2[i], pl->d_i[i], pl->d, nullptr, pl->d_i[i]);
   B.end_group();
@@ -1122,12 +1124,14 @@ tpmlp_status attn_qkv_fwd(const tpmlp_plan* pl, const DeviceInfo& di, const void
 }
 
 tpmlp_status attn_out_fwd(const tpmlp_plan* pl, const DeviceInfo& di, const void* const* WO, const void* const* O,
-                          void* Z, void* ws, cudaStream_t st) {
+                          void* Z, void* ws, cudaStream_t st, const void* residual = nullptr) {
   if (pl->T == 0) return TPMLP_OK;
   Builder B(scratch_params(), pl->dtype == TPMLP_BF16);
   B.begin_group(pl->T, band_for(di.sms));
   Prob& P = B.add_prob(pl->T, pl->d, 256, MAJOR_K, MAJOR_MN, EPI_STORE, pl->d);
   P.out0 = Z;
+  P.aux1 = residual;
+  B.p->residual = residual != nullptr;
   // g operator: every shard's O_i WO_i accumulates into the same tile.
   for (int i = 0; i < pl->t; ++i)
     B.add_seg(P, O[i], pl->T, pl->dq_i[i], WO[i], pl->dq_i[i], pl->d, nullptr, pl->dq_i[i]);
@@ -2193,6 +2197,95 @@ tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const void* x, int
     ++g_last_launches;
   }
   return TPMLP_OK;
+}
+
+namespace {
+
+// The residual stream R of a row-parallel product's output: there, and that output itself or apart from it.
+tpmlp_status residual_checks(const tpmlp_plan* plan, const void* residual, const char* name, const void* out) {
+  TPMLP_TRY(check_ptr("residual", residual, plan->T == 0));
+  const int64_t n = plan->T * plan->d * esize(plan);
+  if (residual != out && overlap(residual, n, out, n))
+    return fail(TPMLP_ERR_INVALID_ARG, "%s overlaps residual without being it", name);
+  return TPMLP_OK;
+}
+
+}  // namespace
+
+tpmlp_status tpmlp_forward_row_residual(const tpmlp_plan* plan, const void* const* W2, const void* b2,
+                                        const void* residual, void* const* H, void* Y, void* workspace,
+                                        tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  DeviceInfo di;
+  TPMLP_TRY(common_checks(plan, workspace, &di));
+  const bool tz = plan->T == 0;
+  TPMLP_TRY(check_array("W2", W2, plan->t, false));
+  TPMLP_TRY(check_array("H", H, plan->t, tz));
+  TPMLP_TRY(check_ptr("Y", Y, tz));
+  TPMLP_TRY(check_ptr("b2", b2, true));
+  TPMLP_TRY(residual_checks(plan, residual, "Y", Y));
+  TPMLP_NO_THROW(return fwd_row(plan, di, W2, b2, Y, H, workspace, reinterpret_cast<cudaStream_t>(stream), nullptr,
+                                true, residual);)
+}
+
+tpmlp_status tpmlp_attn_out_forward_residual(const tpmlp_plan* plan, const void* const* WO, const void* const* O,
+                                             const void* residual, void* Z, void* workspace, tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  DeviceInfo di;
+  TPMLP_TRY(common_checks(plan, workspace, &di, PLAN_ATTN));
+  const bool tz = plan->T == 0;
+  TPMLP_TRY(check_array("WO", WO, plan->t, false));
+  TPMLP_TRY(check_array("O", O, plan->t, tz));
+  TPMLP_TRY(check_ptr("Z", Z, tz));
+  TPMLP_TRY(residual_checks(plan, residual, "Z", Z));
+  TPMLP_NO_THROW(return attn_out_fwd(plan, di, WO, O, Z, workspace, reinterpret_cast<cudaStream_t>(stream),
+                                     residual);)
+}
+
+namespace {
+
+tpmlp_status forward_residual(const tpmlp_plan* plan, const void* X, const void* const* W1, const void* const* W3,
+                              const void* const* W2, const void* const* b1, const void* const* b3, const void* b2,
+                              const void* residual, void* Y, void* const* kept, void* const* H, void* workspace,
+                              tpmlp_stream_t stream, bool ckpt8) {
+  g_last_launches = 0;
+  DeviceInfo di;
+  TPMLP_TRY(common_checks(plan, workspace, &di));
+  const bool tz = plan->T == 0;
+  TPMLP_TRY(check_ptr("X", X, tz));
+  TPMLP_TRY(check_ptr("Y", Y, tz));
+  TPMLP_TRY(check_array("W1", W1, plan->t, false));
+  if (swiglu(plan)) TPMLP_TRY(check_array("W3", W3, plan->t, false));
+  TPMLP_TRY(check_array("W2", W2, plan->t, false));
+  TPMLP_TRY(check_array(ckpt8 ? "ckpt" : "saved", kept, nsaved(plan), tz));
+  TPMLP_TRY(check_array("H", H, plan->t, tz));
+  TPMLP_TRY(check_bias("b1", b1, plan->t));
+  if (swiglu(plan)) TPMLP_TRY(check_bias("b3", b3, plan->t));
+  TPMLP_TRY(check_ptr("b2", b2, true));
+  TPMLP_TRY(residual_checks(plan, residual, "Y", Y));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  TPMLP_NO_THROW(
+    TPMLP_TRY(fwd_column(plan, di, X, W1, W3, b1, swiglu(plan) ? b3 : nullptr, kept, H, workspace, st, nullptr,
+                         ckpt8));
+    return fwd_row(plan, di, W2, b2, Y, H, workspace, st, nullptr, true, residual);
+  )
+}
+
+}  // namespace
+
+tpmlp_status tpmlp_forward_residual(const tpmlp_plan* plan, const void* X, const void* const* W1,
+                                    const void* const* W3, const void* const* W2, const void* const* b1,
+                                    const void* const* b3, const void* b2, const void* residual, void* Y,
+                                    void* const* saved, void* const* H, void* workspace, tpmlp_stream_t stream) {
+  return forward_residual(plan, X, W1, W3, W2, b1, b3, b2, residual, Y, saved, H, workspace, stream, false);
+}
+
+tpmlp_status tpmlp_forward_ckpt8_residual(const tpmlp_plan* plan, const void* X, const void* const* W1,
+                                          const void* const* W3, const void* const* W2, const void* const* b1,
+                                          const void* const* b3, const void* b2, const void* residual, void* Y,
+                                          void* const* ckpt, void* const* H, void* workspace,
+                                          tpmlp_stream_t stream) {
+  return forward_residual(plan, X, W1, W3, W2, b1, b3, b2, residual, Y, ckpt, H, workspace, stream, true);
 }
 
 tpmlp_status tpmlp_plan_set_sequence_stripes(tpmlp_plan* plan, int32_t nstripes, const int64_t* stripe_rows) {

@@ -45,7 +45,7 @@ constexpr int kMaxSegs = 5 * kMaxShards + 2;
 // Fused epilogues.  acc is the fp32 accumulator tile; bias vectors are
 // optional (null = none) and indexed by output column.
 enum EpiKind : int32_t {
-  EPI_STORE = 0,       // out0 = acc (+ aux0[n]: b2, added once after the g-sum)
+  EPI_STORE = 0,       // out0 = acc (+ aux0[n]: b2, added once after the g-sum) (+ aux1: the residual stream)
   EPI_GELU_FWD = 1,    // A = acc (+ aux0[n]: b1_i); out0 = A (kept for backward), out1 = H = GeLU(A)
   EPI_SWIGLU_FWD = 2,  // two accumulators (B = W1_i, B2 = W3_i): G = acc_G (+ aux0[n]: b1_i),
                        // U = acc_U (+ aux1[n]: b3_i); out0 = G, out1 = U, out2 = H = U * Swish(G)
@@ -243,6 +243,7 @@ struct GemmParams {
   int32_t* status;          // device status word (workspace)
   uint64_t timeout_ns;      // bound on every wait inside the kernel
   int32_t ckpt8;            // out0 / out1 of the activation forward epilogues and aux0 / aux1 of the backward ones are 8-bit checkpoints
+  int32_t residual;         // the launch's plain stores add the residual stream (aux1)
   int32_t stall_injection;  // test hook: 1, producers load nothing; 2, stream-K parts but a tile's first run late
 };
 
@@ -370,6 +371,8 @@ int tc_epi_warps_for(const GemmParams& p, int kernel_tag);
 // The kernels of the launches with 8-bit checkpoints (column and dgrad).
 using TcKernelFn = void (*)(GemmParams);
 TcKernelFn tc_ckpt8_kernel(int tag, bool stream_k, int epi_warps);
+// Those of the row-parallel launches with the residual stream (8 epilogue warps).
+TcKernelFn tc_residual_kernel(int tag, bool stream_k);
 cudaError_t launch_simt_gemm(const GemmParams& p, cudaStream_t stream);
 // The epilogues' activation forms on plain arrays (tpmlp_eval_activation).
 cudaError_t launch_act_eval(int fn, const float* x, const float* y, const float* dh, float* o0, float* o1,

@@ -114,3 +114,60 @@ def test_norm_workspace(lib):
         norm_bwd(dgain=6 * FAKE, workspace=small)
     with pytest.raises(ValueError):
         tp.TokenNorm(4, 60)
+
+
+# ---------------------------------------------------------------- the residual in the epilogue
+
+def row_call(plan, **kw):
+    a = {"W2": [FAKE], "b2": None, "residual": 2 * FAKE, "H": [3 * FAKE], "Y": 4 * FAKE, "workspace": 5 * FAKE} | kw
+    tp.tpmlp_forward_row_residual(plan, *a.values(), stream=0)
+
+
+def out_call(plan, **kw):
+    a = {"WO": [FAKE], "O": [3 * FAKE], "residual": 2 * FAKE, "Z": 4 * FAKE, "workspace": 5 * FAKE} | kw
+    tp.tpmlp_attn_out_forward_residual(plan, *a.values(), stream=0)
+
+
+def block_call(fn, plan, **kw):
+    a = {"X": 6 * FAKE, "W1": [FAKE], "W3": None, "W2": [FAKE], "b1": None, "b3": None, "b2": None,
+         "residual": 2 * FAKE, "Y": 4 * FAKE, "kept": [7 * FAKE], "H": [3 * FAKE], "workspace": 5 * FAKE} | kw
+    fn(plan, *a.values(), stream=0)
+
+
+def test_residual_refusals(lib):
+    """Without a GPU the first thing that is missed is the device; with one, the argument."""
+    if torch.cuda.is_available():
+        pytest.skip("the calls without a device")
+    mlp, proj = tp.Plan(64, 64, [64]), tp.AttnPlan(64, 64, [64], [64])
+    calls = [lambda p, **kw: row_call(p, **kw)]
+    calls += [lambda p, f=f, **kw: block_call(f, p, **kw) for f in (tp.tpmlp_forward_residual,
+                                                                     tp.tpmlp_forward_ckpt8_residual)]
+    for call in calls:
+        assert status_of(lambda: call(mlp)) == CUDA
+        assert status_of(lambda: call(proj)) == INVALID
+        with pytest.raises(ValueError, match="expected 1"):
+            call(mlp, W2=[])
+    assert status_of(lambda: out_call(proj)) == CUDA
+    assert status_of(lambda: out_call(mlp)) == INVALID
+    assert status_of(lambda: out_call(proj, workspace=None)) == INVALID
+
+
+@pytest.mark.gpu
+def test_residual_refusals_with_a_device(gpu_lib):
+    mlp, proj = tp.Plan(64, 64, [64]), tp.AttnPlan(64, 64, [64], [64])
+    fns = [lambda **kw: row_call(mlp, **kw)]
+    fns += [lambda f=f, **kw: block_call(f, mlp, **kw) for f in (tp.tpmlp_forward_residual,
+                                                                  tp.tpmlp_forward_ckpt8_residual)]
+    for call, out in [(c, "Y") for c in fns] + [(lambda **kw: out_call(proj, **kw), "Z")]:
+        assert status_of(lambda: call(residual=None)) == INVALID
+        assert status_of(lambda: call(residual=2 * FAKE + 8)) == ALIGN
+        assert status_of(lambda: call(residual=4 * FAKE + 16)) == INVALID  # overlaps the output
+        assert status_of(lambda: call(residual=4 * FAKE - 8176)) == INVALID
+        assert status_of(lambda: call(**{out: None})) == INVALID
+    m = tp.ShardedMLP(64, 64, [64])
+    x = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in (x.float(), x[:32], x.t()):
+        with pytest.raises(ValueError, match="residual"):
+            m.row_forward([x], [x], residual=bad)
+        with pytest.raises(ValueError, match="residual"):
+            m.forward(x, [x], [x], residual=bad)
