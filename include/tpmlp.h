@@ -521,6 +521,82 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const vo
                                            const void* dsum, int64_t ldds, void* dx, int64_t lddx, void* dgain,
                                            void* dbias, void* workspace, tpmlp_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * AdamW over many tensors at once, and the gradients' global norm.
+ *
+ * For every element p of every tensor, with its gradient g:
+ *   f = grad_scale, or max_norm / norm where grad_scale norm > max_norm
+ *   m = beta1 m + (1 - beta1) f g,   v = beta2 v + (1 - beta2) (f g)^2
+ *   p = p - lr weight_decay p
+ *         - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32.  A tensor is n elements behind one another (any n, 0 too), its start
+ * 16-byte aligned like every tensor here.  dtype is that of the parameters,
+ * grad_dtype the gradients'.  master (NULL, or an array; bf16 parameters only): an
+ * fp32 copy of each parameter, which is what is updated; the parameter is then
+ * written only, rounded once.  Without masters a bf16 parameter loses what is
+ * below half its last place.
+ *
+ * tpmlp_grad_norm: norm (one fp32, device) = the root of the sum of the squares
+ * of all gradients (without grad_scale), the same on every run; squares in fp32, so
+ * that gradients beyond 10^19 give an infinity.  workspace:
+ * tpmlp_grad_norm_workspace_size() bytes, zero-filled or used by this call before.
+ * tpmlp_adamw_step: norm (device, or NULL for no norm) is what that call wrote.
+ * A norm that is NaN or an infinity skips the step: nothing is written.
+ *
+ * Moments.  TPMLP_ADAMW_32: n fp32 each.  TPMLP_ADAMW_8: groups of 256 elements,
+ * the last one filled up with zeros; M a group's largest magnitude and e =
+ * floor(log2 M), one more where M > 1.875 2^e, at least -90.  A code c stands for
+ * (1 + (c % 8) / 8) 2^(c / 8) 2^(e - S), for 0 if c = 0: m has 7 bits and its sign
+ * in bit 7 (S = 15), v 8 bits (S = 31).  Storage: the groups' 256 codes each, then
+ * a byte e + 91 per group (0: all zero; 255: a NaN, an infinity or more than 2^127
+ * in the group, which comes back as NaN throughout).  Rounding is stochastic: with r,
+ * 16 random bits of the element, the upper one of the two neighbours is taken where
+ * the distance from the lower, over the gap, is at least 1 - r / 2^16.  Below the smallest
+ * code (1.125 2^(e - S)) m is kept as that code where 2^16 |m| > 2^(e - S) 1.125 r, else as
+ * 0, and a v above 0 as that code.  r of element i of a tensor: with h(x) the hash
+ * x = (x ^ x >> 16) 0x7feb352d, x = (x ^ x >> 15) 0x846ca68b, x ^ x >> 16 in 32 bits,
+ * key = h(h(h(h(seed lo) ^ seed hi) ^ t lo) ^ t hi), q the group's number counted
+ * over all tensors, a = h(h(key ^ q lo) ^ q hi), l = i % 256: the low (l even) or high
+ * half of h(a + (l / 2) 0x9e3779b9).  The step itself uses m and v before they are
+ * rounded.  Moments that are all zero bytes are 0, as before the first step.
+ * tpmlp_adamw_state_size: bytes of one moment of n elements (0 for n out of
+ * range).  tpmlp_adamw8_unpack: the values of 8-bit moments, as bf16 (exact); m_out
+ * or v_out may be NULL.
+ *
+ * step is t, from 1 on.  step_device (NULL: none): t is read from this 64-bit
+ * integer on the device instead, and lr_device (NULL: none) likewise, so that a
+ * captured call goes on counting.  weight_decay: one number per tensor, or NULL
+ * for 0.  Outputs (parameters, masters, moments, norm) that overlap one another or
+ * an input are refused (TPMLP_ERR_INVALID_ARG).  One launch per 400 tensors.    */
+typedef enum { TPMLP_ADAMW_32 = 0, TPMLP_ADAMW_8 = 1 } tpmlp_adamw_states;
+typedef struct {
+  int32_t n;              /* tensors, >= 0 */
+  const int64_t* sizes;   /* n numbers of elements (host memory) */
+  tpmlp_dtype dtype;
+  tpmlp_dtype grad_dtype;
+  tpmlp_adamw_states states;
+} tpmlp_adamw_desc;
+typedef struct {
+  double lr, beta1, beta2; /* beta1, beta2 in [0, 1) */
+  double eps;              /* > 0 */
+  double grad_scale;       /* finite */
+  double max_norm;         /* 0: no clipping; needs norm otherwise */
+  int64_t step;            /* >= 1 (not read with step_device) */
+  uint64_t seed;           /* of the 8-bit moments' rounding */
+  const float* lr_device;
+  const int64_t* step_device;
+} tpmlp_adamw_hyper;
+TPMLP_API size_t tpmlp_adamw_state_size(tpmlp_adamw_states states, int64_t n);
+TPMLP_API size_t tpmlp_grad_norm_workspace_size(void);
+TPMLP_API tpmlp_status tpmlp_grad_norm(const tpmlp_adamw_desc* desc, const void* const* g, float* norm,
+                                       void* workspace, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_adamw_step(const tpmlp_adamw_desc* desc, void* const* p, const void* const* g,
+                                        float* const* master, void* const* m, void* const* v,
+                                        const double* weight_decay, const tpmlp_adamw_hyper* hyper,
+                                        const float* norm, tpmlp_stream_t stream);
+TPMLP_API tpmlp_status tpmlp_adamw8_unpack(const tpmlp_adamw_desc* desc, const void* const* m, const void* const* v,
+                                           void* const* m_out, void* const* v_out, tpmlp_stream_t stream);
+
 /* Watchdog controls, for testing the failure path without faulting a GPU.
  * Neither may run while another call uses the plan.
  *   tpmlp_plan_set_timeout: bound, in milliseconds (>= 1), of every wait

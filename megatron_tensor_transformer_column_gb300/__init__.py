@@ -12,7 +12,8 @@ PyTorch (device memory and streams are all PyTorch provides here) and
 ``TPMLPFunction`` wraps forward/backward as a ``torch.autograd.Function``.
 ``ShardedAttentionProj`` does the same for the attention block's QKV and
 output projections (``tpmlp_attn_*``), ``TokenNorm`` for the norm in front of
-a block (``tpmlp_norm_*``, ``TPMLPNormFunction``).
+a block (``tpmlp_norm_*``, ``TPMLPNormFunction``), ``ShardedAdamW`` for the
+step of all weights (``tpmlp_grad_norm``, ``tpmlp_adamw_*``).
 """
 from __future__ import annotations
 
@@ -40,13 +41,16 @@ __all__ = [
     "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8", "ckpt8_pack", "ckpt8_unpack", "TPMLPCheckpointFunction",
     "ROPE_LAYOUT", "NORM", "NormDesc", "tpmlp_norm_workspace_size", "tpmlp_norm_forward", "tpmlp_norm_backward",
     "TokenNorm", "TPMLPNormFunction", "tpmlp_forward_row_residual", "tpmlp_attn_out_forward_residual",
-    "tpmlp_forward_residual", "tpmlp_forward_ckpt8_residual", "TPMLPResidualFunction",
+    "tpmlp_forward_residual", "tpmlp_forward_ckpt8_residual", "TPMLPResidualFunction", "ADAMW_STATES", "AdamWDesc",
+    "AdamWHyper", "tpmlp_adamw_state_size", "tpmlp_grad_norm_workspace_size", "tpmlp_grad_norm", "tpmlp_adamw_step",
+    "tpmlp_adamw8_unpack", "ShardedAdamW",
 ]
 
 ACT = {"gelu": 0, "swiglu": 1}
 DTYPE = {"bf16": 0, "fp32": 1}
 ROPE_LAYOUT = {"halves": 0, "pairs": 1}
 NORM = {"layer": 0, "rms": 1}
+ADAMW_STATES = {32: 0, 8: 1}  # by the bits of a moment
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_INVALID_ARG", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_ALIGNMENT",
           4: "TPMLP_ERR_UNSUPPORTED", 5: "TPMLP_ERR_CUDA", 6: "TPMLP_ERR_DEVICE_TIMEOUT",
           7: "TPMLP_ERR_NOT_IMPLEMENTED"}
@@ -64,7 +68,8 @@ EXPORTED_SYMBOLS = (
     "tpmlp_ckpt8_size", "tpmlp_ckpt8_pack", "tpmlp_ckpt8_unpack", "tpmlp_forward_ckpt8", "tpmlp_backward_ckpt8",
     "tpmlp_norm_workspace_size", "tpmlp_norm_forward", "tpmlp_norm_backward",
     "tpmlp_forward_row_residual", "tpmlp_attn_out_forward_residual", "tpmlp_forward_residual",
-    "tpmlp_forward_ckpt8_residual",
+    "tpmlp_forward_ckpt8_residual", "tpmlp_adamw_state_size", "tpmlp_grad_norm_workspace_size", "tpmlp_grad_norm",
+    "tpmlp_adamw_step", "tpmlp_adamw8_unpack",
 )
 
 # forms of tpmlp_eval_activation
@@ -112,6 +117,32 @@ class NormDesc(ctypes.Structure):
     def __init__(self, rows, cols, kind="layer", dtype="bf16", eps=1e-5):
         super().__init__(int(rows), int(cols), NORM[kind] if isinstance(kind, str) else int(kind),
                          DTYPE[dtype] if isinstance(dtype, str) else int(dtype), float(eps))
+
+
+class AdamWDesc(ctypes.Structure):
+    """The ``tpmlp_adamw_desc`` of tensors of these numbers of elements; dtypes: keys of DTYPE, bits: of a moment."""
+    _fields_ = [("n", ctypes.c_int32), ("sizes", ctypes.POINTER(ctypes.c_int64)), ("dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("states", ctypes.c_int)]
+
+    def __init__(self, sizes, dtype="bf16", grad_dtype=None, bits=32):
+        grad_dtype = dtype if grad_dtype is None else grad_dtype
+        self._sizes = (ctypes.c_int64 * max(1, len(sizes)))(*[int(n) for n in sizes])
+        super().__init__(len(sizes), ctypes.cast(self._sizes, ctypes.POINTER(ctypes.c_int64)),
+                         DTYPE[dtype] if isinstance(dtype, str) else int(dtype),
+                         DTYPE[grad_dtype] if isinstance(grad_dtype, str) else int(grad_dtype),
+                         ADAMW_STATES.get(bits, -1))
+
+
+class AdamWHyper(ctypes.Structure):
+    """The ``tpmlp_adamw_hyper`` of a step; lr_device, step_device: device addresses or None."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double), ("max_norm", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("lr_device", ctypes.c_void_p),
+                ("step_device", ctypes.c_void_p)]
+
+    def __init__(self, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=1.0, max_norm=0.0, step=1, seed=0,
+                 lr_device=None, step_device=None):
+        super().__init__(lr, beta1, beta2, eps, grad_scale, max_norm, step, seed, lr_device, step_device)
 
 
 _lib = None
@@ -219,6 +250,18 @@ def load():
         lib.tpmlp_forward_residual.restype = st
         lib.tpmlp_forward_ckpt8_residual.argtypes = lib.tpmlp_forward_residual.argtypes
         lib.tpmlp_forward_ckpt8_residual.restype = st
+        ad = ctypes.POINTER(AdamWDesc)
+        lib.tpmlp_adamw_state_size.argtypes = [i32, i64]
+        lib.tpmlp_adamw_state_size.restype = ctypes.c_size_t
+        lib.tpmlp_grad_norm_workspace_size.argtypes = []
+        lib.tpmlp_grad_norm_workspace_size.restype = ctypes.c_size_t
+        lib.tpmlp_grad_norm.argtypes = [ad, pp, vp, vp, vp]
+        lib.tpmlp_grad_norm.restype = st
+        lib.tpmlp_adamw_step.argtypes = [ad, pp, pp, pp, pp, pp, ctypes.POINTER(ctypes.c_double),
+                                         ctypes.POINTER(AdamWHyper), vp, vp]
+        lib.tpmlp_adamw_step.restype = st
+        lib.tpmlp_adamw8_unpack.argtypes = [ad, pp, pp, pp, pp, vp]
+        lib.tpmlp_adamw8_unpack.restype = st
         nd = ctypes.POINTER(NormDesc)
         lib.tpmlp_norm_workspace_size.argtypes = [nd]
         lib.tpmlp_norm_workspace_size.restype = ctypes.c_size_t
@@ -483,6 +526,37 @@ def tpmlp_norm_backward(desc, x, ldx, stats, gain, dy, lddy, dsum, ldds, dx, ldd
     _ok(load().tpmlp_norm_backward(ctypes.byref(desc), _addr(x), ldx, _addr(stats), _addr(gain), _addr(dy), lddy,
                                    _addr(dsum), ldds, _addr(dx), lddx, _addr(dgain), _addr(dbias), _addr(workspace),
                                    _stream(stream)), "tpmlp_norm_backward")
+
+
+def tpmlp_adamw_state_size(bits: int, n: int) -> int:
+    """Bytes of one moment of n elements."""
+    return int(load().tpmlp_adamw_state_size(ADAMW_STATES.get(bits, -1), int(n)))
+
+
+def tpmlp_grad_norm_workspace_size() -> int:
+    return int(load().tpmlp_grad_norm_workspace_size())
+
+
+def tpmlp_grad_norm(desc, g, norm, workspace, stream=None):
+    _ok(load().tpmlp_grad_norm(ctypes.byref(desc), _arr(g, desc.n), _addr(norm), _addr(workspace), _stream(stream)),
+        "tpmlp_grad_norm")
+
+
+def tpmlp_adamw_step(desc, p, g, master, m, v, weight_decay, hyper, norm, stream=None):
+    """weight_decay: one number per tensor, or None."""
+    n = desc.n
+    if weight_decay is not None and not isinstance(weight_decay, ctypes.Array):
+        weight_decay = (ctypes.c_double * len(weight_decay))(*weight_decay)
+    if weight_decay is not None and len(weight_decay) < n:
+        raise ValueError(f"expected {n} weight decays, got {len(weight_decay)}")
+    _ok(load().tpmlp_adamw_step(ctypes.byref(desc), _arr(p, n), _arr(g, n), _arr(master, n), _arr(m, n), _arr(v, n),
+                                weight_decay, ctypes.byref(hyper), _addr(norm), _stream(stream)), "tpmlp_adamw_step")
+
+
+def tpmlp_adamw8_unpack(desc, m, v, m_out, v_out, stream=None):
+    n = desc.n
+    _ok(load().tpmlp_adamw8_unpack(ctypes.byref(desc), _arr(m, n), _arr(v, n), _arr(m_out, n), _arr(v_out, n),
+                                   _stream(stream)), "tpmlp_adamw8_unpack")
 
 
 def tpmlp_plan_set_sequence_stripes(plan: Plan, stripe_rows: Sequence[int]):
@@ -1144,6 +1218,123 @@ class TokenNorm:
                                 dgain.data_ptr() if gain_grad else None, dbias.data_ptr() if bias_grad else None,
                                 self.workspace.data_ptr(), _current(dev))
         return dx, dgain, dbias
+
+
+class ShardedAdamW:
+    """AdamW over all of a program's tensors at once: the shards' weights, gains, biases.
+
+    params: contiguous CUDA tensors of one dtype (bf16 or fp32) and device, updated in place.  bits: of a moment, 32 (fp32
+    tensors) or 8 (uint8 buffers in the format of include/tpmlp.h).  master: fp32 copies of bf16 parameters, a list or
+    True to make them.  weight_decay: a number, or one per tensor.  max_norm: the gradients' global norm is computed and
+    clipped to it (None: no norm; inf: computed, but not clipped); where it is not finite the step changes nothing, but
+    counts.
+    seed: of the 8-bit moments' rounding.  capturable: the step's number and the learning rate are kept on the
+    device (step_device, lr_device), so that a captured step goes on counting; without it a capture is refused."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, bits=32, master=None,
+                 max_norm=None, seed=0, capturable=False):
+        import torch
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no tensors")
+        x = self.params[0]
+        names = {torch.bfloat16: "bf16", torch.float32: "fp32"}
+        if x.dtype not in names or not x.is_cuda:
+            raise ValueError(f"expected bf16 or fp32 CUDA tensors, got {x.dtype} on {x.device}")
+        if bits not in ADAMW_STATES:
+            raise ValueError(f"bits: expected 8 or 32, got {bits}")
+        self.tdtype, self.device, self.bits, self.names = x.dtype, x.device, bits, names
+        self.shapes, self.sizes = [p.shape for p in self.params], [p.numel() for p in self.params]
+        self.lr, self.betas, self.eps, self.max_norm = lr, betas, eps, max_norm
+        self.seed, self.capturable = int(seed), capturable
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError(f"max_norm: expected a positive number or None, got {max_norm}")
+        n = len(self.sizes)
+        decay = [weight_decay] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != n:
+            raise ValueError(f"weight_decay: expected {n} numbers, got {len(decay)}")
+        self._decay = (ctypes.c_double * n)(*decay)
+        self._descs = {g: AdamWDesc(self.sizes, names[self.tdtype], names[g], bits) for g in names}
+        _ptrs("params", self.params, self.shapes, self.tdtype, self.device)
+        if master is True:
+            master = [p.detach().float() for p in self.params]
+        self.master = list(master) if master else None
+        self._master = _ptrs("master", self.master, self.shapes, torch.float32, self.device) if master else None
+        if master and self.tdtype != torch.bfloat16:
+            raise ValueError("masters of fp32 parameters")
+        self._moment_shapes = self.shapes if bits == 32 else [(tpmlp_adamw_state_size(8, k),) for k in self.sizes]
+        dt = torch.float32 if bits == 32 else torch.uint8
+        zeros = lambda: [torch.zeros(s, dtype=dt, device=self.device) for s in self._moment_shapes]
+        self._steps = 0
+        if capturable:
+            self.step_device = torch.zeros((), dtype=torch.int64, device=self.device)
+            self.lr_device = torch.tensor(float(lr), dtype=torch.float32, device=self.device)
+        self.workspace = torch.zeros(tpmlp_grad_norm_workspace_size(), dtype=torch.uint8, device=self.device)
+        self.load_moments(zeros(), zeros())
+
+    @property
+    def steps(self) -> int:
+        """Steps done."""
+        return int(self.step_device) if self.capturable else self._steps
+
+    def load_moments(self, m, v, steps=0):
+        """Takes these tensors as the moments, in the form that self.m and self.v have, after that many steps."""
+        import torch
+        dt = torch.float32 if self.bits == 32 else torch.uint8
+        m, v = list(m), list(v)
+        self._m = _ptrs("m", m, self._moment_shapes, dt, self.device)
+        self._v = _ptrs("v", v, self._moment_shapes, dt, self.device)
+        self.m, self.v, self._steps = m, v, int(steps)
+        if self.capturable:
+            self.step_device.fill_(self._steps)
+
+    def step(self, grads=None, lr=None, grad_scale=1.0, stream=None):
+        """One step with these gradients (None: the parameters' .grad), bf16 or fp32, all of one dtype.  lr: this step's
+        and the later ones'.  Returns the gradients' norm (a device scalar, before grad_scale), None without max_norm."""
+        import torch
+        if grads is None:
+            grads = [p.grad for p in self.params]
+            if any(g is None for g in grads):
+                raise ValueError("a parameter has no .grad")
+        if len(grads) != len(self.shapes):
+            raise ValueError(f"grads: expected {len(self.shapes)} tensors, got {len(grads)}")
+        gd = grads[0].dtype
+        if gd not in self._descs:
+            raise ValueError(f"grads: expected bf16 or fp32, got {gd}")
+        desc = self._descs[gd]
+        p = _ptrs("params", self.params, self.shapes, self.tdtype, self.device)
+        g = _ptrs("grads", grads, self.shapes, gd, self.device)
+        if lr is not None:
+            if self.capturable:
+                raise ValueError("capturable: write the learning rate to lr_device")
+            self.lr = lr
+        with _on(self.device, stream):
+            if not self.capturable and torch.cuda.is_current_stream_capturing():
+                raise ValueError("a captured step would repeat one step's number: capturable=True counts on the device")
+            st, norm = _current(self.device), None
+            h = AdamWHyper(self.lr, *self.betas, self.eps, grad_scale, 0.0, self._steps + 1, self.seed)
+            if self.max_norm is not None:
+                norm = torch.empty((), dtype=torch.float32, device=self.device)
+                h.max_norm = self.max_norm
+                tpmlp_grad_norm(desc, g, norm.data_ptr(), self.workspace.data_ptr(), st)
+            if self.capturable:
+                self.step_device.add_(1)
+                h.lr_device, h.step_device = self.lr_device.data_ptr(), self.step_device.data_ptr()
+            tpmlp_adamw_step(desc, p, g, self._master, self._m, self._v, self._decay, h,
+                             None if norm is None else norm.data_ptr(), st)
+        self._steps += 1
+        return norm
+
+    def moments(self, stream=None):
+        """(m, v): the first and second moments in the parameters' shapes, the fp32 tensors themselves, or, of 8-bit
+        moments, new bf16 tensors (which hold their values exactly)."""
+        import torch
+        if self.bits == 32:
+            return self.m, self.v
+        with _on(self.device, stream):
+            m, v = ([torch.empty(s, dtype=torch.bfloat16, device=self.device) for s in self.shapes] for _ in "mv")
+            tpmlp_adamw8_unpack(self._descs[self.tdtype], self._m, self._v, m, v, _current(self.device))
+        return m, v
 
 
 def _make_function():

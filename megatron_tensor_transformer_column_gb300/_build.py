@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtpmlp.so")
 SOURCES = ["tpmlp_api.cu", "tc_gemm.cu", "tc_gemm_ckpt8.cu", "tc_gemm_residual.cu", "simt_gemm.cu", "qk_norm_rope.cu",
-           "token_norm.cu", "ckpt8.cu", "colsum.cu", "act_eval.cu"]
+           "token_norm.cu", "adamw.cu", "ckpt8.cu", "colsum.cu", "act_eval.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

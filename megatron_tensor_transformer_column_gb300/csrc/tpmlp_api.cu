@@ -1922,9 +1922,9 @@ tpmlp_status tpmlp_ckpt8_unpack(tpmlp_dtype dtype, int64_t rows, int64_t cols, c
 
 // No C++ exception leaves a C entry point: the planner's tables are host memory
 // that may run out.
-#define TPMLP_NO_THROW(body)                                              \
+#define TPMLP_NO_THROW(...)                                               \
   try {                                                                   \
-    body                                                                  \
+    __VA_ARGS__                                                           \
   } catch (...) {                                                         \
     return fail(TPMLP_ERR_INVALID_ARG, "out of host memory");             \
   }
@@ -2286,6 +2286,276 @@ tpmlp_status tpmlp_forward_ckpt8_residual(const tpmlp_plan* plan, const void* X,
                                           void* const* ckpt, void* const* H, void* workspace,
                                           tpmlp_stream_t stream) {
   return forward_residual(plan, X, W1, W3, W2, b1, b3, b2, residual, Y, ckpt, H, workspace, stream, true);
+}
+
+namespace {
+
+constexpr int64_t kMaxTensor = int64_t(1) << 40;  // elements, past any memory
+
+AdamParams* adam_params() {
+  thread_local AdamParams* params = nullptr;
+  if (!params) params = new AdamParams;
+  std::memset(static_cast<void*>(params), 0, sizeof(AdamParams));
+  return params;
+}
+
+int64_t adam_groups(int64_t n) { return (n + kAdamGroup - 1) / kAdamGroup; }
+int64_t moment_bytes(tpmlp_adamw_states states, int64_t n) {
+  return states == TPMLP_ADAMW_8 ? adam_groups(n) * (kAdamGroup + 1) : 4 * n;
+}
+
+tpmlp_status adamw_desc_checks(const tpmlp_adamw_desc* d) {
+  g_last_error[0] = 0;
+  if (!d) return fail(TPMLP_ERR_INVALID_ARG, "desc is NULL");
+  for (tpmlp_dtype t : {d->dtype, d->grad_dtype})
+    if (t != TPMLP_BF16 && t != TPMLP_FP32) return fail(TPMLP_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(t));
+  if (d->states != TPMLP_ADAMW_32 && d->states != TPMLP_ADAMW_8)
+    return fail(TPMLP_ERR_INVALID_ARG, "unknown states %d", static_cast<int>(d->states));
+  if (d->n < 0) return fail(TPMLP_ERR_SHAPE, "n = %d tensors", d->n);
+  if (d->n && !d->sizes) return fail(TPMLP_ERR_INVALID_ARG, "sizes is NULL");
+  for (int k = 0; k < d->n; ++k)
+    if (d->sizes[k] < 0 || d->sizes[k] > kMaxTensor)
+      return fail(TPMLP_ERR_SHAPE, "sizes[%d] = %lld is not in [0, 2^40]", k, static_cast<long long>(d->sizes[k]));
+  return TPMLP_OK;
+}
+
+// An array of n pointers, those of empty tensors not looked at.
+tpmlp_status check_tensors(const char* name, const void* const* arr, const tpmlp_adamw_desc* d) {
+  if (!arr) return d->n ? fail(TPMLP_ERR_INVALID_ARG, "pointer array %s is NULL", name) : TPMLP_OK;
+  for (int k = 0; k < d->n; ++k) {
+    if (!d->sizes[k]) continue;
+    if (!arr[k]) return fail(TPMLP_ERR_INVALID_ARG, "%s[%d] is NULL", name, k);
+    if (!aligned16(arr[k])) return fail(TPMLP_ERR_ALIGNMENT, "%s[%d] (%p) is not 16-byte aligned", name, k, arr[k]);
+  }
+  return TPMLP_OK;
+}
+
+// Refuses an output that overlaps another array.  One sort over all of them.
+struct Spans {
+  struct Span {
+    uintptr_t at, end;
+    const char* name;
+    int k;
+    bool out;
+  };
+  std::vector<Span> all;
+  void add(const char* name, int k, const void* p, int64_t bytes, bool out) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes > 0) all.push_back({at, at + static_cast<uintptr_t>(bytes), name, k, out});
+  }
+  tpmlp_status check() {
+    std::sort(all.begin(), all.end(), [](const Span& a, const Span& b) { return a.at < b.at; });
+    const Span *any = nullptr, *out = nullptr;  // those that reach furthest so far
+    for (const Span& s : all) {
+      const Span* hit = s.out ? any : out;
+      if (hit && s.at < hit->end)
+        return fail(TPMLP_ERR_INVALID_ARG, "%s[%d] overlaps %s[%d]", s.name, s.k, hit->name, hit->k);
+      if (!any || s.end > any->end) any = &s;
+      if (s.out && (!out || s.end > out->end)) out = &s;
+    }
+    return TPMLP_OK;
+  }
+};
+
+uint32_t adam_hash(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x7feb352du;
+  x = (x ^ (x >> 15)) * 0x846ca68bu;
+  return x ^ (x >> 16);
+}
+
+tpmlp_status adamw_hyper_checks(const tpmlp_adamw_hyper* h, bool has_norm) {
+  if (!h) return fail(TPMLP_ERR_INVALID_ARG, "hyper is NULL");
+  if (!h->lr_device && !std::isfinite(h->lr)) return fail(TPMLP_ERR_INVALID_ARG, "lr = %g is not finite", h->lr);
+  for (double b : {h->beta1, h->beta2})
+    if (!(b >= 0.0 && b < 1.0)) return fail(TPMLP_ERR_INVALID_ARG, "beta1, beta2: %g is not in [0, 1)", b);
+  if (!(h->eps > 0.0 && std::isfinite(h->eps))) return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive number", h->eps);
+  if (!std::isfinite(h->grad_scale)) return fail(TPMLP_ERR_INVALID_ARG, "grad_scale = %g is not finite", h->grad_scale);
+  if (!(h->max_norm >= 0.0)) return fail(TPMLP_ERR_INVALID_ARG, "max_norm = %g is below 0", h->max_norm);
+  if (h->max_norm > 0.0 && !has_norm) return fail(TPMLP_ERR_INVALID_ARG, "max_norm without a norm");
+  if (!h->step_device && h->step < 1)
+    return fail(TPMLP_ERR_INVALID_ARG, "step = %lld is below 1", static_cast<long long>(h->step));
+  if ((reinterpret_cast<uintptr_t>(h->step_device) & 7u) || (reinterpret_cast<uintptr_t>(h->lr_device) & 3u))
+    return fail(TPMLP_ERR_ALIGNMENT, "step_device or lr_device is not aligned to its size");
+  return TPMLP_OK;
+}
+
+}  // namespace
+
+size_t tpmlp_adamw_state_size(tpmlp_adamw_states states, int64_t n) {
+  if ((states != TPMLP_ADAMW_32 && states != TPMLP_ADAMW_8) || n < 0 || n > kMaxTensor) return 0;
+  return static_cast<size_t>(moment_bytes(states, n));
+}
+
+size_t tpmlp_grad_norm_workspace_size(void) { return kStatusBytes + (kAdamNormCtas + 1) * sizeof(double); }
+
+tpmlp_status tpmlp_grad_norm(const tpmlp_adamw_desc* desc, const void* const* g, float* norm, void* workspace,
+                             tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(adamw_desc_checks(desc));
+  TPMLP_TRY(check_tensors("g", g, desc));
+  if (!norm) return fail(TPMLP_ERR_INVALID_ARG, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(TPMLP_ERR_ALIGNMENT, "norm is not 4-byte aligned");
+  TPMLP_TRY(check_ptr("workspace", workspace, false));
+  const int64_t es = desc->grad_dtype == TPMLP_BF16 ? 2 : 4;
+  TPMLP_NO_THROW(
+    Spans spans;
+    spans.all.reserve(desc->n + 2);
+    for (int k = 0; k < desc->n; ++k) spans.add("g", k, g[k], desc->sizes[k] * es, false);
+    spans.add("norm", 0, norm, sizeof(float), true);
+    spans.add("workspace", 0, workspace, static_cast<int64_t>(tpmlp_grad_norm_workspace_size()), true);
+    TPMLP_TRY(spans.check());
+    DeviceInfo di;
+    TPMLP_TRY(device_info(&di));
+    AdamParams& a = *adam_params();
+    a.first_batch = 1;
+    int k = 0;
+    do {
+      a.n = 0;
+      for (; k < desc->n && a.n < kAdamTensors; ++k)
+        if (desc->sizes[k]) {
+          AdamTensor& t = a.t[a.n++];
+          t.g = g[k];
+          t.n = desc->sizes[k];
+        }
+      a.more = k < desc->n;
+      cudaError_t e = launch_grad_norm(a, desc->grad_dtype == TPMLP_BF16, workspace, norm, di.sms,
+                                       reinterpret_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e);
+      ++g_last_launches;
+      a.first_batch = 0;
+    } while (k < desc->n);
+    return TPMLP_OK;
+  )
+}
+
+tpmlp_status tpmlp_adamw_step(const tpmlp_adamw_desc* desc, void* const* p, const void* const* g,
+                              float* const* master, void* const* m, void* const* v, const double* weight_decay,
+                              const tpmlp_adamw_hyper* hyper, const float* norm, tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(adamw_desc_checks(desc));
+  const bool bf16 = desc->dtype == TPMLP_BF16;
+  TPMLP_TRY(check_tensors("p", p, desc));
+  TPMLP_TRY(check_tensors("g", g, desc));
+  if (master) {
+    if (!bf16) return fail(TPMLP_ERR_INVALID_ARG, "masters of fp32 parameters");
+    TPMLP_TRY(check_tensors("master", reinterpret_cast<const void* const*>(master), desc));
+  }
+  TPMLP_TRY(check_tensors("m", m, desc));
+  TPMLP_TRY(check_tensors("v", v, desc));
+  TPMLP_TRY(adamw_hyper_checks(hyper, norm != nullptr));
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(TPMLP_ERR_ALIGNMENT, "norm is not 4-byte aligned");
+  for (int k = 0; weight_decay && k < desc->n; ++k)
+    if (!std::isfinite(weight_decay[k])) return fail(TPMLP_ERR_INVALID_ARG, "weight_decay[%d] is not finite", k);
+  const int64_t es = bf16 ? 2 : 4, gs = desc->grad_dtype == TPMLP_BF16 ? 2 : 4;
+  TPMLP_NO_THROW(
+    Spans spans;
+    spans.all.reserve(5 * static_cast<size_t>(desc->n) + 3);
+    for (int k = 0; k < desc->n; ++k) {
+      const int64_t n = desc->sizes[k], mb = moment_bytes(desc->states, n);
+      spans.add("p", k, p[k], n * es, true);
+      spans.add("g", k, g[k], n * gs, false);
+      if (master) spans.add("master", k, master[k], 4 * n, true);
+      spans.add("m", k, m[k], mb, true);
+      spans.add("v", k, v[k], mb, true);
+    }
+    spans.add("norm", 0, norm, sizeof(float), false);
+    spans.add("lr_device", 0, hyper->lr_device, sizeof(float), false);
+    spans.add("step_device", 0, hyper->step_device, sizeof(int64_t), false);
+    TPMLP_TRY(spans.check());
+    DeviceInfo di;
+    TPMLP_TRY(device_info(&di));
+    AdamParams& a = *adam_params();
+    const double t = static_cast<double>(hyper->step);
+    a.ln_b1 = std::log(hyper->beta1);
+    a.ln_b2 = std::log(hyper->beta2);
+    a.norm = norm;
+    a.lr_dev = hyper->lr_device;
+    a.step_dev = hyper->step_device;
+    a.b1 = static_cast<float>(hyper->beta1);
+    a.b1c = static_cast<float>(1.0 - hyper->beta1);
+    a.b2 = static_cast<float>(hyper->beta2);
+    a.b2c = static_cast<float>(1.0 - hyper->beta2);
+    a.lr = static_cast<float>(hyper->lr);
+    a.eps = static_cast<float>(hyper->eps);
+    a.grad_scale = static_cast<float>(hyper->grad_scale);
+    a.max_norm = static_cast<float>(hyper->max_norm);
+    a.key = adam_hash(adam_hash(static_cast<uint32_t>(hyper->seed)) ^ static_cast<uint32_t>(hyper->seed >> 32));
+    if (!a.step_dev) {
+      a.rate = static_cast<float>(1.0 / -std::expm1(t * a.ln_b1));
+      a.c2 = static_cast<float>(1.0 / std::sqrt(-std::expm1(t * a.ln_b2)));
+      const uint64_t step = static_cast<uint64_t>(hyper->step);
+      a.key = adam_hash(adam_hash(a.key ^ static_cast<uint32_t>(step)) ^ static_cast<uint32_t>(step >> 32));
+    }
+    int64_t group = 0;
+    for (int k = 0; k < desc->n;) {
+      a.n = 0;
+      for (; k < desc->n && a.n < kAdamTensors; ++k) {
+        if (!desc->sizes[k]) continue;
+        AdamTensor& x = a.t[a.n++];
+        x.p = p[k];
+        x.g = g[k];
+        x.master = master ? master[k] : nullptr;
+        x.m = m[k];
+        x.v = v[k];
+        x.n = desc->sizes[k];
+        x.group0 = group;
+        x.decay = weight_decay ? static_cast<float>(weight_decay[k]) : 0.0f;
+        group += adam_groups(x.n);
+      }
+      if (!a.n) break;
+      cudaError_t e = launch_adamw(a, bf16, desc->grad_dtype == TPMLP_BF16, desc->states == TPMLP_ADAMW_8,
+                                   reinterpret_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e);
+      ++g_last_launches;
+    }
+    return TPMLP_OK;
+  )
+}
+
+tpmlp_status tpmlp_adamw8_unpack(const tpmlp_adamw_desc* desc, const void* const* m, const void* const* v,
+                                 void* const* m_out, void* const* v_out, tpmlp_stream_t stream) {
+  g_last_launches = 0;
+  TPMLP_TRY(adamw_desc_checks(desc));
+  if (desc->states != TPMLP_ADAMW_8) return fail(TPMLP_ERR_INVALID_ARG, "the moments are not in 8 bits");
+  if (m_out) {
+    TPMLP_TRY(check_tensors("m", m, desc));
+    TPMLP_TRY(check_tensors("m_out", m_out, desc));
+  }
+  if (v_out) {
+    TPMLP_TRY(check_tensors("v", v, desc));
+    TPMLP_TRY(check_tensors("v_out", v_out, desc));
+  }
+  if (!m_out && !v_out) return TPMLP_OK;
+  TPMLP_NO_THROW(
+    Spans spans;
+    spans.all.reserve(4 * static_cast<size_t>(desc->n));
+    for (int k = 0; k < desc->n; ++k) {
+      const int64_t n = desc->sizes[k], mb = moment_bytes(TPMLP_ADAMW_8, n);
+      if (m_out) spans.add("m", k, m[k], mb, false), spans.add("m_out", k, m_out[k], 2 * n, true);
+      if (v_out) spans.add("v", k, v[k], mb, false), spans.add("v_out", k, v_out[k], 2 * n, true);
+    }
+    TPMLP_TRY(spans.check());
+    DeviceInfo di;
+    TPMLP_TRY(device_info(&di));
+    AdamParams& a = *adam_params();
+    for (int k = 0; k < desc->n;) {
+      a.n = 0;
+      for (; k < desc->n && a.n < kAdamTensors; ++k) {
+        if (!desc->sizes[k]) continue;
+        AdamTensor& x = a.t[a.n++];
+        x.m = m_out ? const_cast<void*>(m[k]) : nullptr;
+        x.v = v_out ? const_cast<void*>(v[k]) : nullptr;
+        x.p = m_out ? m_out[k] : nullptr;
+        x.master = v_out ? static_cast<float*>(v_out[k]) : nullptr;
+        x.n = desc->sizes[k];
+      }
+      if (!a.n) break;
+      cudaError_t e = launch_adamw8_unpack(a, reinterpret_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e);
+      ++g_last_launches;
+    }
+    return TPMLP_OK;
+  )
 }
 
 tpmlp_status tpmlp_plan_set_sequence_stripes(tpmlp_plan* plan, int32_t nstripes, const int64_t* stripe_rows) {

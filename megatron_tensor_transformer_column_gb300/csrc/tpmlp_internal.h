@@ -337,6 +337,40 @@ struct NormParams {
 cudaError_t launch_norm(NormParams& p, bool bf16, bool bwd, int sms, cudaStream_t stream);
 cudaError_t launch_norm_gain_grad(const NormParams& p, bool bf16, void* dgain, void* dbias, cudaStream_t stream);
 
+// AdamW over many tensors and the norm of their gradients (adamw.cu).
+constexpr int kAdamTensors = 400;    // of a launch
+constexpr int kAdamGroup = 256;      // elements of a group of 8-bit moments
+constexpr int kAdamNormCtas = 1280;  // bound of a norm launch's CTAs: its partial sums
+struct AdamTensor {
+  void* p;
+  const void* g;
+  float* master;   // or null
+  void* m;         // fp32, or a group's 256 codes after the other's, then a scale byte each
+  void* v;
+  int64_t n;
+  int64_t group0;  // groups in the tensors before it
+  float decay;
+  int32_t end;     // chunks up to its end (set by the launcher)
+};
+struct AdamParams {
+  AdamTensor t[kAdamTensors];
+  double ln_b1, ln_b2;
+  const float* norm;        // or null
+  const float* lr_dev;      // or null: lr
+  const int64_t* step_dev;  // or null: rate, c2 and key are those of the step
+  float b1, b1c, b2, b2c;   // b1c: 1 - b1
+  float lr, rate, c2, eps;  // rate = 1 / (1 - b1^t), c2 = (1 - b2^t)^(-1/2)
+  float grad_scale, max_norm;
+  uint32_t key;
+  int32_t n;
+  int32_t first_batch, more;  // of a norm in several launches
+};
+static_assert(sizeof(AdamParams) <= 32000, "kernel parameter block too large");
+cudaError_t launch_adamw(AdamParams& a, bool bf16, bool grad_bf16, bool bits8, cudaStream_t stream);
+cudaError_t launch_adamw8_unpack(AdamParams& a, cudaStream_t stream);
+cudaError_t launch_grad_norm(AdamParams& a, bool grad_bf16, void* workspace, float* norm, int sms,
+                             cudaStream_t stream);
+
 // Kernel parameters live in the 32 KB parameter space (__grid_constant__).
 static_assert(sizeof(GemmParams) <= 32000, "kernel parameter block too large");
 
