@@ -26,11 +26,19 @@
 
 #include <algorithm>
 
+#include "act.cuh"
 #include "ptx.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
 namespace {
+
+using act::x2::add2;
+using act::x2::fma2;
+using act::x2::mul2;
+using act::x2::pk;
+using act::x2::splat;
+using act::x2::upk;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
@@ -40,33 +48,46 @@ constexpr int kMaxStages = 6;
 template <typename E>
 constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements of a vector
 
+// A vector as pairs of floats (one fp32x2 instruction each), and back.
 template <typename E>
-__device__ __forceinline__ void to_floats(uint4 q, float* v) {
+__device__ __forceinline__ void to_pairs(uint4 q, uint64_t (&v)[kPer<E> / 2]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (sizeof(E) == 2) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (sizeof(E) == 2) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    } else {
-      v[e] = __uint_as_float(w[e]);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = pk(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) v[e] = pk(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
   }
 }
 
 template <typename E>
-__device__ __forceinline__ uint4 from_floats(const float* v) {
+__device__ __forceinline__ uint4 from_pairs(const uint64_t (&v)[kPer<E> / 2]) {
   uint32_t w[4];
+  if constexpr (sizeof(E) == 2) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (sizeof(E) == 2) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      upk(v[e], lo, hi);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
       w[e] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      w[e] = __float_as_uint(v[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float lo, hi;
+      upk(v[e], lo, hi);
+      w[2 * e] = __float_as_uint(lo);
+      w[2 * e + 1] = __float_as_uint(hi);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float both(uint64_t v) {
+  float lo, hi;
+  upk(v, lo, hi);
+  return lo + hi;
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -110,12 +131,16 @@ struct TeamSum {
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(W * 32) : "memory");
       a = b = 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float2 f = mine[w];
+      for (int w = 0; w < W; w += 2) {
+        const float4 f = *reinterpret_cast<const float4*>(mine + w);
         a += f.x;
         b += f.y;
+        a += f.z;
+        b += f.w;
       }
       half ^= 1;
+    } else {
+      __syncwarp();  // keeps what follows from being fetched early, into registers that are not there
     }
     return make_float2(a, b);
   }
@@ -123,18 +148,25 @@ struct TeamSum {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     if constexpr (W > 1) {
-      float2* mine = red + half * W;
-      if ((threadIdx.x & 31) == 0) mine[warp_in_team].x = a;
+      float* mine = reinterpret_cast<float*>(red + half * W);
+      if ((threadIdx.x & 31) == 0) mine[warp_in_team] = a;
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(W * 32) : "memory");
       a = 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) a += mine[w].x;
+      for (int w = 0; w < W; w += 2) {
+        const float2 f = *reinterpret_cast<const float2*>(mine + w);
+        a += f.x;
+        a += f.y;
+      }
       half ^= 1;
     }
     return a;
   }
 };
 
+// Where a thread stands: vector v of its V is columns (v W 32 + t) kPer on.  A
+// vector past the end (on[v] false) is never copied; its slots in the queue hold
+// zeros from the start, so that the arithmetic needs no branches.
 template <typename E, int W, int V>
 struct Thread {
   int t, team, warp_in_team;
@@ -152,191 +184,215 @@ struct Thread {
   }
   // bytes of vector v from a row's start
   __device__ __forceinline__ int off(int v) const { return 16 * t + v * (W * 32 * 16); }
+  // Vector v of a parameter, or `none` where there is none or it is past the end.
+  __device__ __forceinline__ uint4 param(const void* p, int v, uint32_t none) const {
+    if (p && on[v]) return *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + off(v));
+    return make_uint4(none, none, none, none);
+  }
 };
 
-__device__ __forceinline__ uint32_t slot_of(uint32_t base, int arrays, int V, int stage, int array, int v) {
-  return base + static_cast<uint32_t>(((stage * arrays + array) * V + v) * kThreads + threadIdx.x) * 16u;
+// A thread's queue in shared memory: slots of 16 bytes, [stage][array][vector].
+constexpr uint32_t kSlot = kThreads * 16;
+template <int V>
+__device__ __forceinline__ uint32_t slot(uint32_t stage, int array, int v) {
+  return stage + static_cast<uint32_t>(array * V + v) * kSlot;
 }
+
+template <typename E>
+constexpr bool kGainInSmem = sizeof(E) == 2;
+template <typename E>
+constexpr uint32_t kOnes = sizeof(E) == 2 ? 0x3f803f80u : 0x3f800000u;
 
 template <typename E, int W, int V>
 __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_fwd(const __grid_constant__ NormParams p) {
+  constexpr int P = kPer<E> / 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 red[2 * kWarps];
-  const uint32_t base = ptx::smem_u32(smem);
+  __shared__ __align__(16) float2 red[2 * kWarps];
   const Thread<E, W, V> th(p.cols);
   TeamSum<W> sum{red + th.team * 2 * W, 1 + th.team, 0};
   const bool add = p.res != nullptr;
-  const int arrays = add ? 2 : 1, S = p.stages;
+  const int S = p.stages;
+  const uint32_t base = ptx::smem_u32(smem) + threadIdx.x * 16, stage_bytes = (add ? 2 : 1) * V * kSlot;
 
-  auto fetch = [&](int64_t row, int stage) {
+  auto fetch = [&](int64_t row, uint32_t stage) {
     if (row < p.rows) {
       const char* x = static_cast<const char*>(p.x) + row * p.ldx;
       const char* r = static_cast<const char*>(p.res) + row * p.ldr;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (!th.on[v]) continue;
-        copy16(slot_of(base, arrays, V, stage, 0, v), x + th.off(v));
-        if (add) copy16(slot_of(base, arrays, V, stage, 1, v), r + th.off(v));
+        if (th.on[v]) copy16(slot<V>(stage, 0, v), x + th.off(v));
+        if (add && th.on[v]) copy16(slot<V>(stage, 1, v), r + th.off(v));
       }
     }
     copy_commit();
   };
 
-  for (int i = 0; i + 1 < S; ++i) fetch(th.first + i * th.step, i);
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!th.on[v]) {
+        ptx::st_shared_v4(slot<V>(base + i * stage_bytes, 0, v), make_uint4(0, 0, 0, 0));
+        if (add) ptx::st_shared_v4(slot<V>(base + i * stage_bytes, 1, v), make_uint4(0, 0, 0, 0));
+      }
+  for (int i = 0; i + 1 < S; ++i) fetch(th.first + i * th.step, base + i * stage_bytes);
   uint4 gain[V], bias[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    gain[v] = bias[v] = make_uint4(0, 0, 0, 0);
-    if (p.gain && th.on[v]) gain[v] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.gain) + th.off(v));
-    if (p.bias && th.on[v]) bias[v] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.bias) + th.off(v));
+    gain[v] = th.param(p.gain, v, kOnes<E>);
+    bias[v] = th.param(p.bias, v, 0);
   }
-  int stage = 0;
+  int at = 0;
+#pragma unroll 1
   for (int64_t row = th.first; row < p.rows; row += th.step) {
-    fetch(row + (S - 1) * th.step, stage == 0 ? S - 1 : stage - 1);
+    fetch(row + (S - 1) * th.step, base + (at == 0 ? S - 1 : at - 1) * stage_bytes);
     copy_wait_all_but(S - 1);
-    float x[V][kPer<E>];
-    float a = 0.0f;
+    const uint32_t stage = base + at * stage_bytes;
+    at = at + 1 == S ? 0 : at + 1;
+    uint64_t x[V][P];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; ++v) to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 0, v)), x[v]);
+    if (add) {
 #pragma unroll
-      for (int e = 0; e < kPer<E>; ++e) x[v][e] = 0.0f;
-      if (!th.on[v]) continue;
-      to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 0, v)), x[v]);
-      if (add) {
-        float r[kPer<E>];
-        to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 1, v)), r);
+      for (int v = 0; v < V; ++v) {
+        uint64_t r[P];
+        to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 1, v)), r);
 #pragma unroll
-        for (int e = 0; e < kPer<E>; ++e) x[v][e] += r[e];
-        const uint4 q = from_floats<E>(x[v]);
-        *reinterpret_cast<uint4*>(static_cast<char*>(p.sum) + row * p.lds + th.off(v)) = q;
-        to_floats<E>(q, x[v]);
+        for (int e = 0; e < P; ++e) x[v][e] = add2(x[v][e], r[e]);
+        const uint4 q = from_pairs<E>(x[v]);
+        if (th.on[v]) *reinterpret_cast<uint4*>(static_cast<char*>(p.sum) + row * p.lds + th.off(v)) = q;
+        to_pairs<E>(q, x[v]);
       }
     }
     float mu = 0.0f;
     if (!p.rms) {
+      uint64_t a = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < kPer<E>; ++e) a += x[v][e];
-      mu = sum(a, th.warp_in_team) * p.inv_cols;
-    }
-    a = 0.0f;
+        for (int e = 0; e < P; ++e) a = add2(a, x[v][e]);
+      mu = sum(both(a), th.warp_in_team) * p.inv_cols;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!th.on[v]) continue;
+      for (int v = 0; v < V; ++v) {
+        const uint64_t shift = splat(th.on[v] ? -mu : 0.0f);
 #pragma unroll
-      for (int e = 0; e < kPer<E>; ++e) {
-        x[v][e] -= mu;
-        a = fmaf(x[v][e], x[v][e], a);
+        for (int e = 0; e < P; ++e) x[v][e] = add2(x[v][e], shift);
       }
     }
-    const float r = rsqrtf(fmaf(sum(a, th.warp_in_team), p.inv_cols, p.eps));
+    uint64_t a = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < P; ++e) a = fma2(x[v][e], x[v][e], a);
+    const float r = rsqrtf(fmaf(sum(both(a), th.warp_in_team), p.inv_cols, p.eps));
     if (th.t == 0 && p.stats) reinterpret_cast<float2*>(p.stats)[row] = make_float2(mu, r);
+    const uint64_t r2 = splat(r);
+    char* y = static_cast<char*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (!th.on[v]) continue;
-      float g[kPer<E>], b[kPer<E>];
-      to_floats<E>(bias[v], b);
-      if (p.gain) {
-        to_floats<E>(gain[v], g);
+      uint64_t g[P], b[P];
+      to_pairs<E>(gain[v], g);
+      to_pairs<E>(bias[v], b);
 #pragma unroll
-        for (int e = 0; e < kPer<E>; ++e) x[v][e] = fmaf(x[v][e] * r, g[e], b[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kPer<E>; ++e) x[v][e] = fmaf(x[v][e], r, b[e]);
-      }
-      *reinterpret_cast<uint4*>(static_cast<char*>(p.y) + row * p.ldy + th.off(v)) = from_floats<E>(x[v]);
+      for (int e = 0; e < P; ++e) x[v][e] = fma2(mul2(x[v][e], r2), g[e], b[e]);
+      if (th.on[v]) *reinterpret_cast<uint4*>(y + th.off(v)) = from_pairs<E>(x[v]);
     }
-    stage = stage + 1 == S ? 0 : stage + 1;
   }
   copy_wait<0>();
 }
 
-template <typename E, int W, int V>
+// kBias: dbias is summed up as well.
+template <typename E, int W, int V, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_bwd(const __grid_constant__ NormParams p) {
+  constexpr int P = kPer<E> / 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 red[2 * kWarps];
-  const uint32_t base = ptx::smem_u32(smem);
+  __shared__ __align__(16) float2 red[2 * kWarps];
   const Thread<E, W, V> th(p.cols);
   TeamSum<W> sum{red + th.team * 2 * W, 1 + th.team, 0};
   const bool add = p.dsum != nullptr;
-  const int arrays = add ? 3 : 2, S = p.stages;
+  const int S = p.stages;
+  // The gain's vectors lie in front of the queue (bf16; fp32 leaves no room for them beside the queue, they come from L2):
+  // registers are for the sums.
+  const uint32_t gains = ptx::smem_u32(smem) + threadIdx.x * 16, base = gains + (kGainInSmem<E> ? V * kSlot : 0);
+  const uint32_t stage_bytes = (add ? 3 : 2) * V * kSlot;
 
-  auto fetch = [&](int64_t row, int stage) {
+  auto fetch = [&](int64_t row, uint32_t stage) {
     if (row < p.rows) {
       const char* x = static_cast<const char*>(p.x) + row * p.ldx;
       const char* dy = static_cast<const char*>(p.dy) + row * p.lddy;
       const char* ds = static_cast<const char*>(p.dsum) + row * p.ldds;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (!th.on[v]) continue;
-        copy16(slot_of(base, arrays, V, stage, 0, v), x + th.off(v));
-        copy16(slot_of(base, arrays, V, stage, 1, v), dy + th.off(v));
-        if (add) copy16(slot_of(base, arrays, V, stage, 2, v), ds + th.off(v));
+        if (th.on[v]) copy16(slot<V>(stage, 0, v), x + th.off(v));
+        if (th.on[v]) copy16(slot<V>(stage, 1, v), dy + th.off(v));
+        if (add && th.on[v]) copy16(slot<V>(stage, 2, v), ds + th.off(v));
       }
     }
     copy_commit();
   };
 
-  for (int i = 0; i + 1 < S; ++i) fetch(th.first + i * th.step, i);
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!th.on[v]) {
+        ptx::st_shared_v4(slot<V>(base + i * stage_bytes, 0, v), make_uint4(0, 0, 0, 0));
+        ptx::st_shared_v4(slot<V>(base + i * stage_bytes, 1, v), make_uint4(0, 0, 0, 0));
+      }
+  for (int i = 0; i + 1 < S; ++i) fetch(th.first + i * th.step, base + i * stage_bytes);
   const float2* stats = reinterpret_cast<const float2*>(p.stats);
   float2 next = th.first < p.rows ? stats[th.first] : make_float2(0.0f, 0.0f);
-  uint4 gain[V];
-  float dg[V][kPer<E>], db[V][kPer<E>];
+  uint64_t dg[V][P], db[V][P];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    gain[v] = make_uint4(0, 0, 0, 0);
-    if (p.gain && th.on[v]) gain[v] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.gain) + th.off(v));
+    if (kGainInSmem<E>) ptx::st_shared_v4(slot<V>(gains, 0, v), th.param(p.gain, v, kOnes<E>));
 #pragma unroll
-    for (int e = 0; e < kPer<E>; ++e) dg[v][e] = db[v][e] = 0.0f;
+    for (int e = 0; e < P; ++e) dg[v][e] = db[v][e] = 0;
   }
-  int stage = 0;
+  int at = 0;
+#pragma unroll 1
   for (int64_t row = th.first; row < p.rows; row += th.step) {
-    fetch(row + (S - 1) * th.step, stage == 0 ? S - 1 : stage - 1);
+    fetch(row + (S - 1) * th.step, base + (at == 0 ? S - 1 : at - 1) * stage_bytes);
     const float mu = next.x, r = next.y;
     if (row + th.step < p.rows) next = stats[row + th.step];
     copy_wait_all_but(S - 1);
-    float sw = 0.0f, swn = 0.0f;
+    const uint32_t stage = base + at * stage_bytes;
+    at = at + 1 == S ? 0 : at + 1;
+    const uint64_t shift = splat(-mu), r2 = splat(r);
+    uint64_t sw = 0, swn = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (!th.on[v]) continue;
-      float x[kPer<E>], w[kPer<E>], g[kPer<E>];
-      to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 0, v)), x);
-      to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 1, v)), w);
-      to_floats<E>(gain[v], g);
+      uint64_t x[P], w[P], g[P];
+      to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 0, v)), x);
+      to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 1, v)), w);
+      to_pairs<E>(kGainInSmem<E> ? ptx::ld_shared_v4(slot<V>(gains, 0, v)) : th.param(p.gain, v, kOnes<E>), g);
 #pragma unroll
-      for (int e = 0; e < kPer<E>; ++e) {
-        const float n = (x[e] - mu) * r;
-        dg[v][e] = fmaf(w[e], n, dg[v][e]);
-        db[v][e] += w[e];
-        if (p.gain) w[e] *= g[e];
-        sw += w[e];
-        swn = fmaf(w[e], n, swn);
+      for (int e = 0; e < P; ++e) {
+        const uint64_t n = mul2(add2(x[e], shift), r2);
+        dg[v][e] = fma2(w[e], n, dg[v][e]);
+        if (kBias) db[v][e] = add2(db[v][e], w[e]);
+        w[e] = mul2(w[e], g[e]);
+        sw = add2(sw, w[e]);
+        swn = fma2(w[e], n, swn);
       }
     }
-    const float2 m = sum(sw, swn, th.warp_in_team);
-    const float c1 = p.rms ? 0.0f : m.x * p.inv_cols, c2 = m.y * p.inv_cols;
+    const float2 m = sum(both(sw), both(swn), th.warp_in_team);
+    // dx = r w - r mean(w) - (x - mu) r^2 mean(w n)
+    const uint64_t c1 = splat(p.rms ? 0.0f : -(r * (m.x * p.inv_cols))), c2 = splat(-(r * r * (m.y * p.inv_cols)));
+    char* dx = static_cast<char*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (!th.on[v]) continue;
-      float x[kPer<E>], w[kPer<E>], g[kPer<E>];
-      to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 0, v)), x);
-      to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 1, v)), w);
-      to_floats<E>(gain[v], g);
+      uint64_t x[P], w[P], g[P];
+      to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 0, v)), x);
+      to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 1, v)), w);
+      to_pairs<E>(kGainInSmem<E> ? ptx::ld_shared_v4(slot<V>(gains, 0, v)) : th.param(p.gain, v, kOnes<E>), g);
 #pragma unroll
-      for (int e = 0; e < kPer<E>; ++e) {
-        const float n = (x[e] - mu) * r;
-        if (p.gain) w[e] *= g[e];
-        x[e] = r * fmaf(-n, c2, w[e] - c1);
-      }
+      for (int e = 0; e < P; ++e) x[e] = fma2(add2(x[e], shift), c2, fma2(mul2(w[e], g[e]), r2, c1));
       if (add) {
-        to_floats<E>(ptx::ld_shared_v4(slot_of(base, arrays, V, stage, 2, v)), w);
+        to_pairs<E>(ptx::ld_shared_v4(slot<V>(stage, 2, v)), w);
 #pragma unroll
-        for (int e = 0; e < kPer<E>; ++e) x[e] += w[e];
+        for (int e = 0; e < P; ++e) x[e] = add2(x[e], w[e]);
       }
-      *reinterpret_cast<uint4*>(static_cast<char*>(p.dx) + row * p.lddx + th.off(v)) = from_floats<E>(x);
+      if (th.on[v]) *reinterpret_cast<uint4*>(dx + th.off(v)) = from_pairs<E>(x);
     }
-    stage = stage + 1 == S ? 0 : stage + 1;
   }
   copy_wait<0>();
   if (!p.partial) return;
@@ -344,15 +400,18 @@ __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_bwd(const __grid_const
   // This CTA's sums, over its teams in order (the queues' memory is reused).
   constexpr int kWide = W * 32 * V * kPer<E>;
   float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    if (which && !p.want_bias) break;
+#pragma unroll
+  for (int which = 0; which < (kBias ? 2 : 1); ++which) {
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int e = 0; e < kPer<E>; ++e)
-        sums[th.team * kWide + (v * W * 32 + th.t) * kPer<E> + e] = which ? db[v][e] : dg[v][e];
+      for (int e = 0; e < P; ++e) {
+        float lo, hi;
+        upk(which ? db[v][e] : dg[v][e], lo, hi);
+        *reinterpret_cast<float2*>(sums + th.team * kWide + (v * W * 32 + th.t) * kPer<E> + 2 * e) =
+            make_float2(lo, hi);
+      }
     __syncthreads();
     float* out = p.partial + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * p.cols;
     for (int c = threadIdx.x; c < p.cols; c += kThreads) {
@@ -395,35 +454,47 @@ struct Pick {
   int W, V;
 };
 
-// The team and the vectors a thread holds: up to 32 elements a thread, then up
-// to 16 warps a token.
 template <typename E, int W, int V>
-Pick pick_one(bool bwd) {
-  return {bwd ? tpmlp_norm_bwd<E, W, V> : tpmlp_norm_fwd<E, W, V>, W, V};
+Pick pick_one(bool bwd, bool bias) {
+  return {!bwd   ? tpmlp_norm_fwd<E, W, V>
+          : bias ? tpmlp_norm_bwd<E, W, V, true>
+                 : tpmlp_norm_bwd<E, W, V, false>,
+          W, V};
 }
 
-template <typename E>
-Pick pick(int cols, bool bwd) {
+// 24 or 32 elements a thread, whichever holds the token with fewer warps to spare.
+template <typename E, int W>
+Pick pick_team(int cols, bool bwd, bool bias) {
   constexpr int V = 32 / kPer<E>;
-  if (cols <= 256) return pick_one<E, 1, V / 4>(bwd);
-  if (cols <= 512) return pick_one<E, 1, V / 2>(bwd);
-  if (cols <= 1024) return pick_one<E, 1, V>(bwd);
-  if (cols <= 2048) return pick_one<E, 2, V>(bwd);
-  if (cols <= 4096) return pick_one<E, 4, V>(bwd);
-  if (cols <= 8192) return pick_one<E, 8, V>(bwd);
-  return pick_one<E, 16, V>(bwd);
+  return cols <= W * 32 * 24 ? pick_one<E, W, V / 4 * 3>(bwd, bias) : pick_one<E, W, V>(bwd, bias);
+}
+
+// The team and the vectors a thread holds: up to 32 elements a thread, then up
+// to 16 warps a token.
+
+template <typename E>
+Pick pick(int cols, bool bwd, bool bias) {
+  constexpr int V = 32 / kPer<E>;
+  if (cols <= 256) return pick_one<E, 1, V / 4>(bwd, bias);
+  if (cols <= 512) return pick_one<E, 1, V / 2>(bwd, bias);
+  if (cols <= 1024) return pick_team<E, 1>(cols, bwd, bias);
+  if (cols <= 2048) return pick_team<E, 2>(cols, bwd, bias);
+  if (cols <= 4096) return pick_team<E, 4>(cols, bwd, bias);
+  if (cols <= 8192) return pick_team<E, 8>(cols, bwd, bias);
+  return pick_team<E, 16>(cols, bwd, bias);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(NormParams& p, bool bf16, bool bwd, int sms, cudaStream_t stream) {
   if (p.rows <= 0) return cudaSuccess;
-  const Pick k = bf16 ? pick<__nv_bfloat16>(p.cols, bwd) : pick<float>(p.cols, bwd);
+  const Pick k = bf16 ? pick<__nv_bfloat16>(p.cols, bwd, p.want_bias) : pick<float>(p.cols, bwd, p.want_bias);
   const int arrays = bwd ? (p.dsum ? 3 : 2) : (p.res ? 2 : 1);
   const int stage = arrays * k.V * kThreads * 16;
-  p.stages = std::max(1, std::min(kMaxStages, (kMaxSmem - 1024) / stage));
+  const int gains = bwd && bf16 ? k.V * kThreads * 16 : 0;
+  p.stages = std::max(1, std::min(kMaxStages, (kMaxSmem - 1024 - gains) / stage));
   const int sums = bwd ? kThreads * k.V * (bf16 ? 8 : 4) * 4 : 0;
-  const int bytes = std::max(p.stages * stage, sums);
+  const int bytes = std::max(gains + p.stages * stage, sums);
   cudaError_t e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
   if (e != cudaSuccess) return e;
   p.ctas = static_cast<int32_t>(std::min<int64_t>(p.rows, std::min(sms, kNormMaxCtas)));
