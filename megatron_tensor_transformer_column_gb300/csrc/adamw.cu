@@ -29,18 +29,28 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "act.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPer = 8;  // elements of a thread and pass
-constexpr int kPasses = 2;
+using act::x2::add2;
+using act::x2::fma2;
+using act::x2::mul2;
+using act::x2::pk;
+using act::x2::splat;
+using act::x2::upk;
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 8;     // elements of a thread and pass
+constexpr int kPasses = 4;  // of a CTA: a warp's consecutive groups, whose scale bytes are one word
 constexpr int kChunk = kThreads * kPer * kPasses;  // elements of a CTA
 constexpr uint32_t kNanScale = 255;
-static_assert(kChunk % kAdamGroup == 0 && 32 * kPer == kAdamGroup, "a warp's pass is a group");
+static_assert(32 * kPer == kAdamGroup && kPasses == 4, "a warp's pass is a group, its chunk's scales a word");
 
 __device__ __forceinline__ uint32_t hash32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x7feb352du;
@@ -48,102 +58,206 @@ __device__ __forceinline__ uint32_t hash32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// Elements i .. i + 7 of an array of n (those past the end read as 0).
-template <typename E>
-__device__ __forceinline__ void load8(const E* p, int64_t i, int64_t n, float (&v)[8]) {
-  if (i + 8 <= n) {
-    if constexpr (sizeof(E) == 2) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p + i);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = i + k < n ? static_cast<float>(p[i + k]) : 0.0f;
-  }
+// Loads under a predicate (zeros without it), with no branch around them: where
+// two paths meet the loaded registers would be copied, and waited for, one load
+// after the other.
+__device__ __forceinline__ uint4 load16_if(const void* p, uint32_t go) {
+  uint4 q;
+  asm volatile(
+      "{\n .reg .pred go;\n setp.ne.u32 go, %5, 0;\n"
+      " mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+      " @go ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
+      : "l"(p), "r"(go)
+      : "memory");
+  return q;
 }
-
+__device__ __forceinline__ uint2 load8_if(const void* p, uint32_t go) {
+  uint2 q;
+  asm volatile(
+      "{\n .reg .pred go;\n setp.ne.u32 go, %3, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n"
+      " @go ld.global.v2.u32 {%0, %1}, [%2];\n}"
+      : "=&r"(q.x), "=&r"(q.y)
+      : "l"(p), "r"(go)
+      : "memory");
+  return q;
+}
+// 8 elements as they lie in memory.
 template <typename E>
-__device__ __forceinline__ void store8(E* p, int64_t i, int64_t n, const float (&v)[8]) {
-  if (i + 8 <= n) {
-    if constexpr (sizeof(E) == 2) {
-      uint32_t w[4];
+struct Eight {
+  static constexpr int kQuads = sizeof(E) / 2;
+  uint4 q[kQuads];
+  // elements i .. i + 7, all of which the array has; nothing without `go`
+  __device__ __forceinline__ void load(const E* p, int64_t i, uint32_t go) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    for (int k = 0; k < kQuads; ++k) q[k] = load16_if(p + i + k * (16 / static_cast<int>(sizeof(E))), go);
+  }
+  __device__ __forceinline__ void store(E* p, int64_t i) const {
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) reinterpret_cast<uint4*>(p + i)[k] = q[k];
+  }
+  // of an array of n: what lies past its end is 0 and is not touched
+  __device__ __forceinline__ void load_tail(const E* p, int64_t i, int64_t n) {
+    uint32_t w[8] = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (i + k >= n) continue;
+      if constexpr (sizeof(E) == 2)
+        w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i + k]) << (16 * (k & 1));
+      else w[k] = reinterpret_cast<const uint32_t*>(p)[i + k];
+    }
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) q[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+  __device__ __forceinline__ void store_tail(E* p, int64_t i, int64_t n) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 f = q[sizeof(E) == 2 ? 0 : k / 4];
+      const int e = sizeof(E) == 2 ? k / 2 : k % 4;
+      const uint32_t w = e == 0 ? f.x : e == 1 ? f.y : e == 2 ? f.z : f.w;
+      if (i + k >= n) continue;
+      if constexpr (sizeof(E) == 2) reinterpret_cast<uint16_t*>(p)[i + k] = static_cast<uint16_t>(w >> (16 * (k & 1)));
+      else reinterpret_cast<uint32_t*>(p)[i + k] = w;
+    }
+  }
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
+    if constexpr (sizeof(E) == 2) {
+      const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = pk(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        v[2 * k] = pk(__uint_as_float(q[k].x), __uint_as_float(q[k].y));
+        v[2 * k + 1] = pk(__uint_as_float(q[k].z), __uint_as_float(q[k].w));
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const uint64_t (&v)[4]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      upk(v[k], lo, hi);
+      if constexpr (sizeof(E) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[2 * k] = __float_as_uint(lo);
+        w[2 * k + 1] = __float_as_uint(hi);
       }
-      *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
     }
-  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i + k < n) p[i + k] = static_cast<E>(v[k]);
+    for (int k = 0; k < static_cast<int>(sizeof(E)) / 2; ++k)
+      q[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
   }
-}
+};
 
 // ------------------------------------------------------------------ moments in 8 bits
 
-// 8 codes of a group with this scale byte, as floats.
+// 2^(e - S) as fp32 bits: what a code's bits 20.. are added to.
 template <bool kSecond>
-__device__ __forceinline__ void decode8(uint2 q, uint32_t scale, float (&x)[8]) {
-  constexpr uint32_t kMask = kSecond ? 0xffu : 0x7fu;
-  const uint32_t base = (scale + (kSecond ? 96u : 112u) - 91u) << 23;  // 2^(e - S)
-  const float zero = scale == kNanScale ? __uint_as_float(0x7fffffffu) : 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t c = (k < 4 ? q.x : q.y) >> (8 * (k & 3));
-    const uint32_t mag = c & kMask;
-    float v = mag ? __uint_as_float((mag << 20) + base) : zero;
-    if (!kSecond) v = __uint_as_float(__float_as_uint(v) | ((c & 0x80u) << 24));
-    x[k] = v;
-  }
+__device__ __forceinline__ uint32_t scale_bits(uint32_t scale) {
+  return (scale + (kSecond ? 96u : 112u) - 91u) << 23;
 }
 
-// 8 elements of the warp's group to codes; the scale byte of the group.
+// 8 codes of a group with this scale byte, as floats.  A word without a zero
+// code (all but a few): a code moved to bits 20.., the sign (of m) to bit 31,
+// and the scale's exponent added.
 template <bool kSecond>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], const uint32_t (&r)[8], uint32_t& scale) {
-  uint32_t big = 0;
+__device__ __forceinline__ void decode8(uint2 q, uint32_t scale, uint64_t (&x)[4]) {
+  constexpr uint32_t kMask = kSecond ? 0xffffffffu : 0x7f7f7f7fu;
+  const uint32_t base = scale_bits<kSecond>(scale);
+  const uint32_t a = q.x & kMask, b = q.y & kMask;
+  float v[8];
+  if ((((a - 0x01010101u) & ~a) | ((b - 0x01010101u) & ~b)) & 0x80808080u) {  // a zero byte
+    const float zero = scale == kNanScale ? __uint_as_float(0x7fffffffu) : 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) big = max(big, __float_as_uint(x[k]) & 0x7fffffffu);
-  big = __reduce_max_sync(0xffffffffu, big);
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t c = (k < 4 ? q.x : q.y) >> (8 * (k & 3));
+      const uint32_t mag = c & (kMask & 0xffu);
+      v[k] = mag ? __uint_as_float((mag << 20) + base) : zero;
+      if (!kSecond && (c & 0x80u)) v[k] = -v[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w = k < 4 ? q.x : q.y;
+      if (kSecond) {
+        v[k] = __uint_as_float(__byte_perm(w, 0, 0x4440 | (k & 3)) * (1u << 20) + base);
+      } else {
+        const int c = static_cast<int>(__byte_perm(w, 0, 0x0444 | ((k & 3) << 12)));  // the code in the top byte
+        v[k] = __uint_as_float((static_cast<uint32_t>(c >> 4) & 0x87f00000u) + base);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = pk(v[2 * k], v[2 * k + 1]);
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 8 elements of the warp's group to codes; the scale byte of the group.  r8: the
+// random bits of elements 2 k (low half) and 2 k + 1.  With the group's exponent
+// taken off, bits 20.. of a magnitude are its code; all moved up by 4, so that the
+// code is the top byte (the sign of m falls off at the top) and the random bits
+// stand at 8...
+template <bool kSecond>
+__device__ __forceinline__ uint2 encode8(const uint64_t (&pairs)[4], const uint32_t (&h)[4], uint32_t& scale) {
+  float x[8], m[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) upk(pairs[k], x[2 * k], x[2 * k + 1]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m[k] = kSecond ? x[k] : fabsf(x[k]);
+  const float most = max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), max3_nan(m[6], m[7], m[7]));
+  const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu);
   const int e = max(static_cast<int>((big + 0xfffffu) >> 23) - 127, -90);
-  if (e >= 127) {  // a NaN, an infinity or a number beyond 2^127: the group is lost
-    scale = kNanScale;
+  if (big == 0 || e >= 127) {  // nothing; or a NaN, an infinity or a number beyond 2^127: the group is lost
+    scale = big ? kNanScale : 0u;
     return make_uint2(0, 0);
   }
-  scale = big ? static_cast<uint32_t>(e + 91) : 0u;
-  const int base = (e + (kSecond ? 96 : 112)) << 23;
-  uint32_t w[2] = {0, 0};
+  scale = static_cast<uint32_t>(e + 91);
+  const uint32_t base = static_cast<uint32_t>(e + (kSecond ? 96 : 112)) << 23;
+  const uint32_t base4 = base << 4;
+  uint32_t z[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t bits = __float_as_uint(x[k]);
-    const uint32_t a = bits & 0x7fffffffu;
-    const int y = static_cast<int>(a) - base;
-    uint32_t c = static_cast<uint32_t>(y + static_cast<int>(r[k] << 4)) >> 20;
-    if (y < (1 << 20)) {  // below the smallest code, 1.125 2^(e - S)
+    const uint32_t r8 = __byte_perm(h[k >> 1], 0, k & 1 ? 0x4324 : 0x4104);
+    z[k] = (bits << 4) + (r8 - base4);
+    if (!kSecond) z[k] = (z[k] & 0x7fffffffu) | (bits & 0x80000000u);
+  }
+  const float least = min3(min3(m[0], m[1], m[2]), min3(m[3], m[4], m[5]), fminf(m[6], m[7]));
+  if (__float_as_uint(least) < base + (1u << 20)) {  // below the smallest code, 1.125 2^(e - S)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t a = __float_as_uint(m[k]);
+      if (a >= base + (1u << 20)) continue;
+      uint32_t c;
       if (kSecond) {
         c = a ? 1u : 0u;
       } else {
-        const float t = __uint_as_float(a) * __uint_as_float(static_cast<uint32_t>(142 - e) << 23);  // 2^(S - e) |x|
-        c = t * 65536.0f > static_cast<float>(r[k]) * 1.125f ? 1u : 0u;
+        const uint32_t r = k & 1 ? h[k >> 1] >> 16 : h[k >> 1] & 0xffffu;
+        const float t = m[k] * __uint_as_float(static_cast<uint32_t>(142 - e) << 23);  // 2^(S - e) |x|
+        c = t * 65536.0f > static_cast<float>(r) * 1.125f ? 1u : 0u;
+        c |= (__float_as_uint(x[k]) >> 24) & 0x80u;
       }
+      z[k] = c << 24;
     }
-    if (!kSecond) c |= (bits >> 24) & 0x80u;
-    w[k >> 2] |= c << (8 * (k & 3));
   }
-  return make_uint2(w[0], w[1]);
+  uint2 q;
+  q.x = __byte_perm(__byte_perm(z[0], z[1], 0x0073), __byte_perm(z[2], z[3], 0x0073), 0x5410);
+  q.y = __byte_perm(__byte_perm(z[4], z[5], 0x0073), __byte_perm(z[6], z[7], 0x0073), 0x5410);
+  return q;
 }
 
 // ------------------------------------------------------------------ the step
@@ -161,15 +275,88 @@ __device__ __forceinline__ int find_chunk(const AdamParams& a, int64_t& first) {
   return lo;
 }
 
-template <typename P, typename G, bool k8>
-__global__ void __launch_bounds__(kThreads) tpmlp_adamw_step_all(const __grid_constant__ AdamParams a) {
+// What a thread reads for a pass.  M: the type that the weight is read as.
+template <typename M, typename G, bool k8>
+struct Pass {
+  Eight<G> g;
+  Eight<M> p;
+  Eight<float> m, v;  // in 32 bits,
+  uint2 mc, vc;       // or codes
+  __device__ __forceinline__ void load(const AdamTensor& t, const M* src, int64_t i, bool whole, uint32_t go) {
+    if (whole) {
+      g.load(static_cast<const G*>(t.g), i, go);
+      p.load(src, i, go);
+    } else {
+      g.load_tail(static_cast<const G*>(t.g), i, t.n);
+      p.load_tail(src, i, t.n);
+    }
+    if constexpr (k8) {  // whole groups always
+      mc = load8_if(static_cast<const uint8_t*>(t.m) + i, go);
+      vc = load8_if(static_cast<const uint8_t*>(t.v) + i, go);
+    } else if (whole) {
+      m.load(static_cast<const float*>(t.m), i, go);
+      v.load(static_cast<const float*>(t.v), i, go);
+    } else {
+      m.load_tail(static_cast<const float*>(t.m), i, t.n);
+      v.load_tail(static_cast<const float*>(t.v), i, t.n);
+    }
+  }
+};
+
+// The scale bytes of a warp's kPasses groups, which are neighbours, as one word
+// (n of them where the tensor ends before).  A warp reads and writes them once
+// for its whole chunk: with a byte of a group at a time, stores to and loads from
+// the same sectors held each other up (135 M weights: 520 us instead of 240).
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p, int n) {
+  if (n >= kPasses) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+  for (int k = 0; k < n; ++k) w |= static_cast<uint32_t>(p[k]) << (8 * k);
+  return w;
+}
+__device__ __forceinline__ void store_scales(uint8_t* p, int n, uint32_t w) {
+  if (n >= kPasses) {
+    *reinterpret_cast<uint32_t*>(p) = w;
+  } else {
+    for (int k = 0; k < n; ++k) p[k] = static_cast<uint8_t>(w >> (8 * k));
+  }
+}
+
+template <typename E>
+__device__ __forceinline__ void put8(const uint64_t (&x)[4], E* p, int64_t i, int64_t n, bool whole) {
+  Eight<E> out;
+  out.set(x);
+  if (whole) out.store(p, i);
+  else out.store_tail(p, i, n);
+}
+
+// kMaster: the fp32 copy is updated, the weight only written.  m and v take one
+// rounding for each product and sum as the formulas have them, so that what the
+// random bits make of them does not depend on how products and sums are fused.
+template <typename P, typename G, bool k8, bool kMaster>
+__global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(const __grid_constant__ AdamParams a) {
+  using M = typename std::conditional<kMaster, float, P>::type;
   int64_t first;
-  const AdamTensor& t = a.t[find_chunk(a, first)];
+  const AdamTensor t = a.t[find_chunk(a, first)];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t codes = (t.n + kAdamGroup - 1) / kAdamGroup * kAdamGroup;
+  M* src = kMaster ? reinterpret_cast<M*>(t.master) : static_cast<M*>(t.p);
+  int64_t at = first + warp * (kPasses * kAdamGroup);  // this warp's group, the next one on every pass
+  Pass<M, G, k8> now;
+  now.load(t, src, at + lane * kPer, true, at + kAdamGroup <= t.n);
+  uint8_t* ms = static_cast<uint8_t*>(t.m) + codes + at / kAdamGroup;
+  uint8_t* vs = static_cast<uint8_t*>(t.v) + codes + at / kAdamGroup;
+  const int groups = static_cast<int>(min(static_cast<int64_t>(kPasses), max(int64_t{0}, (codes - at) / kAdamGroup)));
+  uint32_t m_scales = 0, v_scales = 0, m_new = 0, v_new = 0;
+  if (k8) {
+    m_scales = load_scales(ms, groups);
+    v_scales = load_scales(vs, groups);
+  }
+
   float f = a.grad_scale;
   if (a.norm) {
     const float norm = *a.norm * a.grad_scale;
     if (!(norm <= 3.402823466e38f)) return;  // NaN or infinity
-    if (a.max_norm > 0.0f && norm > a.max_norm) f *= a.max_norm / norm;
+    if (a.max_norm > 0.0f && norm > a.max_norm) f *= a.max_norm * __frcp_rn(norm);
   }
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   float rate = a.rate, c2 = a.c2;
@@ -180,62 +367,71 @@ __global__ void __launch_bounds__(kThreads) tpmlp_adamw_step_all(const __grid_co
     c2 = rsqrtf(-expm1f(static_cast<float>(static_cast<double>(step) * a.ln_b2)));
     key = hash32(hash32(key ^ static_cast<uint32_t>(step)) ^ static_cast<uint32_t>(step >> 32));
   }
-  const float lr_t = lr * rate;
-  const float shrink = lr * t.decay;
-#pragma unroll 1
-  for (int pass = 0; pass < kPasses; ++pass) {
-    const int64_t i = first + (pass * kThreads + threadIdx.x) * kPer;
-    if (i - (threadIdx.x & 31) * kPer >= t.n) break;  // the warp's group is past the end
-    float g[8], p[8], m[8], v[8];
-    load8(static_cast<const G*>(t.g), i, t.n, g);
-    if (t.master) load8(t.master, i, t.n, p);
-    else load8(static_cast<const P*>(t.p), i, t.n, p);
-    const int64_t groups = (t.n + kAdamGroup - 1) / kAdamGroup, q = i / kAdamGroup;
-    uint8_t* mc = static_cast<uint8_t*>(t.m);
-    uint8_t* vc = static_cast<uint8_t*>(t.v);
+  const uint64_t f2 = splat(f), b1 = splat(a.b1), b1c = splat(a.b1c), b2 = splat(a.b2), b2c = splat(a.b2c);
+  const uint64_t root_scale = splat(c2), eps = splat(a.eps), shrink = splat(-(lr * t.decay)), rate2 = splat(-(lr * rate));
+  uint32_t seeds = 0;
+  if (k8) {  // lane k: the random bits' start of pass k's group
+    const uint64_t q = static_cast<uint64_t>(t.group0 + at / kAdamGroup + lane % kPasses);
+    seeds = hash32(hash32(key ^ static_cast<uint32_t>(q)) ^ static_cast<uint32_t>(q >> 32));
+  }
+
+  // One pass.  whole: the group is; next: whether the one after it is, and is this warp's, whose loads are on their way
+  // while this one is worked on.
+  auto one = [&](int pass, bool whole, bool next) {
+    const int64_t i = at + lane * kPer;
+    uint64_t x[4], p[4], m[4], v[4];
+    now.g.get(x);
+    now.p.get(p);
     if constexpr (k8) {
-      const uint2 cm = *reinterpret_cast<const uint2*>(mc + i), cv = *reinterpret_cast<const uint2*>(vc + i);
-      const uint32_t sm = mc[groups * kAdamGroup + q], sv = vc[groups * kAdamGroup + q];
-      decode8<false>(cm, sm, m);
-      decode8<true>(cv, sv, v);
+      decode8<false>(now.mc, (m_scales >> (8 * pass)) & 0xffu, m);
+      decode8<true>(now.vc, (v_scales >> (8 * pass)) & 0xffu, v);
     } else {
-      load8(static_cast<const float*>(t.m), i, t.n, m);
-      load8(static_cast<const float*>(t.v), i, t.n, v);
+      now.m.get(m);
+      now.v.get(v);
     }
+    if (whole) now.load(t, src, i + kAdamGroup, true, next);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = g[k] * f;
-      m[k] = fmaf(m[k], a.b1, x * a.b1c);
-      v[k] = fmaf(v[k], a.b2, x * a.b2c * x);
-      float root;
-      asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v[k]));
-      const float u = __fdividef(m[k] * lr_t, fmaf(root, c2, a.eps));
-      p[k] = fmaf(-shrink, p[k], p[k]) - u;
+    for (int k = 0; k < 4; ++k) {
+      x[k] = mul2(x[k], f2);
+      m[k] = add2(mul2(m[k], b1), mul2(x[k], b1c));
+      v[k] = add2(mul2(v[k], b2), mul2(mul2(x[k], b2c), x[k]));
+      float lo, hi;
+      upk(v[k], lo, hi);
+      asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(lo));
+      asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(hi));
+      upk(fma2(pk(lo, hi), root_scale, eps), lo, hi);
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(lo));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(hi));
+      p[k] = fma2(mul2(m[k], pk(lo, hi)), rate2, fma2(shrink, p[k], p[k]));
     }
-    if (t.master) store8(t.master, i, t.n, p);
-    store8(static_cast<P*>(t.p), i, t.n, p);
+    if (kMaster) put8(p, t.master, i, t.n, whole);
+    put8(p, static_cast<P*>(t.p), i, t.n, whole);
     if constexpr (k8) {
-      const uint64_t number = static_cast<uint64_t>(t.group0 + q);
-      const uint32_t h = hash32(hash32(key ^ static_cast<uint32_t>(number)) ^ static_cast<uint32_t>(number >> 32));
-      uint32_t r[8];
+      const uint32_t seed = __shfl_sync(0xffffffffu, seeds, pass) + lane * (4 * 0x9e3779b9u);
+      uint32_t h[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t x = hash32(h + ((threadIdx.x & 31) * 4 + k) * 0x9e3779b9u);
-        r[2 * k] = x & 0xffffu;
-        r[2 * k + 1] = x >> 16;
-      }
+      for (int k = 0; k < 4; ++k) h[k] = hash32(seed + k * 0x9e3779b9u);
       uint32_t sm, sv;
-      const uint2 cm = encode8<false>(m, r, sm), cv = encode8<true>(v, r, sv);
-      *reinterpret_cast<uint2*>(mc + i) = cm;
-      *reinterpret_cast<uint2*>(vc + i) = cv;
-      if ((threadIdx.x & 31) == 0) {
-        mc[groups * kAdamGroup + q] = static_cast<uint8_t>(sm);
-        vc[groups * kAdamGroup + q] = static_cast<uint8_t>(sv);
-      }
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i) = encode8<false>(m, h, sm);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i) = encode8<true>(v, h, sv);
+      m_new |= sm << (8 * pass);
+      v_new |= sv << (8 * pass);
     } else {
-      store8(static_cast<float*>(t.m), i, t.n, m);
-      store8(static_cast<float*>(t.v), i, t.n, v);
+      put8(m, static_cast<float*>(t.m), i, t.n, whole);
+      put8(v, static_cast<float*>(t.v), i, t.n, whole);
     }
+  };
+  int pass = 0;
+#pragma unroll 1
+  for (; pass < kPasses && at + kAdamGroup <= t.n; ++pass, at += kAdamGroup)
+    one(pass, true, pass + 1 < kPasses && at + 2 * kAdamGroup <= t.n);
+  if (pass < kPasses && at < t.n) {  // the tensor's last group, where it is not whole
+    now.load(t, src, at + lane * kPer, false, 1);
+    one(pass, false, false);
+  }
+  if (k8 && lane == 0) {
+    store_scales(ms, groups, m_new);
+    store_scales(vs, groups, v_new);
   }
 }
 
@@ -243,23 +439,35 @@ __global__ void __launch_bounds__(kThreads) tpmlp_adamw_step_all(const __grid_co
 // t.p and t.master: where m and v go.
 __global__ void __launch_bounds__(kThreads) tpmlp_adamw8_unpack_all(const __grid_constant__ AdamParams a) {
   int64_t first;
-  const AdamTensor& t = a.t[find_chunk(a, first)];
-  const int64_t groups = (t.n + kAdamGroup - 1) / kAdamGroup;
+  const AdamTensor t = a.t[find_chunk(a, first)];
+  const int64_t codes = (t.n + kAdamGroup - 1) / kAdamGroup * kAdamGroup;
+  const uint8_t* src[2] = {static_cast<const uint8_t*>(t.m), static_cast<const uint8_t*>(t.v)};
+  __nv_bfloat16* dst[2] = {static_cast<__nv_bfloat16*>(t.p), reinterpret_cast<__nv_bfloat16*>(t.master)};
+  const int64_t i0 = first + threadIdx.x * kPer;
+  uint2 c[2][kPasses];
+  uint32_t s[2][kPasses];
 #pragma unroll
   for (int pass = 0; pass < kPasses; ++pass) {
-    const int64_t i = first + (pass * kThreads + threadIdx.x) * kPer;
+    const int64_t i = i0 + pass * (kThreads * kPer);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      if (dst[w] && i < t.n) {
+        c[w][pass] = *reinterpret_cast<const uint2*>(src[w] + i);
+        s[w][pass] = src[w][codes + i / kAdamGroup];
+      }
+  }
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int64_t i = i0 + pass * (kThreads * kPer);
     if (i >= t.n) break;
-    const int64_t q = groups * kAdamGroup + i / kAdamGroup;
-    const uint8_t* mc = static_cast<const uint8_t*>(t.m);
-    const uint8_t* vc = static_cast<const uint8_t*>(t.v);
-    float x[8];
-    if (t.p) {
-      decode8<false>(*reinterpret_cast<const uint2*>(mc + i), mc[q], x);
-      store8(static_cast<__nv_bfloat16*>(t.p), i, t.n, x);
+    uint64_t x[4];
+    if (dst[0]) {
+      decode8<false>(c[0][pass], s[0][pass], x);
+      put8(x, dst[0], i, t.n, i + kPer <= t.n);
     }
-    if (t.master) {
-      decode8<true>(*reinterpret_cast<const uint2*>(vc + i), vc[q], x);
-      store8(reinterpret_cast<__nv_bfloat16*>(t.master), i, t.n, x);
+    if (dst[1]) {
+      decode8<true>(c[1][pass], s[1][pass], x);
+      put8(x, dst[1], i, t.n, i + kPer <= t.n);
     }
   }
 }
@@ -277,16 +485,29 @@ __global__ void __launch_bounds__(kThreads) tpmlp_grad_norm_all(const __grid_con
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     while (c >= a.t[k].end) ++k;
     const AdamTensor& t = a.t[k];
-    const int64_t first = static_cast<int64_t>(c - (k ? a.t[k - 1].end : 0)) * kChunk;
+    const int64_t i0 = static_cast<int64_t>(c - (k ? a.t[k - 1].end : 0)) * kChunk + threadIdx.x * kPer;
+    Eight<G> g[kPasses];
 #pragma unroll
     for (int pass = 0; pass < kPasses; ++pass) {
-      const int64_t i = first + (pass * kThreads + threadIdx.x) * kPer;
-      float g[8], y = 0.0f;
+      const int64_t i = i0 + pass * (kThreads * kPer);
+      g[pass].load(static_cast<const G*>(t.g), i, i + kPer <= t.n);
+    }
+    if (i0 + (kPasses - 1) * (kThreads * kPer) + kPer > t.n) {  // near the tensor's end
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-      if (i < t.n) load8(static_cast<const G*>(t.g), i, t.n, g);
+      for (int pass = 0; pass < kPasses; ++pass) {
+        const int64_t i = i0 + pass * (kThreads * kPer);
+        if (i < t.n && i + kPer > t.n) g[pass].load_tail(static_cast<const G*>(t.g), i, t.n);
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y = fmaf(g[j], g[j], y);
+    for (int pass = 0; pass < kPasses; ++pass) {
+      uint64_t x[4], y2 = 0;
+      g[pass].get(x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y2 = fma2(x[j], x[j], y2);
+      float y, z;
+      upk(y2, y, z);
+      y += z;
       const float sum = s + y, back = sum - s;
       lost += (s - (sum - back)) + (y - back);
       s = sum;
@@ -326,11 +547,10 @@ __global__ void __launch_bounds__(kThreads) tpmlp_grad_norm_all(const __grid_con
 
 using AdamKernel = void (*)(AdamParams);
 
-template <bool k8>
-AdamKernel pick(bool bf16, bool gbf16) {
-  if (bf16) return gbf16 ? tpmlp_adamw_step_all<__nv_bfloat16, __nv_bfloat16, k8>
-                         : tpmlp_adamw_step_all<__nv_bfloat16, float, k8>;
-  return gbf16 ? tpmlp_adamw_step_all<float, __nv_bfloat16, k8> : tpmlp_adamw_step_all<float, float, k8>;
+template <typename G, bool k8>
+AdamKernel pick(bool bf16, bool master) {
+  if (!bf16) return tpmlp_adamw_step_all<float, G, k8, false>;
+  return master ? tpmlp_adamw_step_all<__nv_bfloat16, G, k8, true> : tpmlp_adamw_step_all<__nv_bfloat16, G, k8, false>;
 }
 
 // Ends of the tensors' chunks; their number.
@@ -350,7 +570,9 @@ cudaError_t launch_adamw(AdamParams& a, bool bf16, bool grad_bf16, bool bits8, c
   const int chunks = lay_out(a);
   if (chunks < 0) return cudaErrorInvalidConfiguration;
   if (chunks == 0) return cudaSuccess;
-  const AdamKernel k = bits8 ? pick<true>(bf16, grad_bf16) : pick<false>(bf16, grad_bf16);
+  const bool master = a.t[0].master != nullptr;  // of all tensors or none
+  const AdamKernel k = grad_bf16 ? (bits8 ? pick<__nv_bfloat16, true>(bf16, master) : pick<__nv_bfloat16, false>(bf16, master))
+                                 : (bits8 ? pick<float, true>(bf16, master) : pick<float, false>(bf16, master));
   k<<<chunks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
