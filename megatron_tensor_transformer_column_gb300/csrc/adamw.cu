@@ -161,17 +161,17 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t scale) {
   return (scale + (kSecond ? 96u : 112u) - 91u) << 23;
 }
 
-// 8 codes of a group with this scale byte, as floats.  A word without a zero
-// code (all but a few): a code moved to bits 20.., the sign (of m) to bit 31,
-// and the scale's exponent added.
+// 8 codes of a group with this scale byte, as floats.  Without a zero code (all
+// but a few words) two codes at a time as bf16 numbers: a code's place there is
+// bits 4.., the sign's (of m) bit 15, and the scale's exponent is added.
 template <bool kSecond>
 __device__ __forceinline__ void decode8(uint2 q, uint32_t scale, uint64_t (&x)[4]) {
   constexpr uint32_t kMask = kSecond ? 0xffffffffu : 0x7f7f7f7fu;
   const uint32_t base = scale_bits<kSecond>(scale);
   const uint32_t a = q.x & kMask, b = q.y & kMask;
-  float v[8];
   if ((((a - 0x01010101u) & ~a) | ((b - 0x01010101u) & ~b)) & 0x80808080u) {  // a zero byte
     const float zero = scale == kNanScale ? __uint_as_float(0x7fffffffu) : 0.0f;
+    float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint32_t c = (k < 4 ? q.x : q.y) >> (8 * (k & 3));
@@ -179,20 +179,23 @@ __device__ __forceinline__ void decode8(uint2 q, uint32_t scale, uint64_t (&x)[4
       v[k] = mag ? __uint_as_float((mag << 20) + base) : zero;
       if (!kSecond && (c & 0x80u)) v[k] = -v[k];
     }
-  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t w = k < 4 ? q.x : q.y;
+    for (int k = 0; k < 4; ++k) x[k] = pk(v[2 * k], v[2 * k + 1]);
+  } else {
+    const uint32_t base2 = (base >> 16) * 0x10001u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = k < 2 ? q.x : q.y;
+      uint32_t h;
       if (kSecond) {
-        v[k] = __uint_as_float(__byte_perm(w, 0, 0x4440 | (k & 3)) * (1u << 20) + base);
+        h = __byte_perm(w, 0, k & 1 ? 0x4342 : 0x4140) * 16u + base2;
       } else {
-        const int c = static_cast<int>(__byte_perm(w, 0, 0x0444 | ((k & 3) << 12)));  // the code in the top byte
-        v[k] = __uint_as_float((static_cast<uint32_t>(c >> 4) & 0x87f00000u) + base);
+        const uint32_t c = __byte_perm(w, 0, k & 1 ? 0x3424 : 0x1404);  // the codes in the upper bytes
+        h = ((c & 0x80008000u) | ((c >> 4) & 0x07f007f0u)) + base2;
       }
+      x[k] = pk(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u));
     }
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = pk(v[2 * k], v[2 * k + 1]);
 }
 
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -206,19 +209,19 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return r;
 }
 
-// 8 elements of the warp's group to codes; the scale byte of the group.  r8: the
-// random bits of elements 2 k (low half) and 2 k + 1.  With the group's exponent
-// taken off, bits 20.. of a magnitude are its code; all moved up by 4, so that the
-// code is the top byte (the sign of m falls off at the top) and the random bits
-// stand at 8...
+// 8 elements of the warp's group to codes; the scale byte of the group.  h: the
+// random bits of elements 2 k (low half) and 2 k + 1.  Multiplied by a power of
+// two, the group's numbers have the exponent 128 + c / 8 (m) or 96 + c / 8 (v): so
+// bits 20 .. 27 are the code, and shifted up by 4 it is the top byte (what is
+// above it falls off), under which the random bits stand at 8 .. 23 to round it.
 template <bool kSecond>
 __device__ __forceinline__ uint2 encode8(const uint64_t (&pairs)[4], const uint32_t (&h)[4], uint32_t& scale) {
-  float x[8], m[8];
+  float x[8], y[8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) upk(pairs[k], x[2 * k], x[2 * k + 1]);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m[k] = kSecond ? x[k] : fabsf(x[k]);
-  const float most = max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), max3_nan(m[6], m[7], m[7]));
+  auto mag = [](float v) { return kSecond ? v : fabsf(v); };
+  const float most = max3_nan(max3_nan(mag(x[0]), mag(x[1]), mag(x[2])), max3_nan(mag(x[3]), mag(x[4]), mag(x[5])),
+                              max3_nan(mag(x[6]), mag(x[7]), mag(x[7])));
   const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(most) & 0x7fffffffu);
   const int e = max(static_cast<int>((big + 0xfffffu) >> 23) - 127, -90);
   if (big == 0 || e >= 127) {  // nothing; or a NaN, an infinity or a number beyond 2^127: the group is lost
@@ -226,29 +229,32 @@ __device__ __forceinline__ uint2 encode8(const uint64_t (&pairs)[4], const uint3
     return make_uint2(0, 0);
   }
   scale = static_cast<uint32_t>(e + 91);
-  const uint32_t base = static_cast<uint32_t>(e + (kSecond ? 96 : 112)) << 23;
-  const uint32_t base4 = base << 4;
+  // 2^16 / 2^e: 2^(e - 15) becomes 2; 1 / 2^e: 2^(e - 31) becomes 2^-31
+  const uint64_t up = splat(__uint_as_float(static_cast<uint32_t>((kSecond ? 127 : 143) - e) << 23));
+  constexpr float kLeast = kSecond ? 1.125f * 0x1p-31f : 2.25f;  // the smallest code
   uint32_t z[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t bits = __float_as_uint(x[k]);
-    const uint32_t r8 = __byte_perm(h[k >> 1], 0, k & 1 ? 0x4324 : 0x4104);
-    z[k] = (bits << 4) + (r8 - base4);
-    if (!kSecond) z[k] = (z[k] & 0x7fffffffu) | (bits & 0x80000000u);
+  for (int k = 0; k < 4; ++k) {
+    upk(mul2(pairs[k], up), y[2 * k], y[2 * k + 1]);
+#pragma unroll
+    for (int j = 2 * k; j < 2 * k + 2; ++j) {
+      const uint32_t bits = __float_as_uint(y[j]);
+      z[j] = bits * 16u + __byte_perm(h[k], 0, j & 1 ? 0x4324 : 0x4104);
+      if (!kSecond) z[j] |= bits & 0x80000000u;
+    }
   }
-  const float least = min3(min3(m[0], m[1], m[2]), min3(m[3], m[4], m[5]), fminf(m[6], m[7]));
-  if (__float_as_uint(least) < base + (1u << 20)) {  // below the smallest code, 1.125 2^(e - S)
+  const float least = min3(min3(mag(y[0]), mag(y[1]), mag(y[2])), min3(mag(y[3]), mag(y[4]), mag(y[5])),
+                           fminf(mag(y[6]), mag(y[7])));
+  if (least < kLeast) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t a = __float_as_uint(m[k]);
-      if (a >= base + (1u << 20)) continue;
+      if (mag(y[k]) >= kLeast) continue;
       uint32_t c;
       if (kSecond) {
-        c = a ? 1u : 0u;
+        c = x[k] > 0.0f ? 1u : 0u;
       } else {
         const uint32_t r = k & 1 ? h[k >> 1] >> 16 : h[k >> 1] & 0xffffu;
-        const float t = m[k] * __uint_as_float(static_cast<uint32_t>(142 - e) << 23);  // 2^(S - e) |x|
-        c = t * 65536.0f > static_cast<float>(r) * 1.125f ? 1u : 0u;
+        c = mag(y[k]) * 32768.0f > static_cast<float>(r) * 1.125f ? 1u : 0u;  // y / 2 times 2^16
         c |= (__float_as_uint(x[k]) >> 24) & 0x80u;
       }
       z[k] = c << 24;
