@@ -1161,30 +1161,31 @@ class TokenNorm:
         if not n:
             raise ValueError(_lib.tpmlp_last_error().decode(errors="replace"))
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        self._shape = torch.Size((self.T, self.d))
+        self.device = self.workspace.device
+        self._shape, self._wide = torch.Size((self.T, self.d)), torch.Size((self.d,))
+        self._f32 = torch.float32
 
     def _rows(self, name, x):
         """(address, row stride) of a [T, d] argument."""
-        if x.shape != self._shape or x.dtype != self.tdtype or x.device != self.workspace.device:
-            raise ValueError(f"{name}: expected {tuple(self._shape)} of {self.tdtype} on {self.workspace.device}, got "
+        if x.shape != self._shape or x.dtype != self.tdtype or x.device != self.device:
+            raise ValueError(f"{name}: expected {tuple(self._shape)} of {self.tdtype} on {self.device}, got "
                              f"{tuple(x.shape)} of {x.dtype} on {x.device}")
-        return _rows_apart(name, x)
+        return (x.data_ptr(), self.d) if x.is_contiguous() else _rows_apart(name, x)
 
     def _vector(self, name, x):
-        return None if x is None else _ptr(name, x, (self.d,), self.tdtype, self.workspace.device)
+        return None if x is None else _ptr(name, x, self._wide, self.tdtype, self.device)
 
     def forward(self, x, gain=None, bias=None, residual=None, out=None, stream=None):
         """(y, stats, s): s = x + residual (x itself without one) normed to y; s and stats are what backward takes.
         out: (y, s) to write to; s may be x or residual, y may be x or residual where s is not."""
-        import torch
-        dev = self.workspace.device
+        dev = self.device
         xp, ldx = self._rows("x", x)
         rp, ldr = self._rows("residual", residual) if residual is not None else (None, 0)
         g, b = self._vector("gain", gain), self._vector("bias", bias)
         with _on(dev, stream):
             if out is None:
-                y = torch.empty(self._shape, dtype=self.tdtype, device=dev)
-                s = torch.empty(self._shape, dtype=self.tdtype, device=dev) if residual is not None else x
+                y = x.new_empty(self._shape)
+                s = x.new_empty(self._shape) if residual is not None else x
             else:
                 y, s = out
                 if residual is None and s is not None and s is not x:
@@ -1192,31 +1193,31 @@ class TokenNorm:
                 s = x if residual is None else s
             yp, ldy = self._rows("y", y)
             sp, lds = self._rows("sum", s) if residual is not None else (None, 0)
-            stats = torch.empty((self.T, 2), dtype=torch.float32, device=dev)
-            tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr() or None,
-                               _current(dev))
+            stats = x.new_empty((self.T, 2), dtype=self._f32)
+            _ok(_lib.tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr(),
+                                        _current(dev)), "tpmlp_norm_forward")
         return y, stats, s
 
     def backward(self, x, stats, dy, gain=None, dsum=None, out=None, stream=None, gain_grad=None, bias_grad=False):
         """(dx, dgain, dbias) from the s and stats of forward and the gradients of y and (dsum, optional) of s itself.
         out: the dx to write to, which may be dy, dsum or x.  gain_grad: whether to compute dgain (None: if a gain is
         given)."""
-        import torch
-        dev = self.workspace.device
+        dev = self.device
         xp, ldx = self._rows("x", x)
         dyp, lddy = self._rows("dy", dy)
         dsp, ldds = self._rows("dsum", dsum) if dsum is not None else (None, 0)
-        g, st = self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), torch.float32, dev)
+        g, st = self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), self._f32, dev)
         if gain_grad is None:
             gain_grad = gain is not None
         with _on(dev, stream):
-            dx = torch.empty(self._shape, dtype=self.tdtype, device=dev) if out is None else out
+            dx = x.new_empty(self._shape) if out is None else out
             dxp, lddx = self._rows("out", dx)
-            dgain = torch.empty(self.d, dtype=self.tdtype, device=dev) if gain_grad else None
-            dbias = torch.empty(self.d, dtype=self.tdtype, device=dev) if bias_grad else None
-            tpmlp_norm_backward(self.desc, xp, ldx, st or None, g, dyp, lddy, dsp, ldds, dxp, lddx,
-                                dgain.data_ptr() if gain_grad else None, dbias.data_ptr() if bias_grad else None,
-                                self.workspace.data_ptr(), _current(dev))
+            dgain = x.new_empty(self._wide) if gain_grad else None
+            dbias = x.new_empty(self._wide) if bias_grad else None
+            _ok(_lib.tpmlp_norm_backward(self.desc, xp, ldx, st, g, dyp, lddy, dsp, ldds, dxp, lddx,
+                                         dgain.data_ptr() if gain_grad else None,
+                                         dbias.data_ptr() if bias_grad else None, self.workspace.data_ptr(),
+                                         _current(dev)), "tpmlp_norm_backward")
         return dx, dgain, dbias
 
 
@@ -1265,6 +1266,14 @@ class ShardedAdamW:
         self._moment_shapes = self.shapes if bits == 32 else [(tpmlp_adamw_state_size(8, k),) for k in self.sizes]
         dt = torch.float32 if bits == 32 else torch.uint8
         zeros = lambda: [torch.zeros(s, dtype=dt, device=self.device) for s in self._moment_shapes]
+        # moments(): where each moment starts in one buffer, in 16-byte steps, and the end; those whose part is longer
+        # than they are, or has another shape
+        self._moment_parts = [-(-k // 8) * 8 for k in self.sizes] * 2
+        self._moment_at = [0]
+        for k in self._moment_parts:
+            self._moment_at.append(self._moment_at[-1] + k)
+        self._moment_fix = [(i, k, s) for i, (k, s) in enumerate(zip(self.sizes * 2, self.shapes * 2)) if k % 8 or len(s) != 1]
+        self._hyper = AdamWHyper()
         self._steps = 0
         if capturable:
             self.step_device = torch.zeros((), dtype=torch.int64, device=self.device)
@@ -1301,40 +1310,51 @@ class ShardedAdamW:
         gd = grads[0].dtype
         if gd not in self._descs:
             raise ValueError(f"grads: expected bf16 or fp32, got {gd}")
-        desc = self._descs[gd]
         p = _ptrs("params", self.params, self.shapes, self.tdtype, self.device)
         g = _ptrs("grads", grads, self.shapes, gd, self.device)
         if lr is not None:
             if self.capturable:
                 raise ValueError("capturable: write the learning rate to lr_device")
             self.lr = lr
+        desc, h = self._descs[gd], self._hyper
+        h.lr, (h.beta1, h.beta2), h.eps, h.grad_scale = self.lr, self.betas, self.eps, grad_scale
+        h.step, h.seed, h.max_norm = self._steps + 1, self.seed, self.max_norm or 0.0
         with _on(self.device, stream):
+            st, norm, at = _current(self.device), None, None
             if not self.capturable and torch.cuda.is_current_stream_capturing():
                 raise ValueError("a captured step would repeat one step's number: capturable=True counts on the device")
-            st, norm = _current(self.device), None
-            h = AdamWHyper(self.lr, *self.betas, self.eps, grad_scale, 0.0, self._steps + 1, self.seed)
             if self.max_norm is not None:
-                norm = torch.empty((), dtype=torch.float32, device=self.device)
-                h.max_norm = self.max_norm
-                tpmlp_grad_norm(desc, g, norm.data_ptr(), self.workspace.data_ptr(), st)
+                norm = self.workspace.new_empty((), dtype=torch.float32)
+                at = norm.data_ptr()
+                _ok(_lib.tpmlp_grad_norm(desc, g, at, self.workspace.data_ptr(), st), "tpmlp_grad_norm")
             if self.capturable:
                 self.step_device.add_(1)
                 h.lr_device, h.step_device = self.lr_device.data_ptr(), self.step_device.data_ptr()
-            tpmlp_adamw_step(desc, p, g, self._master, self._m, self._v, self._decay, h,
-                             None if norm is None else norm.data_ptr(), st)
+            _ok(_lib.tpmlp_adamw_step(desc, p, g, self._master, self._m, self._v, self._decay, h, at, st),
+                "tpmlp_adamw_step")
         self._steps += 1
         return norm
 
     def moments(self, stream=None):
         """(m, v): the first and second moments in the parameters' shapes, the fp32 tensors themselves, or, of 8-bit
-        moments, new bf16 tensors (which hold their values exactly)."""
+        moments, new bf16 tensors (which hold their values exactly), parts of one buffer."""
         import torch
         if self.bits == 32:
             return self.m, self.v
+        n = len(self.sizes)
         with _on(self.device, stream):
-            m, v = ([torch.empty(s, dtype=torch.bfloat16, device=self.device) for s in self.shapes] for _ in "mv")
-            tpmlp_adamw8_unpack(self._descs[self.tdtype], self._m, self._v, m, v, _current(self.device))
-        return m, v
+            buf = torch.empty(self._moment_at[-1], dtype=torch.bfloat16, device=self.device)
+            base = buf.data_ptr()
+            at = [base + 2 * a for a in self._moment_at]
+            _ok(_lib.tpmlp_adamw8_unpack(self._descs[self.tdtype], self._m, self._v, (ctypes.c_void_p * n)(*at[:n]),
+                                         (ctypes.c_void_p * n)(*at[n:2 * n]), _current(self.device)),
+                "tpmlp_adamw8_unpack")
+        parts = buf.split(self._moment_parts)
+        if self._moment_fix:
+            parts = list(parts)
+            for k, size, shape in self._moment_fix:
+                parts[k] = parts[k][:size].view(shape)
+        return list(parts[:n]), list(parts[n:])
 
 
 def _make_function():

@@ -22,24 +22,21 @@ constexpr int kThreads = 256; // 32 columns x 8 row groups of 4 rows
 
 // Element (row, col) of a stored row-major array, or of the launch's striped
 // input (token stripes) when `striped`.
-__device__ __forceinline__ float load_elem(const GemmParams& p, const void* base, int64_t ld, bool striped,
-                                           int64_t row, int64_t col) {
+__device__ __forceinline__ const float* elem(const GemmParams& p, const void* base, int64_t ld, bool striped,
+                                             int64_t row, int64_t col) {
   if (striped) {
     const Stripes& st = p.stripes;
     int j = 0;
     while (j + 1 < st.num && row >= st.row0[j + 1]) ++j;
-    return static_cast<const float*>(st.in[j])[(row - st.row0[j]) * st.in_ld + col];
+    return static_cast<const float*>(st.in[j]) + (row - st.row0[j]) * st.in_ld + col;
   }
-  return static_cast<const float*>(base)[row * ld + col];
+  return static_cast<const float*>(base) + row * ld + col;
 }
 
-__device__ __forceinline__ float load_a(const GemmParams& p, const Seg& S, int major, int64_t m, int64_t k) {
-  return major == MAJOR_MN ? load_elem(p, S.a, S.lda, S.a_striped, k, m) : load_elem(p, S.a, S.lda, S.a_striped, m, k);
-}
-
-__device__ __forceinline__ float load_b(const GemmParams& p, const void* b, int64_t ldb, bool striped, int major,
-                                        int64_t k, int64_t n) {
-  return major == MAJOR_MN ? load_elem(p, b, ldb, striped, k, n) : load_elem(p, b, ldb, striped, n, k);
+// Elements (mn, k) of an operand: base is [K x MN] (MAJOR_MN) or [MN x K].
+__device__ __forceinline__ const float* operand(const GemmParams& p, const void* base, int64_t ld, bool striped,
+                                                int major, int64_t mn, int64_t k) {
+  return major == MAJOR_MN ? elem(p, base, ld, striped, k, mn) : elem(p, base, ld, striped, mn, k);
 }
 
 // A value of one lane of a row of 32 columns to and from an 8-bit checkpoint:
@@ -123,9 +120,9 @@ __device__ __forceinline__ void ckpt8_epilogue(const Prob& P, int64_t row0, int6
 }
 
 __global__ void __launch_bounds__(kThreads) tpmlp_fp32_simt_gemm(const __grid_constant__ GemmParams p) {
-  __shared__ float As[kK][kT + 1];   // [k][m]
-  __shared__ float Bs[kK][kT + 1];   // [k][n]
-  __shared__ float B2s[kK][kT + 1];  // [k][n] (SwiGLU up projection)
+  __shared__ __align__(16) float As[kK][kT + 4];  // [k][m], rows of 16 bytes
+  __shared__ float Bs[kK][kT + 1];                // [k][n]
+  __shared__ float B2s[kK][kT + 1];               // [k][n] (SwiGLU up projection)
 
   // tile decode (same raster as the tensor-core path, tile_m = 32)
   const int tile = blockIdx.x;
@@ -149,34 +146,68 @@ __global__ void __launch_bounds__(kThreads) tpmlp_fp32_simt_gemm(const __grid_co
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float acc2[4] = {0.f, 0.f, 0.f, 0.f};
 
-  for (int s = P.seg_begin; s < P.seg_begin + P.seg_count; ++s) {
-    const Seg& S = p.segs[s];
-    for (int k0 = 0; k0 < S.K; k0 += kK) {
-      for (int e = threadIdx.x; e < kT * kK; e += kThreads) {
-        // coalesce along the contiguous dimension of each operand
-        int mm, kk, nn, kb;
-        if (P.a_major == MAJOR_MN) { mm = e & 31; kk = e >> 5; } else { kk = e & 31; mm = e >> 5; }
-        if (P.b_major == MAJOR_MN) { nn = e & 31; kb = e >> 5; } else { kb = e & 31; nn = e >> 5; }
-        const int64_t gm = m0 + mm, gk = k0 + kk, gn = n0 + nn, gkb = k0 + kb;
-        As[kk][mm] = (gm < P.M && gk < S.K) ? load_a(p, S, P.a_major, gm, gk) : 0.f;
-        const bool bin = gn < P.N && gkb < S.K;
-        Bs[kb][nn] = bin ? load_b(p, S.b, S.ldb, S.b_striped, P.b_major, gkb, gn) : 0.f;
-        if (dual) B2s[kb][nn] = bin ? load_b(p, S.b2, S.ldb, false, P.b_major, gkb, gn) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll 8
-      for (int kk = 0; kk < kK; ++kk) {
-        const float b = Bs[kk][tx];
-        const float b2 = dual ? B2s[kk][tx] : 0.f;
+  // A chunk of K travels global memory -> registers -> shared memory, the next
+  // one's loads on their way while this one is worked on, all of a thread's at
+  // once.  (Waiting for each before the next one, 203 x 264 with K = 408 took
+  // 47 us.)  Along the contiguous dimension of each operand lanes are neighbours.
+  constexpr int kLoads = kT * kK / kThreads;
+  float ra[kLoads], rb[kLoads], rb2[kLoads];
+  const int fast = threadIdx.x & 31, slow = threadIdx.x >> 5;
+  auto fetch = [&](const Seg& S, int k0) {
+    const float *pa[kLoads], *pb[kLoads], *pb2[kLoads];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = As[kk][4 * ty + i];
-          acc[i] = fmaf(a, b, acc[i]);
-          if (dual) acc2[i] = fmaf(a, b2, acc2[i]);
-        }
-      }
-      __syncthreads();
+    for (int i = 0; i < kLoads; ++i) {
+      const int other = slow + i * (kThreads / 32);
+      const int64_t m = m0 + (P.a_major == MAJOR_MN ? fast : other), ka = k0 + (P.a_major == MAJOR_MN ? other : fast);
+      const int64_t n = n0 + (P.b_major == MAJOR_MN ? fast : other), kb = k0 + (P.b_major == MAJOR_MN ? other : fast);
+      const bool bin = n < P.N && kb < S.K;
+      pa[i] = m < P.M && ka < S.K ? operand(p, S.a, S.lda, S.a_striped, P.a_major, m, ka) : nullptr;
+      pb[i] = bin ? operand(p, S.b, S.ldb, S.b_striped, P.b_major, n, kb) : nullptr;
+      pb2[i] = bin && dual ? operand(p, S.b2, S.ldb, false, P.b_major, n, kb) : nullptr;
     }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      ra[i] = pa[i] ? *pa[i] : 0.f;
+      rb[i] = pb[i] ? *pb[i] : 0.f;
+      if (dual) rb2[i] = pb2[i] ? *pb2[i] : 0.f;
+    }
+  };
+  int sg = P.seg_begin, k0 = 0;
+  bool more = P.seg_count > 0;
+  if (more) fetch(p.segs[sg], 0);
+  while (more) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int other = slow + i * (kThreads / 32);
+      if (P.a_major == MAJOR_MN) As[other][fast] = ra[i];
+      else As[fast][other] = ra[i];
+      if (P.b_major == MAJOR_MN) Bs[other][fast] = rb[i];
+      else Bs[fast][other] = rb[i];
+      if (dual) {
+        if (P.b_major == MAJOR_MN) B2s[other][fast] = rb2[i];
+        else B2s[fast][other] = rb2[i];
+      }
+    }
+    __syncthreads();
+    k0 += kK;
+    if (k0 >= p.segs[sg].K) {
+      k0 = 0;
+      more = ++sg < P.seg_begin + P.seg_count;
+    }
+    if (more) fetch(p.segs[sg], k0);
+#pragma unroll 8
+    for (int kk = 0; kk < kK; ++kk) {
+      const float b = Bs[kk][tx];
+      const float b2 = dual ? B2s[kk][tx] : 0.f;
+      const float4 a4 = *reinterpret_cast<const float4*>(&As[kk][4 * ty]);
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] = fmaf(a[i], b, acc[i]);
+        if (dual) acc2[i] = fmaf(a[i], b2, acc2[i]);
+      }
+    }
+    __syncthreads();
   }
 
   const int64_t col = n0 + tx;

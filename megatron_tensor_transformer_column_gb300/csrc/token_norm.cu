@@ -212,7 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_fwd(const __grid_const
   TeamSum<W> sum{red + th.team * 2 * W, 1 + th.team, 0};
   const bool add = p.res != nullptr;
   const int S = p.stages;
-  const uint32_t base = ptx::smem_u32(smem) + threadIdx.x * 16, stage_bytes = (add ? 2 : 1) * V * kSlot;
+  // In front of the queue (bf16): the vectors of gain and bias, one copy for all teams.
+  constexpr uint32_t kParamBytes = kGainInSmem<E> ? V * W * 32 * 16 : 0;
+  const uint32_t gains = ptx::smem_u32(smem) + th.t * 16, biases = gains + kParamBytes;
+  const uint32_t base = ptx::smem_u32(smem) + (p.bias ? 2 : 1) * kParamBytes + threadIdx.x * 16;
+  const uint32_t stage_bytes = (add ? 2 : 1) * V * kSlot;
 
   auto fetch = [&](int64_t row, uint32_t stage) {
     if (row < p.rows) {
@@ -234,17 +238,21 @@ __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_fwd(const __grid_const
         ptx::st_shared_v4(slot<V>(base + i * stage_bytes, 0, v), make_uint4(0, 0, 0, 0));
         if (add) ptx::st_shared_v4(slot<V>(base + i * stage_bytes, 1, v), make_uint4(0, 0, 0, 0));
       }
-  for (int i = 0; i + 1 < S; ++i) fetch(th.first + i * th.step, base + i * stage_bytes);
-  uint4 gain[V], bias[V];
+  for (int i = 0; i < S; ++i) fetch(th.first + i * th.step, base + i * stage_bytes);
+  if (kGainInSmem<E>) {
+    // every team writes the same: a thread reads back what it wrote, or the same from another
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    gain[v] = th.param(p.gain, v, kOnes<E>);
-    bias[v] = th.param(p.bias, v, 0);
+    for (int v = 0; v < V; ++v) {
+      ptx::st_shared_v4(gains + v * (W * 32 * 16), th.param(p.gain, v, kOnes<E>));
+      if (p.bias) ptx::st_shared_v4(biases + v * (W * 32 * 16), th.param(p.bias, v, 0));
+    }
   }
+  auto param = [&](const void* src, uint32_t at, int v, uint32_t none) {
+    return kGainInSmem<E> ? ptx::ld_shared_v4(at + v * (W * 32 * 16)) : th.param(src, v, none);
+  };
   int at = 0;
 #pragma unroll 1
   for (int64_t row = th.first; row < p.rows; row += th.step) {
-    fetch(row + (S - 1) * th.step, base + (at == 0 ? S - 1 : at - 1) * stage_bytes);
     copy_wait_all_but(S - 1);
     const uint32_t stage = base + at * stage_bytes;
     at = at + 1 == S ? 0 : at + 1;
@@ -263,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_fwd(const __grid_const
         to_pairs<E>(q, x[v]);
       }
     }
+    fetch(row + S * th.step, stage);  // what lay there is in registers
     float mu = 0.0f;
     if (!p.rms) {
       uint64_t a = 0;
@@ -289,11 +298,17 @@ __global__ void __launch_bounds__(kThreads, 1) tpmlp_norm_fwd(const __grid_const
     char* y = static_cast<char*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      uint64_t g[P], b[P];
-      to_pairs<E>(gain[v], g);
-      to_pairs<E>(bias[v], b);
+      uint64_t g[P];
+      to_pairs<E>(param(p.gain, gains, v, kOnes<E>), g);
+      if (p.bias) {
+        uint64_t b[P];
+        to_pairs<E>(param(p.bias, biases, v, 0), b);
 #pragma unroll
-      for (int e = 0; e < P; ++e) x[v][e] = fma2(mul2(x[v][e], r2), g[e], b[e]);
+        for (int e = 0; e < P; ++e) x[v][e] = fma2(mul2(x[v][e], r2), g[e], b[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < P; ++e) x[v][e] = mul2(mul2(x[v][e], r2), g[e]);
+      }
       if (th.on[v]) *reinterpret_cast<uint4*>(y + th.off(v)) = from_pairs<E>(x[v]);
     }
   }
@@ -462,7 +477,7 @@ Pick pick_one(bool bwd, bool bias) {
           W, V};
 }
 
-// 24 or 32 elements a thread, whichever holds the token with fewer warps to spare.
+// 24 or 32 elements a thread, whichever leaves fewer threads idle.
 template <typename E, int W>
 Pick pick_team(int cols, bool bwd, bool bias) {
   constexpr int V = 32 / kPer<E>;
@@ -471,7 +486,6 @@ Pick pick_team(int cols, bool bwd, bool bias) {
 
 // The team and the vectors a thread holds: up to 32 elements a thread, then up
 // to 16 warps a token.
-
 template <typename E>
 Pick pick(int cols, bool bwd, bool bias) {
   constexpr int V = 32 / kPer<E>;
@@ -491,10 +505,11 @@ cudaError_t launch_norm(NormParams& p, bool bf16, bool bwd, int sms, cudaStream_
   const Pick k = bf16 ? pick<__nv_bfloat16>(p.cols, bwd, p.want_bias) : pick<float>(p.cols, bwd, p.want_bias);
   const int arrays = bwd ? (p.dsum ? 3 : 2) : (p.res ? 2 : 1);
   const int stage = arrays * k.V * kThreads * 16;
-  const int gains = bwd && bf16 ? k.V * kThreads * 16 : 0;
-  p.stages = std::max(1, std::min(kMaxStages, (kMaxSmem - 1024 - gains) / stage));
+  int params = 0;  // gain (and bias) in front of the queue
+  if (bf16) params = bwd ? k.V * kThreads * 16 : (p.bias ? 2 : 1) * k.V * k.W * 32 * 16;
+  p.stages = std::max(1, std::min(kMaxStages, (kMaxSmem - 1024 - params) / stage));
   const int sums = bwd ? kThreads * k.V * (bf16 ? 8 : 4) * 4 : 0;
-  const int bytes = std::max(gains + p.stages * stage, sums);
+  const int bytes = std::max(params + p.stages * stage, sums);
   cudaError_t e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
   if (e != cudaSuccess) return e;
   p.ctas = static_cast<int32_t>(std::min<int64_t>(p.rows, std::min(sms, kNormMaxCtas)));
