@@ -1163,7 +1163,6 @@ class TokenNorm:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
         self.device = self.workspace.device
         self._shape, self._wide = torch.Size((self.T, self.d)), torch.Size((self.d,))
-        self._f32 = torch.float32
 
     def _rows(self, name, x):
         """(address, row stride) of a [T, d] argument."""
@@ -1178,14 +1177,15 @@ class TokenNorm:
     def forward(self, x, gain=None, bias=None, residual=None, out=None, stream=None):
         """(y, stats, s): s = x + residual (x itself without one) normed to y; s and stats are what backward takes.
         out: (y, s) to write to; s may be x or residual, y may be x or residual where s is not."""
+        import torch
         dev = self.device
         xp, ldx = self._rows("x", x)
         rp, ldr = self._rows("residual", residual) if residual is not None else (None, 0)
         g, b = self._vector("gain", gain), self._vector("bias", bias)
         with _on(dev, stream):
             if out is None:
-                y = x.new_empty(self._shape)
-                s = x.new_empty(self._shape) if residual is not None else x
+                y = torch.empty(self._shape, dtype=self.tdtype, device=dev)
+                s = torch.empty(self._shape, dtype=self.tdtype, device=dev) if residual is not None else x
             else:
                 y, s = out
                 if residual is None and s is not None and s is not x:
@@ -1193,7 +1193,7 @@ class TokenNorm:
                 s = x if residual is None else s
             yp, ldy = self._rows("y", y)
             sp, lds = self._rows("sum", s) if residual is not None else (None, 0)
-            stats = x.new_empty((self.T, 2), dtype=self._f32)
+            stats = torch.empty((self.T, 2), dtype=torch.float32, device=dev)
             _ok(_lib.tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr(),
                                         _current(dev)), "tpmlp_norm_forward")
         return y, stats, s
@@ -1202,18 +1202,19 @@ class TokenNorm:
         """(dx, dgain, dbias) from the s and stats of forward and the gradients of y and (dsum, optional) of s itself.
         out: the dx to write to, which may be dy, dsum or x.  gain_grad: whether to compute dgain (None: if a gain is
         given)."""
-        dev = self.device
+        import torch
+        td, dev = self.tdtype, self.device
         xp, ldx = self._rows("x", x)
         dyp, lddy = self._rows("dy", dy)
         dsp, ldds = self._rows("dsum", dsum) if dsum is not None else (None, 0)
-        g, st = self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), self._f32, dev)
+        g, st = self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), torch.float32, dev)
         if gain_grad is None:
             gain_grad = gain is not None
         with _on(dev, stream):
-            dx = x.new_empty(self._shape) if out is None else out
+            dx = torch.empty(self._shape, dtype=td, device=dev) if out is None else out
             dxp, lddx = self._rows("out", dx)
-            dgain = x.new_empty(self._wide) if gain_grad else None
-            dbias = x.new_empty(self._wide) if bias_grad else None
+            dgain = torch.empty(self.d, dtype=td, device=dev) if gain_grad else None
+            dbias = torch.empty(self.d, dtype=td, device=dev) if bias_grad else None
             _ok(_lib.tpmlp_norm_backward(self.desc, xp, ldx, st, g, dyp, lddy, dsp, ldds, dxp, lddx,
                                          dgain.data_ptr() if gain_grad else None,
                                          dbias.data_ptr() if bias_grad else None, self.workspace.data_ptr(),
@@ -1266,13 +1267,15 @@ class ShardedAdamW:
         self._moment_shapes = self.shapes if bits == 32 else [(tpmlp_adamw_state_size(8, k),) for k in self.sizes]
         dt = torch.float32 if bits == 32 else torch.uint8
         zeros = lambda: [torch.zeros(s, dtype=dt, device=self.device) for s in self._moment_shapes]
-        # moments(): where each moment starts in one buffer, in 16-byte steps, and the end; those whose part is longer
-        # than they are, or has another shape
-        self._moment_parts = [-(-k // 8) * 8 for k in self.sizes] * 2
-        self._moment_at = [0]
-        for k in self._moment_parts:
-            self._moment_at.append(self._moment_at[-1] + k)
-        self._moment_fix = [(i, k, s) for i, (k, s) in enumerate(zip(self.sizes * 2, self.shapes * 2)) if k % 8 or len(s) != 1]
+        # moments(): where each moment starts in one buffer (in 16-byte steps) and the end; the parts that the buffer is
+        # split into, those that are moments, and those that need another shape
+        self._moment_at, self._moment_parts, self._moment_is, self._moment_shape = [0], [], [], []
+        for i, (k, s) in enumerate(zip(self.sizes * 2, self.shapes * 2)):
+            self._moment_is.append(len(self._moment_parts))
+            self._moment_parts += [k, -k % 8] if k % 8 else [k]
+            self._moment_at.append(self._moment_at[-1] + k + -k % 8)
+            if len(s) != 1:
+                self._moment_shape.append((i, s))
         self._hyper = AdamWHyper()
         self._steps = 0
         if capturable:
@@ -1324,7 +1327,7 @@ class ShardedAdamW:
             if not self.capturable and torch.cuda.is_current_stream_capturing():
                 raise ValueError("a captured step would repeat one step's number: capturable=True counts on the device")
             if self.max_norm is not None:
-                norm = self.workspace.new_empty((), dtype=torch.float32)
+                norm = torch.empty((), dtype=torch.float32, device=self.device)
                 at = norm.data_ptr()
                 _ok(_lib.tpmlp_grad_norm(desc, g, at, self.workspace.data_ptr(), st), "tpmlp_grad_norm")
             if self.capturable:
@@ -1349,12 +1352,11 @@ class ShardedAdamW:
             _ok(_lib.tpmlp_adamw8_unpack(self._descs[self.tdtype], self._m, self._v, (ctypes.c_void_p * n)(*at[:n]),
                                          (ctypes.c_void_p * n)(*at[n:2 * n]), _current(self.device)),
                 "tpmlp_adamw8_unpack")
-        parts = buf.split(self._moment_parts)
-        if self._moment_fix:
-            parts = list(parts)
-            for k, size, shape in self._moment_fix:
-                parts[k] = parts[k][:size].view(shape)
-        return list(parts[:n]), list(parts[n:])
+        parts = torch.split_with_sizes(buf, self._moment_parts)
+        parts = [parts[i] for i in self._moment_is]
+        for i, shape in self._moment_shape:
+            parts[i] = parts[i].view(shape)
+        return parts[:n], parts[n:]
 
 
 def _make_function():

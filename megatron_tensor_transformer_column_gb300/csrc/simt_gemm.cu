@@ -33,10 +33,54 @@ __device__ __forceinline__ const float* elem(const GemmParams& p, const void* ba
   return static_cast<const float*>(base) + row * ld + col;
 }
 
-// Elements (mn, k) of an operand: base is [K x MN] (MAJOR_MN) or [MN x K].
-__device__ __forceinline__ const float* operand(const GemmParams& p, const void* base, int64_t ld, bool striped,
-                                                int major, int64_t mn, int64_t k) {
-  return major == MAJOR_MN ? elem(p, base, ld, striped, k, mn) : elem(p, base, ld, striped, mn, k);
+constexpr int kLoads = kT * kK / kThreads;  // a thread's elements of a chunk of an operand
+
+// A thread's elements (mn, k) of an operand [K x MN] (MAJOR_MN) or [MN x K], for
+// the chunks of one segment: neighbouring lanes along the contiguous dimension.
+struct Operand {
+  const float* at;   // the thread's first element of the chunk K = 0
+  int64_t apart;     // between its elements
+  int64_t step;      // from a K to the next
+  int mn0, k0;       // its first element; the next ones are 8 further in the other dimension
+  bool mn_major;
+  __device__ __forceinline__ Operand(const void* base, int64_t ld, int major, int64_t tile0) {
+    const int fast = threadIdx.x & 31, slow = threadIdx.x >> 5;
+    mn_major = major == MAJOR_MN;
+    mn0 = static_cast<int>(tile0) + (mn_major ? fast : slow);
+    k0 = mn_major ? slow : fast;
+    step = mn_major ? ld : 1;
+    apart = (kThreads / 32) * ld;
+    at = static_cast<const float*>(base) + (mn_major ? k0 * ld + mn0 : mn0 * ld + k0);
+  }
+  __device__ __forceinline__ void load(int k, int MN, int K, float (&r)[kLoads]) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int more = i * (kThreads / 32);
+      const bool in = mn_major ? mn0 < MN && k + k0 + more < K : mn0 + more < MN && k + k0 < K;
+      r[i] = in ? at[k * step + i * apart] : 0.f;
+    }
+  }
+  // of the launch's striped input
+  __device__ __forceinline__ void load_striped(const GemmParams& p, int k, int MN, int K, float (&r)[kLoads]) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int more = i * (kThreads / 32);
+      const int mn = mn0 + (mn_major ? 0 : more), kk = k + k0 + (mn_major ? more : 0);
+      r[i] = mn < MN && kk < K ? *elem(p, nullptr, 0, true, mn_major ? kk : mn, mn_major ? mn : kk) : 0.f;
+    }
+  }
+};
+
+// An operand's chunk into shared memory, [k][mn] with rows of kLd floats.
+template <int kLd>
+__device__ __forceinline__ void put(float (*s)[kLd], bool mn_major, const float (&r)[kLoads]) {
+  const int fast = threadIdx.x & 31, slow = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int other = slow + i * (kThreads / 32);
+    if (mn_major) s[other][fast] = r[i];
+    else s[fast][other] = r[i];
+  }
 }
 
 // A value of one lane of a row of 32 columns to and from an 8-bit checkpoint:
@@ -149,65 +193,55 @@ __global__ void __launch_bounds__(kThreads) tpmlp_fp32_simt_gemm(const __grid_co
   // A chunk of K travels global memory -> registers -> shared memory, the next
   // one's loads on their way while this one is worked on, all of a thread's at
   // once.  (Waiting for each before the next one, 203 x 264 with K = 408 took
-  // 47 us.)  Along the contiguous dimension of each operand lanes are neighbours.
-  constexpr int kLoads = kT * kK / kThreads;
-  float ra[kLoads], rb[kLoads], rb2[kLoads];
-  const int fast = threadIdx.x & 31, slow = threadIdx.x >> 5;
-  auto fetch = [&](const Seg& S, int k0) {
-    const float *pa[kLoads], *pb[kLoads], *pb2[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int other = slow + i * (kThreads / 32);
-      const int64_t m = m0 + (P.a_major == MAJOR_MN ? fast : other), ka = k0 + (P.a_major == MAJOR_MN ? other : fast);
-      const int64_t n = n0 + (P.b_major == MAJOR_MN ? fast : other), kb = k0 + (P.b_major == MAJOR_MN ? other : fast);
-      const bool bin = n < P.N && kb < S.K;
-      pa[i] = m < P.M && ka < S.K ? operand(p, S.a, S.lda, S.a_striped, P.a_major, m, ka) : nullptr;
-      pb[i] = bin ? operand(p, S.b, S.ldb, S.b_striped, P.b_major, n, kb) : nullptr;
-      pb2[i] = bin && dual ? operand(p, S.b2, S.ldb, false, P.b_major, n, kb) : nullptr;
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      ra[i] = pa[i] ? *pa[i] : 0.f;
-      rb[i] = pb[i] ? *pb[i] : 0.f;
-      if (dual) rb2[i] = pb2[i] ? *pb2[i] : 0.f;
-    }
-  };
-  int sg = P.seg_begin, k0 = 0;
-  bool more = P.seg_count > 0;
-  if (more) fetch(p.segs[sg], 0);
-  while (more) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int other = slow + i * (kThreads / 32);
-      if (P.a_major == MAJOR_MN) As[other][fast] = ra[i];
-      else As[fast][other] = ra[i];
-      if (P.b_major == MAJOR_MN) Bs[other][fast] = rb[i];
-      else Bs[fast][other] = rb[i];
+  // 47 us; working out every element's address anew 35.)
+  const int seg_end = P.seg_begin + P.seg_count;
+  for (int sg = P.seg_begin; sg < seg_end; ++sg) {
+    const Seg& S = p.segs[sg];
+    const int K = S.K;
+    const bool a_striped = S.a_striped, b_striped = S.b_striped;
+    const Operand A(S.a, S.lda, P.a_major, m0), B(S.b, S.ldb, P.b_major, n0), B2(S.b2, S.ldb, P.b_major, n0);
+    float ra[kLoads], rb[kLoads], rb2[kLoads];
+    auto fetch = [&](int k) {
+      if (a_striped) A.load_striped(p, k, P.M, K, ra);
+      else A.load(k, P.M, K, ra);
+      if (b_striped) B.load_striped(p, k, P.N, K, rb);
+      else B.load(k, P.N, K, rb);
+      if (dual) B2.load(k, P.N, K, rb2);
+    };
+    fetch(0);
+    for (int k0 = 0; k0 < K; k0 += kK) {
+      put(As, A.mn_major, ra);
+      put(Bs, B.mn_major, rb);
+      if (dual) put(B2s, B.mn_major, rb2);
+      __syncthreads();
+      if (k0 + kK < K) fetch(k0 + kK);
       if (dual) {
-        if (P.b_major == MAJOR_MN) B2s[other][fast] = rb2[i];
-        else B2s[fast][other] = rb2[i];
-      }
-    }
-    __syncthreads();
-    k0 += kK;
-    if (k0 >= p.segs[sg].K) {
-      k0 = 0;
-      more = ++sg < P.seg_begin + P.seg_count;
-    }
-    if (more) fetch(p.segs[sg], k0);
 #pragma unroll 8
-    for (int kk = 0; kk < kK; ++kk) {
-      const float b = Bs[kk][tx];
-      const float b2 = dual ? B2s[kk][tx] : 0.f;
-      const float4 a4 = *reinterpret_cast<const float4*>(&As[kk][4 * ty]);
-      const float a[4] = {a4.x, a4.y, a4.z, a4.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = fmaf(a[i], b, acc[i]);
-        if (dual) acc2[i] = fmaf(a[i], b2, acc2[i]);
+        for (int kk = 0; kk < kK; ++kk) {
+          const float b = Bs[kk][tx], b2 = B2s[kk][tx];
+          const float4 a = *reinterpret_cast<const float4*>(&As[kk][4 * ty]);
+          acc[0] = fmaf(a.x, b, acc[0]);
+          acc[1] = fmaf(a.y, b, acc[1]);
+          acc[2] = fmaf(a.z, b, acc[2]);
+          acc[3] = fmaf(a.w, b, acc[3]);
+          acc2[0] = fmaf(a.x, b2, acc2[0]);
+          acc2[1] = fmaf(a.y, b2, acc2[1]);
+          acc2[2] = fmaf(a.z, b2, acc2[2]);
+          acc2[3] = fmaf(a.w, b2, acc2[3]);
+        }
+      } else {
+#pragma unroll 8
+        for (int kk = 0; kk < kK; ++kk) {
+          const float b = Bs[kk][tx];
+          const float4 a = *reinterpret_cast<const float4*>(&As[kk][4 * ty]);
+          acc[0] = fmaf(a.x, b, acc[0]);
+          acc[1] = fmaf(a.y, b, acc[1]);
+          acc[2] = fmaf(a.z, b, acc[2]);
+          acc[3] = fmaf(a.w, b, acc[3]);
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 
   const int64_t col = n0 + tx;
