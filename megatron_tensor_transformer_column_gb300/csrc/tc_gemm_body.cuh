@@ -740,16 +740,9 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
           }
         }
       }
-      if (kEpis == EPIS_RESIDUAL && row_ok) {  // this thread's row of the residual stream, likewise
-        const int c0 = part * kCols;
-        const int cn = min(kCols, ti.valid_n - c0);
-        if (cn > 0) {
-          const char* a = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(P.aux1) + grow * P.ldo +
-                                                        ti.n0 + c0);
-          for (int b = 0; b < 2 * cn; b += 128) ptx::prefetch_l2(a + b);
-          ptx::prefetch_l2(a + 2 * cn - 1);
-        }
-      }
+      ResidualBlock<N> res;
+      if constexpr (kEpis == EPIS_RESIDUAL)  // the first chunk's block, while the accumulator is still being computed
+        res.load(P, wrow, P.M, ti.n0 + part * kCols, min(N, ti.valid_n - part * kCols), lane);
       if (!bounded_wait(tfull_bar(acc), acc_phase, ctl, kDevTimeoutEpilogue)) break;
       ptx::tc_fence_after();
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kAccCols);
@@ -819,7 +812,8 @@ __device__ __forceinline__ void tc_gemm_body(const GemmParams& p, uint8_t* smem_
                 add_bias<N>(P.aux0, ti.n0 + col, nvalid, v);
                 store_block<N>(es, p, P, 0, ti.n0 + col, wrow, nvalid, v, lane);
               } else if constexpr (kEpis == EPIS_RESIDUAL) {
-                residual_chunk<N>(p, P, es, grow, ti.n0 + col, wrow, nvalid, v, lane);
+                const int nnext = c < 3 ? min(N, ti.valid_n - col - N) : 0;
+                residual_chunk<N>(p, P, es, res, ti.n0 + col, wrow, nvalid, nnext, v, lane);
               } else if constexpr (kEpis == EPIS_CK8_FWD) {
                 ckpt8_gelu_chunk<N>(p, P, es, row_ok, ti.n0 + col, wrow, nvalid, v, lane);
               } else {

@@ -276,9 +276,7 @@ __device__ __forceinline__ uint32_t stage_off(int r, int g) {
 // Rows grow0 .. grow0 + 31 (valid_rows of them), columns x .. x + N - 1
 // (nvalid of them) of a row-major bf16 array into staging block blk,
 // coalesced: a warp instruction covers 32 / (N / 8) whole rows.
-// kOnce: of an array that this launch may write as well (each element after its
-// reading, by the same warp): loads that keep nothing in L1.
-template <int N, bool kOnce = false>
+template <int N>
 __device__ __forceinline__ void stage_rows(const void* src, int64_t ld, int64_t grow0, int valid_rows, int x,
                                            int nvalid, uint32_t blk, int lane) {
   constexpr int P = N / 8;
@@ -288,11 +286,8 @@ __device__ __forceinline__ void stage_rows(const void* src, int64_t ld, int64_t 
   for (int i = 0; i < P; ++i) {
     const int r = i * RPI + lane / P;
     uint4 q = make_uint4(0, 0, 0, 0);
-    if (r < valid_rows && 8 * g < nvalid) {
-      const uint4* s =
-          reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + (grow0 + r) * ld + x + 8 * g);
-      q = kOnce ? __ldcg(s) : __ldg(s);
-    }
+    if (r < valid_rows && 8 * g < nvalid)
+      q = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(src) + (grow0 + r) * ld + x + 8 * g));
     ptx::st_shared_v4(blk + stage_off<N>(r, g), q);
   }
 }
@@ -553,17 +548,44 @@ __device__ __forceinline__ void epilogue_chunk(const GemmParams& p, const Prob& 
   }
 }
 
-// The plain store of a chunk with the residual stream's block added: it comes in
-// through the block that the sum leaves by.
+// The residual stream's block of a chunk, on its way: whole rows, 16 bytes a lane
+// and step.  The launch may write the same array (each element after its reading,
+// by the same warp), so the loads keep nothing in L1.
 template <int N>
-__device__ __forceinline__ void residual_chunk(const GemmParams& p, const Prob& P, EpiStore& es, int64_t grow, int x,
-                                               int y, int nvalid, float (&acc)[N], int lane) {
+struct ResidualBlock {
+  uint4 q[N / 8];
+  __device__ __forceinline__ void load(const Prob& P, int y, int rows, int x, int nvalid, int lane) {
+    constexpr int kRows = 32 / (N / 8);  // of a step
+    const int r0 = lane / (N / 8), g = lane % (N / 8);
+    const __nv_bfloat16* s = static_cast<const __nv_bfloat16*>(P.aux1) + (static_cast<int64_t>(y) + r0) * P.ldo + x + 8 * g;
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      q[i] = make_uint4(0, 0, 0, 0);
+      if (y + r0 + i * kRows < rows && 8 * g < nvalid)
+        q[i] = __ldcg(reinterpret_cast<const uint4*>(s + static_cast<int64_t>(i) * kRows * P.ldo));
+    }
+  }
+  __device__ __forceinline__ void stage(uint32_t blk, int lane) const {
+    constexpr int kRows = 32 / (N / 8);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+      ptx::st_shared_v4(blk + stage_off<N>(i * kRows + lane / (N / 8), lane % (N / 8)), q[i]);
+  }
+};
+
+// The plain store of a chunk with the residual stream's block added: it passes
+// through the block of shared memory that the sum leaves by.  next: of the chunk
+// after this one (nnext valid columns at xnext), whose loads start here.
+template <int N>
+__device__ __forceinline__ void residual_chunk(const GemmParams& p, const Prob& P, EpiStore& es, ResidualBlock<N>& res,
+                                               int x, int y, int nvalid, int nnext, float (&acc)[N], int lane) {
   if (y >= es.rows) return;
   add_bias<N>(P.aux0, x, nvalid, acc);
   const uint32_t b = es.buf + es.next * epi_block_bytes<N>();
   if (lane == 0) ptx::bulk_wait_group_read<1>();  // the store that last used block b has read it
   __syncwarp();
-  stage_rows<N, true>(P.aux1, P.ldo, grow - lane, es.rows - y, x, nvalid, b, lane);
+  res.stage(b, lane);
+  res.load(P, y, es.rows, x + N, nnext, lane);
   __syncwarp();
   float r[N];
   read_row<N>(b, lane, r);
