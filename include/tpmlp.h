@@ -579,7 +579,7 @@ typedef struct {
 typedef struct {
   double lr, beta1, beta2; /* beta1, beta2 in [0, 1) */
   double eps;              /* > 0 */
-  double grad_scale;       /* finite */
+  double grad_scale;       /* finite, >= 0 */
   double max_norm;         /* 0: no clipping; needs norm otherwise */
   int64_t step;            /* >= 1 (not read with step_device) */
   uint64_t seed;           /* of the 8-bit moments' rounding */
@@ -665,7 +665,8 @@ TPMLP_API const char* tpmlp_last_error(void);
  * projections; 1.03: sequence-parallel layout; 1.04: stream-K tail, larger
  * bf16 workspace; 1.05: tpmlp_last_split_tiles, tpmlp_eval_activation, a
  * 16 KB counter block in the bf16 workspace).  The norm and rotation of the
- * heads and the 8-bit checkpoints were added to 1.05; nothing of it changed. */
+ * heads, the 8-bit checkpoints, the norm of the tokens, the residual in the
+ * row-parallel products and AdamW were added to 1.05; nothing of it changed. */
 TPMLP_API int tpmlp_version(void);
 
 /* Kernel launches the last compute call (tpmlp_forward, tpmlp_backward, a

@@ -1150,7 +1150,8 @@ class TokenNorm:
     """Layer norm or RMS norm of T tokens of d elements in front of a block, with the workspace of its backward pass.
 
     x, residual, sum, y, dy, dsum, dx: [T, d] in the norm's dtype, rows contiguous but possibly further apart than they
-    are long (a column slice); gain, bias: [d]; stats: [T, 2] fp32."""
+    are long (a column slice); gain, bias: [d]; stats: [T, 2] fp32.  Calls of backward share the workspace: on several
+    streams they must be ordered."""
 
     def __init__(self, T: int, d: int, kind: str = "layer", dtype: str = "bf16", eps: float = 1e-5, device=None):
         import torch
@@ -1476,7 +1477,8 @@ def _make_norm_function():
     import torch
 
     def rows(x):
-        return x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+        apart = x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]
+        return x if apart and x.stride(0) * x.element_size() % 16 == 0 else x.contiguous()
 
     class TPMLPNormFunction(torch.autograd.Function):
         """y = TPMLPNormFunction.apply(norm, x, gain, bias), or (y, x + residual) = TPMLPNormFunction.apply(norm, x,
@@ -1497,8 +1499,10 @@ def _make_norm_function():
             s, stats, gain = ctx.saved_tensors
             if dy is None:  # y was not used
                 dy = torch.zeros_like(s)
+            need = ctx.needs_input_grad
             dx, dgain, dbias = ctx.norm.backward(s, stats, rows(dy), gain, None if ds is None else rows(ds),
-                                                 bias_grad=ctx.has_bias)
+                                                 gain_grad=gain is not None and need[2],
+                                                 bias_grad=ctx.has_bias and need[3])
             return (None, dx, dgain, dbias, dx)[:ctx.n]
 
     return TPMLPNormFunction

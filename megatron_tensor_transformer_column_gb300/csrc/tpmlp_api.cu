@@ -2369,7 +2369,8 @@ tpmlp_status adamw_hyper_checks(const tpmlp_adamw_hyper* h, bool has_norm) {
   for (double b : {h->beta1, h->beta2})
     if (!(b >= 0.0 && b < 1.0)) return fail(TPMLP_ERR_INVALID_ARG, "beta1, beta2: %g is not in [0, 1)", b);
   if (!(h->eps > 0.0 && std::isfinite(h->eps))) return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive number", h->eps);
-  if (!std::isfinite(h->grad_scale)) return fail(TPMLP_ERR_INVALID_ARG, "grad_scale = %g is not finite", h->grad_scale);
+  if (!(h->grad_scale >= 0.0 && std::isfinite(h->grad_scale)))
+    return fail(TPMLP_ERR_INVALID_ARG, "grad_scale = %g is not a number from 0 on", h->grad_scale);
   if (!(h->max_norm >= 0.0)) return fail(TPMLP_ERR_INVALID_ARG, "max_norm = %g is below 0", h->max_norm);
   if (h->max_norm > 0.0 && !has_norm) return fail(TPMLP_ERR_INVALID_ARG, "max_norm without a norm");
   if (!h->step_device && h->step < 1)

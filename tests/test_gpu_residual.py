@@ -79,6 +79,8 @@ def test_schedules(gpu_lib, mode):
     check(mlp.row_forward(a["H"], a["W"], b2=a["b2"], residual=a["R"]), a, True, a["R"], True)
     assert bool(gpu_lib.tpmlp_last_split_tiles(gpu_lib.LAUNCH_FWD_ROW)) == (mode != "OFF")
     check(proj.out_forward(a["W"], a["H"], residual=a["R"]), a, False, a["R"], True)
+    R = a["R"].clone()
+    check(proj.out_forward(a["W"], a["H"], residual=R, out=R), a, False, a["R"], True)
     mlp.check()
     proj.check()
 

@@ -286,3 +286,24 @@ def test_autograd(gpu_lib, kind, residual):
             o64 = s64 if k else ref.norm_forward(s64, c["g"], c["b"] if bias is not None else None, kind, EPS)[0]
             v = torch.autograd.grad((o64 * c["dy"].detach()).sum(), c["x"])[0]
             assert all((u.double() - v).abs().max() <= 1e-5 * v.abs().max() for u in got)
+
+
+def test_autograd_of_other_layouts(gpu_lib):
+    """A frozen gain, gradients that arrive expanded or transposed, rows at a distance that is no whole number of 16
+    bytes."""
+    T, d = 24, 64
+    a = make(T, d, "fp32")
+    norm = gpu_lib.TokenNorm(T, d, "layer", "fp32", eps=EPS)
+    want = gpu_lib.TPMLPNormFunction.apply(norm, a["x"], a["g"], a["b"])
+    wide = torch.zeros(T, d + 3, device="cuda")
+    wide[:, :d] = a["x"]
+    x = wide[:, :d].requires_grad_()
+    y = gpu_lib.TPMLPNormFunction.apply(norm, x, a["g"], a["b"])
+    assert torch.equal(y, want)
+    for dy in (torch.ones((), device="cuda").expand(T, d), a["dy"].t().contiguous().t(), a["dy"]):
+        got = torch.autograd.grad(y, x, dy, retain_graph=True)[0]
+        s, stats = norm.forward(a["x"], a["g"], a["b"])[2:0:-1]
+        assert torch.equal(got, norm.backward(s, stats, dy.contiguous(), a["g"])[0])
+        assert gpu_lib.tpmlp_last_launch_count() == 2
+    y.sum().backward()
+    assert a["g"].grad is None and x.grad is not None

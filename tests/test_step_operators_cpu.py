@@ -213,7 +213,7 @@ def test_adamw_descriptions(lib):
         step_call(weight_decay=[0.1])
     nan, inf = float("nan"), float("inf")
     for h in (dict(lr=nan), dict(lr=inf), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=nan), dict(eps=0.0), dict(eps=nan),
-              dict(eps=inf), dict(grad_scale=inf), dict(max_norm=-1.0), dict(max_norm=nan), dict(max_norm=1.0),
+              dict(eps=inf), dict(grad_scale=inf), dict(grad_scale=-1.0), dict(max_norm=-1.0), dict(max_norm=nan), dict(max_norm=1.0),
               dict(step=0), dict(step=-3)):
         assert status_of(lambda: step_call(hyper=h)) == INVALID
     assert status_of(lambda: step_call(hyper=dict(step_device=8 * FAKE + 4))) == ALIGN
