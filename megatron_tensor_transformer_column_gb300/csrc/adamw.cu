@@ -337,7 +337,9 @@ __device__ __forceinline__ void put8(const uint64_t (&x)[4], E* p, int64_t i, in
 
 // kMaster: the fp32 copy is updated, the weight only written.  m and v take one
 // rounding for each product and sum as the formulas have them, so that what the
-// random bits make of them does not depend on how products and sums are fused.
+// random bits make of them does not depend on how products and sums are fused:
+// the assembler fuses an fp32x2 product with the sum behind it although both are
+// .rn, so each product is a sum itself, with a -0 that only the host knows.
 template <typename P, typename G, bool k8, bool kMaster>
 __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(const __grid_constant__ AdamParams a) {
   using M = typename std::conditional<kMaster, float, P>::type;
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(con
     c2 = rsqrtf(-expm1f(static_cast<float>(static_cast<double>(step) * a.ln_b2)));
     key = hash32(hash32(key ^ static_cast<uint32_t>(step)) ^ static_cast<uint32_t>(step >> 32));
   }
-  const uint64_t f2 = splat(f), b1 = splat(a.b1), b1c = splat(a.b1c), b2 = splat(a.b2), b2c = splat(a.b2c);
+  const uint64_t zero = splat(a.minus_zero), f2 = splat(f), b1 = splat(a.b1), b1c = splat(a.b1c), b2 = splat(a.b2), b2c = splat(a.b2c);
   const uint64_t root_scale = splat(c2), eps = splat(a.eps), shrink = splat(-(lr * t.decay)), rate2 = splat(-(lr * rate));
   uint32_t seeds = 0;
   if (k8) {  // lane k: the random bits' start of pass k's group
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(con
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       x[k] = mul2(x[k], f2);
-      m[k] = add2(mul2(m[k], b1), mul2(x[k], b1c));
-      v[k] = add2(mul2(v[k], b2), mul2(mul2(x[k], b2c), x[k]));
+      m[k] = add2(fma2(m[k], b1, zero), fma2(x[k], b1c, zero));
+      v[k] = add2(fma2(v[k], b2, zero), fma2(mul2(x[k], b2c), x[k], zero));
       float lo, hi;
       upk(v[k], lo, hi);
       asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(lo));

@@ -2480,6 +2480,7 @@ tpmlp_status tpmlp_adamw_step(const tpmlp_adamw_desc* desc, void* const* p, cons
     a.eps = static_cast<float>(hyper->eps);
     a.grad_scale = static_cast<float>(hyper->grad_scale);
     a.max_norm = static_cast<float>(hyper->max_norm);
+    a.minus_zero = -0.0f;
     a.key = adam_hash(adam_hash(static_cast<uint32_t>(hyper->seed)) ^ static_cast<uint32_t>(hyper->seed >> 32));
     if (!a.step_dev) {
       a.rate = static_cast<float>(1.0 / -std::expm1(t * a.ln_b1));

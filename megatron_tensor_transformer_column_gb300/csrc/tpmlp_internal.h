@@ -361,6 +361,7 @@ struct AdamParams {
   float b1, b1c, b2, b2c;   // b1c: 1 - b1
   float lr, rate, c2, eps;  // rate = 1 / (1 - b1^t), c2 = (1 - b2^t)^(-1/2)
   float grad_scale, max_norm;
+  float minus_zero;         // -0.0f
   uint32_t key;
   int32_t n;
   int32_t first_batch, more;  // of a norm in several launches
