@@ -730,13 +730,16 @@ def _current(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """A context with the call's device and stream as the current ones, so that what the call allocates belongs to
     that stream.  stream: None (the device's current one), a torch stream or a raw handle (0: the default stream)."""
     import torch
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            return contextlib.nullcontext()
+            return _NOTHING
         return torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         handle = int(stream)
@@ -1162,8 +1165,9 @@ class TokenNorm:
         if not n:
             raise ValueError(_lib.tpmlp_last_error().decode(errors="replace"))
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        self.device = self.workspace.device
+        self.device, self._ws = self.workspace.device, self.workspace.data_ptr()
         self._shape, self._wide = torch.Size((self.T, self.d)), torch.Size((self.d,))
+        self._empty, self._f32 = torch.empty, torch.float32
 
     def _rows(self, name, x):
         """(address, row stride) of a [T, d] argument."""
@@ -1178,23 +1182,30 @@ class TokenNorm:
     def forward(self, x, gain=None, bias=None, residual=None, out=None, stream=None):
         """(y, stats, s): s = x + residual (x itself without one) normed to y; s and stats are what backward takes.
         out: (y, s) to write to; s may be x or residual, y may be x or residual where s is not."""
-        import torch
-        dev = self.device
+        td, dev, empty = self.tdtype, self.device, self._empty
         xp, ldx = self._rows("x", x)
-        rp, ldr = self._rows("residual", residual) if residual is not None else (None, 0)
-        g, b = self._vector("gain", gain), self._vector("bias", bias)
+        rp, ldr = (None, 0) if residual is None else self._rows("residual", residual)
+        g = None if gain is None else self._vector("gain", gain)
+        b = None if bias is None else self._vector("bias", bias)
         with _on(dev, stream):
+            ldy = lds = self.d
+            s, sp = x, None
             if out is None:
-                y = torch.empty(self._shape, dtype=self.tdtype, device=dev)
-                s = torch.empty(self._shape, dtype=self.tdtype, device=dev) if residual is not None else x
+                y = empty(self._shape, dtype=td, device=dev)
+                yp = y.data_ptr()
+                if residual is not None:
+                    s = empty(self._shape, dtype=td, device=dev)
+                    sp = s.data_ptr()
             else:
                 y, s = out
                 if residual is None and s is not None and s is not x:
                     raise ValueError("out: a sum without a residual")
-                s = x if residual is None else s
-            yp, ldy = self._rows("y", y)
-            sp, lds = self._rows("sum", s) if residual is not None else (None, 0)
-            stats = torch.empty((self.T, 2), dtype=torch.float32, device=dev)
+                yp, ldy = self._rows("y", y)
+                if residual is None:
+                    s = x
+                else:
+                    sp, lds = self._rows("sum", s)
+            stats = empty((self.T, 2), dtype=self._f32, device=dev)
             _ok(_lib.tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr(),
                                         _current(dev)), "tpmlp_norm_forward")
         return y, stats, s
@@ -1203,23 +1214,29 @@ class TokenNorm:
         """(dx, dgain, dbias) from the s and stats of forward and the gradients of y and (dsum, optional) of s itself.
         out: the dx to write to, which may be dy, dsum or x.  gain_grad: whether to compute dgain (None: if a gain is
         given)."""
-        import torch
-        td, dev = self.tdtype, self.device
+        td, dev, empty = self.tdtype, self.device, self._empty
         xp, ldx = self._rows("x", x)
         dyp, lddy = self._rows("dy", dy)
-        dsp, ldds = self._rows("dsum", dsum) if dsum is not None else (None, 0)
-        g, st = self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), torch.float32, dev)
+        dsp, ldds = (None, 0) if dsum is None else self._rows("dsum", dsum)
+        g, st = None if gain is None else self._vector("gain", gain), _ptr("stats", stats, (self.T, 2), self._f32, dev)
         if gain_grad is None:
             gain_grad = gain is not None
         with _on(dev, stream):
-            dx = torch.empty(self._shape, dtype=td, device=dev) if out is None else out
-            dxp, lddx = self._rows("out", dx)
-            dgain = torch.empty(self.d, dtype=td, device=dev) if gain_grad else None
-            dbias = torch.empty(self.d, dtype=td, device=dev) if bias_grad else None
-            _ok(_lib.tpmlp_norm_backward(self.desc, xp, ldx, st, g, dyp, lddy, dsp, ldds, dxp, lddx,
-                                         dgain.data_ptr() if gain_grad else None,
-                                         dbias.data_ptr() if bias_grad else None, self.workspace.data_ptr(),
-                                         _current(dev)), "tpmlp_norm_backward")
+            if out is None:
+                dx = empty(self._shape, dtype=td, device=dev)
+                dxp, lddx = dx.data_ptr(), self.d
+            else:
+                dx = out
+                dxp, lddx = self._rows("out", dx)
+            dgain = dbias = dgp = dbp = None
+            if gain_grad:
+                dgain = empty(self.d, dtype=td, device=dev)
+                dgp = dgain.data_ptr()
+            if bias_grad:
+                dbias = empty(self.d, dtype=td, device=dev)
+                dbp = dbias.data_ptr()
+            _ok(_lib.tpmlp_norm_backward(self.desc, xp, ldx, st, g, dyp, lddy, dsp, ldds, dxp, lddx, dgp, dbp,
+                                         self._ws, _current(dev)), "tpmlp_norm_backward")
         return dx, dgain, dbias
 
 
