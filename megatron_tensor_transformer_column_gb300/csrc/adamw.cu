@@ -24,7 +24,18 @@
 //
 // The codes are cut out of the fp32 bits: with the group's exponent taken off,
 // a magnitude's bits 20.. are its code, and adding 16 random bits at bit 4
-// rounds it.  A warp holds one group, 8 elements a lane.
+// rounds it.  A warp holds one group, 8 elements a lane, and takes four groups
+// one after the other, the next one's loads on their way.
+//
+// Bound by HBM with moments in 32 bits (10 to 20 instructions an element of 22 to
+// 30 bytes), by the integer pipe and the issue slots with 8 bits (52 instructions
+// an element of 10 bytes; 74 and 76 % of them taken).  Measured on GB300, six
+// tensors of 22.5 M, and share of the copy bandwidth:
+//   bf16 weights, fp32 masters, 32 bits 543 us (1.0); without masters 426 (1.0)
+//   8 bits: bf16 weights 238 us (0.84), with masters 329 (0.97), fp32 weights 321
+//     (0.99); read out as bf16 118 (1.0)
+//   the norm of bf16 gradients 44 us (0.90), of fp32 ones 80 (0.99)
+// A first version with 82 instructions an element took 435 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
