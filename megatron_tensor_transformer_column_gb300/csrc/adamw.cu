@@ -25,15 +25,16 @@
 // The codes are cut out of the fp32 bits: with the group's exponent taken off,
 // a magnitude's bits 20.. are its code, and adding 16 random bits at bit 4
 // rounds it.  A warp holds one group, 8 elements a lane, and takes four groups
-// one after the other, the next one's loads on their way.
+// one after the other, the next one's loads on their way from L2, where the lines
+// of all four are asked for at the start (238 -> 222 us on the first shape below).
 //
 // Bound by HBM with moments in 32 bits (10 to 20 instructions an element of 22 to
 // 30 bytes), by the integer pipe and the issue slots with 8 bits (52 instructions
-// an element of 10 bytes; 74 and 76 % of them taken).  Measured on GB300, six
+// an element of 10 bytes; 74 and 76 % of them taken before that).  Measured on GB300, six
 // tensors of 22.5 M, and share of the copy bandwidth:
 //   bf16 weights, fp32 masters, 32 bits 543 us (1.0); without masters 426 (1.0)
-//   8 bits: bf16 weights 238 us (0.84), with masters 329 (0.97), fp32 weights 321
-//     (0.99); read out as bf16 118 (1.0)
+//   8 bits: bf16 weights 222 us (0.90), with masters 316 (1.0), fp32 weights 312
+//     (1.0); read out as bf16 118 (1.0)
 //   the norm of bf16 gradients 44 us (0.90), of fp32 ones 80 (0.99)
 // A first version with 82 instructions an element took 435 us.
 #include <cuda_bf16.h>
@@ -43,6 +44,7 @@
 #include <type_traits>
 
 #include "act.cuh"
+#include "ptx.cuh"
 #include "tpmlp_internal.h"
 
 namespace tpmlp {
@@ -93,6 +95,11 @@ __device__ __forceinline__ uint2 load8_if(const void* p, uint32_t go) {
       : "memory");
   return q;
 }
+// Lines of 128 bytes from p on into L2, one a lane.
+__device__ __forceinline__ void prefetch(const void* p, int bytes, int lane) {
+  for (int at = lane * 128; at < bytes; at += 32 * 128) ptx::prefetch_l2(static_cast<const char*>(p) + at);
+}
+
 // 8 elements as they lie in memory.
 template <typename E>
 struct Eight {
@@ -362,6 +369,12 @@ __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(con
   int64_t at = first + warp * (kPasses * kAdamGroup);  // this warp's group, the next one on every pass
   Pass<M, G, k8> now;
   now.load(t, src, at + lane * kPer, true, at + kAdamGroup <= t.n);
+  if (k8 && at + kPasses * kAdamGroup <= t.n) {  // the warp's other groups on their way into L2
+    constexpr int kAll = kPasses * kAdamGroup;
+    prefetch(static_cast<const G*>(t.g) + at, kAll * static_cast<int>(sizeof(G)), lane);
+    prefetch(src + at, kAll * static_cast<int>(sizeof(M)), lane);
+    prefetch((lane & 16 ? static_cast<const uint8_t*>(t.v) : static_cast<const uint8_t*>(t.m)) + at, kAll, lane & 15);
+  }
   uint8_t* ms = static_cast<uint8_t*>(t.m) + codes + at / kAdamGroup;
   uint8_t* vs = static_cast<uint8_t*>(t.v) + codes + at / kAdamGroup;
   const int groups = static_cast<int>(min(static_cast<int64_t>(kPasses), max(int64_t{0}, (codes - at) / kAdamGroup)));
