@@ -1351,8 +1351,10 @@ class ShardedAdamW:
             if self.capturable:
                 self.step_device.add_(1)
                 h.lr_device, h.step_device = self.lr_device.data_ptr(), self.step_device.data_ptr()
-            _ok(_lib.tpmlp_adamw_step(desc, p, g, self._master, self._m, self._v, self._decay, h, at, st),
-                "tpmlp_adamw_step")
+            status = _lib.tpmlp_adamw_step(desc, p, g, self._master, self._m, self._v, self._decay, h, at, st)
+            if status and self.capturable:  # refused: not a step
+                self.step_device.sub_(1)
+            _ok(status, "tpmlp_adamw_step")
         self._steps += 1
         return norm
 
@@ -1361,7 +1363,7 @@ class ShardedAdamW:
         moments, new bf16 tensors (which hold their values exactly), parts of one buffer."""
         import torch
         if self.bits == 32:
-            return self.m, self.v
+            return list(self.m), list(self.v)
         n = len(self.sizes)
         with _on(self.device, stream):
             buf = torch.empty(self._moment_at[-1], dtype=torch.bfloat16, device=self.device)

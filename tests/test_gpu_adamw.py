@@ -412,3 +412,9 @@ def test_refusals_of_the_class(gpu_lib):
             tp.ShardedAdamW(twice).step([torch.ones_like(t) for t in twice])
         assert e.value.status == 1
     assert (y == 0).all()
+    for capturable in (False, True):
+        opt = tp.ShardedAdamW([y], capturable=capturable)
+        opt.step([torch.ones_like(y)])
+        with pytest.raises(tp.TpmlpError):
+            opt.step([y])
+        assert opt.steps == 1  # a refused call is not a step
