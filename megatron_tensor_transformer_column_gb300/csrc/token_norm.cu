@@ -25,12 +25,12 @@
 // launch, each in a fixed order.
 //
 // Measured on GB300, bf16, device time and share of the copy bandwidth:
-//   8192 x 16384: forward 87 us (0.91), with the sum 184 (0.86), backward 133
-//     (0.89), with dsum 160 us (0.98)
-//   8192 x 4096:  26 (0.75), 47 (0.84), 35 (0.85), 45 us (0.88); 32768 x 4096:
-//     93 (0.85), 179 (0.88), 130 (0.91), 156 us (1.01)
-//   8192 x 768 (layer norm with bias): forward with the sum 8.7, backward 12.2 us,
-//     3 of them the second launch
+//   8192 x 16384: forward 84 us (0.94), with the sum 180 (0.87), backward 132
+//     (0.90), with dsum 161 us (0.98)
+//   8192 x 4096:  24 (0.83), 46 (0.86), 34 (0.86), 45 us (0.88); 32768 x 4096:
+//     93 (0.85), 175 (0.90), 129 (0.92), 156 us (1.01)
+//   8192 x 768 (layer norm with bias): forward with the sum 8.4, backward with dsum
+//     12.4 us, 3 of them the second launch; one token of 4096 3.6 and 5.8 us
 // A first version, one element an instruction and with a branch around every
 // vector, took 188 and 243 us on the first shape: bound by issue (33 instructions
 // an element backward, now 22 and half of the issue slots) and by each token's
@@ -62,6 +62,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kMaxStages = 6;
+// Forward, a stage is refilled as soon as it is in registers, and 64 KB on their
+// way to an SM are best: with all of shared memory 8192 x 4096 with the sum takes
+// 48 us instead of 46, 32768 x 4096 180 instead of 174, one token 4.3 instead of
+// 3.6; with less, 65536 x 256 29 instead of 22.  Backward a stage is free only
+// when its token is done: two of them (one: 30 % slower; three: 0 to 3 %).
+constexpr int kFlight = 64 * 1024;
 
 template <typename E>
 constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements of a vector
@@ -525,7 +531,8 @@ cudaError_t launch_norm(NormParams& p, bool bf16, bool bwd, int sms, cudaStream_
   const int stage = arrays * k.V * kThreads * 16;
   int params = 0;  // gain (and bias) in front of the queue
   if (bf16) params = bwd ? k.V * kThreads * 16 : (p.bias ? 2 : 1) * k.V * k.W * 32 * 16;
-  p.stages = std::max(1, std::min(kMaxStages, (kMaxSmem - 1024 - params) / stage));
+  const int fit = (kMaxSmem - 1024 - params) / stage;
+  p.stages = std::max(1, std::min(fit, bwd ? 2 : std::min(kMaxStages, kFlight / stage)));
   const int sums = bwd ? kThreads * k.V * (bf16 ? 8 : 4) * 4 : 0;
   const int bytes = std::max(params + p.stages * stage, sums);
   cudaError_t e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
