@@ -1165,9 +1165,13 @@ class TokenNorm:
         if not n:
             raise ValueError(_lib.tpmlp_last_error().decode(errors="replace"))
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
-        self.device, self._ws = self.workspace.device, self.workspace.data_ptr()
         self._shape, self._wide = torch.Size((self.T, self.d)), torch.Size((self.d,))
         self._empty, self._f32 = torch.empty, torch.float32
+
+    @property
+    def device(self):
+        """The workspace's: a copy, or one that was loaded onto another device, works on its own."""
+        return self.workspace.device
 
     def _rows(self, name, x):
         """(address, row stride) of a [T, d] argument."""
@@ -1206,8 +1210,9 @@ class TokenNorm:
                 else:
                     sp, lds = self._rows("sum", s)
             stats = empty((self.T, 2), dtype=self._f32, device=dev)
-            _ok(_lib.tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr(),
-                                        _current(dev)), "tpmlp_norm_forward")
+            lib = _lib or load()  # an object that was pickled may be the first to need it
+            _ok(lib.tpmlp_norm_forward(self.desc, xp, ldx, rp, ldr, g, b, sp, lds, yp, ldy, stats.data_ptr(),
+                                       _current(dev)), "tpmlp_norm_forward")
         return y, stats, s
 
     def backward(self, x, stats, dy, gain=None, dsum=None, out=None, stream=None, gain_grad=None, bias_grad=False):
@@ -1235,8 +1240,9 @@ class TokenNorm:
             if bias_grad:
                 dbias = empty(self.d, dtype=td, device=dev)
                 dbp = dbias.data_ptr()
-            _ok(_lib.tpmlp_norm_backward(self.desc, xp, ldx, st, g, dyp, lddy, dsp, ldds, dxp, lddx, dgp, dbp,
-                                         self._ws, _current(dev)), "tpmlp_norm_backward")
+            lib = _lib or load()
+            _ok(lib.tpmlp_norm_backward(self.desc, xp, ldx, st, g, dyp, lddy, dsp, ldds, dxp, lddx, dgp, dbp,
+                                        self.workspace.data_ptr(), _current(dev)), "tpmlp_norm_backward")
         return dx, dgain, dbias
 
 
