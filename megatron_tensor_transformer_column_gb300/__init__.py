@@ -1251,7 +1251,7 @@ class ShardedAdamW:
 
     params: contiguous CUDA tensors of one dtype (bf16 or fp32) and device, updated in place.  bits: of a moment, 32 (fp32
     tensors) or 8 (uint8 buffers in the format of include/tpmlp.h).  master: fp32 copies of bf16 parameters, a list or
-    True to make them.  weight_decay: a number, or one per tensor.  max_norm: the gradients' global norm is computed and
+    True to make them.  The tensors in params, master, m and v may be replaced between two steps.  weight_decay: a number, or one per tensor.  max_norm: the gradients' global norm is computed and
     clipped to it (None: no norm; inf: computed, but not clipped); where it is not finite the step changes nothing, but
     counts.
     seed: of the 8-bit moments' rounding.  capturable: the step's number and the learning rate are kept on the
@@ -1281,16 +1281,18 @@ class ShardedAdamW:
             raise ValueError(f"weight_decay: expected {n} numbers, got {len(decay)}")
         self._decay = (ctypes.c_double * n)(*decay)
         self._descs = {g: AdamWDesc(self.sizes, names[self.tdtype], names[g], bits) for g in names}
-        _ptrs("params", self.params, self.shapes, self.tdtype, self.device)
+        self._taken = {}
+        self._addresses("params", self.shapes, self.tdtype)
         if master is True:
             master = [p.detach().float() for p in self.params]
         self.master = list(master) if master else None
-        self._master = _ptrs("master", self.master, self.shapes, torch.float32, self.device) if master else None
-        if master and self.tdtype != torch.bfloat16:
-            raise ValueError("masters of fp32 parameters")
+        if master:
+            self._addresses("master", self.shapes, torch.float32)
+            if self.tdtype != torch.bfloat16:
+                raise ValueError("masters of fp32 parameters")
         self._moment_shapes = self.shapes if bits == 32 else [(tpmlp_adamw_state_size(8, k),) for k in self.sizes]
-        dt = torch.float32 if bits == 32 else torch.uint8
-        zeros = lambda: [torch.zeros(s, dtype=dt, device=self.device) for s in self._moment_shapes]
+        self._moment_type = torch.float32 if bits == 32 else torch.uint8
+        zeros = lambda: [torch.zeros(s, dtype=self._moment_type, device=self.device) for s in self._moment_shapes]
         # moments(): where each moment starts in one buffer (in 16-byte steps) and the end; the parts that the buffer is
         # split into, those that are moments, and those that need another shape
         self._moment_at, self._moment_parts, self._moment_is, self._moment_shape = [0], [], [], []
@@ -1313,13 +1315,25 @@ class ShardedAdamW:
         """Steps done."""
         return int(self.step_device) if self.capturable else self._steps
 
+    def _addresses(self, name, shapes, dtype):
+        """The addresses of self.params, master, m or v as the list stands.  What was checked last is kept alive by
+        tensors of its own, so that the same address is still the same memory and need not be checked again."""
+        xs = getattr(self, name)
+        at, array, _ = self._taken.get(name, (None, None, None))
+        now = [x.data_ptr() for x in xs]
+        if now != at:
+            array = _ptrs(name, xs, shapes, dtype, self.device)
+            self._taken[name] = now, array, [x.detach() for x in xs]
+        return array
+
+    def _moments(self):
+        return [self._addresses(name, self._moment_shapes, self._moment_type) for name in "mv"]
+
     def load_moments(self, m, v, steps=0):
         """Takes these tensors as the moments, in the form that self.m and self.v have, after that many steps."""
-        import torch
-        dt = torch.float32 if self.bits == 32 else torch.uint8
         m, v = list(m), list(v)
-        self._m = _ptrs("m", m, self._moment_shapes, dt, self.device)
-        self._v = _ptrs("v", v, self._moment_shapes, dt, self.device)
+        for name, xs in (("m", m), ("v", v)):
+            _ptrs(name, xs, self._moment_shapes, self._moment_type, self.device)
         self.m, self.v, self._steps = m, v, int(steps)
         if self.capturable:
             self.step_device.fill_(self._steps)
@@ -1337,8 +1351,10 @@ class ShardedAdamW:
         gd = grads[0].dtype
         if gd not in self._descs:
             raise ValueError(f"grads: expected bf16 or fp32, got {gd}")
-        p = _ptrs("params", self.params, self.shapes, self.tdtype, self.device)
+        p = self._addresses("params", self.shapes, self.tdtype)
         g = _ptrs("grads", grads, self.shapes, gd, self.device)
+        master = self._addresses("master", self.shapes, torch.float32) if self.master else None
+        m, v = self._moments()
         if lr is not None:
             if self.capturable:
                 raise ValueError("capturable: write the learning rate to lr_device")
@@ -1357,7 +1373,7 @@ class ShardedAdamW:
             if self.capturable:
                 self.step_device.add_(1)
                 h.lr_device, h.step_device = self.lr_device.data_ptr(), self.step_device.data_ptr()
-            status = _lib.tpmlp_adamw_step(desc, p, g, self._master, self._m, self._v, self._decay, h, at, st)
+            status = _lib.tpmlp_adamw_step(desc, p, g, master, m, v, self._decay, h, at, st)
             if status and self.capturable:  # refused: not a step
                 self.step_device.sub_(1)
             _ok(status, "tpmlp_adamw_step")
@@ -1370,12 +1386,12 @@ class ShardedAdamW:
         import torch
         if self.bits == 32:
             return list(self.m), list(self.v)
-        n = len(self.sizes)
+        n, (mp, vp) = len(self.sizes), self._moments()
         with _on(self.device, stream):
             buf = torch.empty(self._moment_at[-1], dtype=torch.bfloat16, device=self.device)
             base = buf.data_ptr()
             at = [base + 2 * a for a in self._moment_at]
-            _ok(_lib.tpmlp_adamw8_unpack(self._descs[self.tdtype], self._m, self._v, (ctypes.c_void_p * n)(*at[:n]),
+            _ok(_lib.tpmlp_adamw8_unpack(self._descs[self.tdtype], mp, vp, (ctypes.c_void_p * n)(*at[:n]),
                                          (ctypes.c_void_p * n)(*at[n:2 * n]), _current(self.device)),
                 "tpmlp_adamw8_unpack")
         parts = torch.split_with_sizes(buf, self._moment_parts)
