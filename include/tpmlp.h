@@ -529,7 +529,11 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const vo
  *   m = beta1 m + (1 - beta1) f g,   v = beta2 v + (1 - beta2) (f g)^2
  *   p = p - lr weight_decay p
  *         - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32.  A tensor is n elements behind one another (any n, 0 too), its start
+ * in fp32: lr, eps, grad_scale and weight_decay have to be numbers of its range, eps and
+ * a max_norm that is not 0 from 2^-126 on (refused otherwise).  v is held in steps of
+ * 2^-149 at the least: a gradient whose (1 - beta2) (f g)^2 is below that leaves v as it
+ * is, and where eps is far below such a gradient its steps are longer than the
+ * formula's.  A tensor is n elements behind one another (any n, 0 too), its start
  * 16-byte aligned like every tensor here.  dtype is that of the parameters,
  * grad_dtype the gradients'.  master (NULL, or an array; bf16 parameters only): an
  * fp32 copy of each parameter, which is what is updated; the parameter is then
@@ -538,7 +542,8 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const vo
  *
  * tpmlp_grad_norm: norm (one fp32, device) = the root of the sum of the squares
  * of all gradients (without grad_scale), the same on every run; squares in fp32, so
- * that gradients beyond 10^19 give an infinity.  workspace:
+ * that gradients beyond 10^19 give an infinity, and those below 10^-19 lose digits, below
+ * 10^-23 all of them.  workspace:
  * tpmlp_grad_norm_workspace_size() bytes, zero-filled or used by this call before.
  * tpmlp_adamw_step: norm (device, or NULL for no norm) is what that call wrote.
  * A norm that is NaN or an infinity skips the step: nothing is written.
@@ -578,7 +583,7 @@ typedef struct {
 } tpmlp_adamw_desc;
 typedef struct {
   double lr, beta1, beta2; /* beta1, beta2 in [0, 1) */
-  double eps;              /* > 0 */
+  double eps;              /* >= 2^-126 */
   double grad_scale;       /* finite, >= 0 */
   double max_norm;         /* 0: no clipping; needs norm otherwise */
   int64_t step;            /* >= 1 (not read with step_device) */

@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -2363,18 +2364,26 @@ uint32_t adam_hash(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// The kernel has these numbers in fp32: what is finite or above 0 here has to be so there.
+bool finite32(double x) { return std::isfinite(static_cast<float>(x)); }
+bool normal32(double x) { return x >= std::numeric_limits<float>::min() && finite32(x); }
+
 tpmlp_status adamw_hyper_checks(const tpmlp_adamw_hyper* h, bool has_norm) {
   if (!h) return fail(TPMLP_ERR_INVALID_ARG, "hyper is NULL");
-  if (!h->lr_device && !std::isfinite(h->lr)) return fail(TPMLP_ERR_INVALID_ARG, "lr = %g is not finite", h->lr);
+  if (!h->lr_device && !finite32(h->lr)) return fail(TPMLP_ERR_INVALID_ARG, "lr = %g is not finite in fp32", h->lr);
   for (double b : {h->beta1, h->beta2})
     if (!(b >= 0.0 && b < 1.0)) return fail(TPMLP_ERR_INVALID_ARG, "beta1, beta2: %g is not in [0, 1)", b);
-  if (!(h->eps > 0.0 && std::isfinite(h->eps))) return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive number", h->eps);
-  if (!(h->grad_scale >= 0.0 && std::isfinite(h->grad_scale)))
-    return fail(TPMLP_ERR_INVALID_ARG, "grad_scale = %g is not a number from 0 on", h->grad_scale);
-  if (!(h->max_norm >= 0.0)) return fail(TPMLP_ERR_INVALID_ARG, "max_norm = %g is below 0", h->max_norm);
+  if (!normal32(h->eps)) return fail(TPMLP_ERR_INVALID_ARG, "eps = %g is not a positive normal number of fp32", h->eps);
+  if (!(h->grad_scale >= 0.0 && finite32(h->grad_scale)))
+    return fail(TPMLP_ERR_INVALID_ARG, "grad_scale = %g is not an fp32 number from 0 on", h->grad_scale);
+  if (!(h->max_norm == 0.0 || h->max_norm >= std::numeric_limits<float>::min()))
+    return fail(TPMLP_ERR_INVALID_ARG, "max_norm = %g is neither 0 nor a positive normal number of fp32", h->max_norm);
   if (h->max_norm > 0.0 && !has_norm) return fail(TPMLP_ERR_INVALID_ARG, "max_norm without a norm");
   if (!h->step_device && h->step < 1)
     return fail(TPMLP_ERR_INVALID_ARG, "step = %lld is below 1", static_cast<long long>(h->step));
+  if (!h->lr_device && !h->step_device &&
+      !finite32(h->lr / -std::expm1(static_cast<double>(h->step) * std::log(h->beta1))))
+    return fail(TPMLP_ERR_INVALID_ARG, "lr / (1 - beta1^step) is not finite in fp32");
   if ((reinterpret_cast<uintptr_t>(h->step_device) & 7u) || (reinterpret_cast<uintptr_t>(h->lr_device) & 3u))
     return fail(TPMLP_ERR_ALIGNMENT, "step_device or lr_device is not aligned to its size");
   return TPMLP_OK;
@@ -2446,7 +2455,8 @@ tpmlp_status tpmlp_adamw_step(const tpmlp_adamw_desc* desc, void* const* p, cons
   TPMLP_TRY(adamw_hyper_checks(hyper, norm != nullptr));
   if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(TPMLP_ERR_ALIGNMENT, "norm is not 4-byte aligned");
   for (int k = 0; weight_decay && k < desc->n; ++k)
-    if (!std::isfinite(weight_decay[k])) return fail(TPMLP_ERR_INVALID_ARG, "weight_decay[%d] is not finite", k);
+    if (!finite32(weight_decay[k]) || (!hyper->lr_device && !finite32(hyper->lr * weight_decay[k])))
+      return fail(TPMLP_ERR_INVALID_ARG, "weight_decay[%d], or its product with lr, is not finite in fp32", k);
   const int64_t es = bf16 ? 2 : 4, gs = desc->grad_dtype == TPMLP_BF16 ? 2 : 4;
   TPMLP_NO_THROW(
     Spans spans;
