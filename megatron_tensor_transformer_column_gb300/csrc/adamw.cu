@@ -41,6 +41,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "act.cuh"
@@ -353,12 +354,25 @@ __device__ __forceinline__ void put8(const uint64_t (&x)[4], E* p, int64_t i, in
   else out.store_tail(p, i, n);
 }
 
+// kFlush: a v below 2^-126 may be taken for 0, as the faster root does.  The
+// denominator is then less by 2^-63 (1 - b2^t)^(-1/2) at most, a 2^-25th of itself
+// where eps is at least kFlushEps times the first step's correction: half of one
+// fp32 rounding.  A smaller eps takes the root that keeps such a v, three
+// instructions an element more: with 8 bits 222 -> 236 us for 135 M bf16 weights,
+// with 32 bits or masters, which HBM bounds, equal (there always).
+template <bool kFlush>
+__device__ __forceinline__ void root(float& x) {
+  if constexpr (kFlush) asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(x));
+  else asm("sqrt.approx.f32 %0, %0;" : "+f"(x));
+}
+constexpr double kFlushEps = 0x1p-38;
+
 // kMaster: the fp32 copy is updated, the weight only written.  m and v take one
 // rounding for each product and sum as the formulas have them, so that what the
 // random bits make of them does not depend on how products and sums are fused:
 // the assembler fuses an fp32x2 product with the sum behind it although both are
 // .rn, so each product is a sum itself, with a -0 that only the host knows.
-template <typename P, typename G, bool k8, bool kMaster>
+template <typename P, typename G, bool k8, bool kMaster, bool kFlush>
 __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(const __grid_constant__ AdamParams a) {
   using M = typename std::conditional<kMaster, float, P>::type;
   int64_t first;
@@ -429,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(con
       v[k] = add2(fma2(v[k], b2, zero), fma2(mul2(x[k], b2c), x[k], zero));
       float lo, hi;
       upk(v[k], lo, hi);
-      asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(lo));
-      asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(hi));
+      root<kFlush>(lo);
+      root<kFlush>(hi);
       upk(fma2(pk(lo, hi), root_scale, eps), lo, hi);
       asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(lo));
       asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(hi));
@@ -579,10 +593,17 @@ __global__ void __launch_bounds__(kThreads) tpmlp_grad_norm_all(const __grid_con
 
 using AdamKernel = void (*)(AdamParams);
 
-template <typename G, bool k8>
+template <typename G, bool k8, bool kFlush>
 AdamKernel pick(bool bf16, bool master) {
-  if (!bf16) return tpmlp_adamw_step_all<float, G, k8, false>;
-  return master ? tpmlp_adamw_step_all<__nv_bfloat16, G, k8, true> : tpmlp_adamw_step_all<__nv_bfloat16, G, k8, false>;
+  if (!bf16) return tpmlp_adamw_step_all<float, G, k8, false, kFlush>;
+  return master ? tpmlp_adamw_step_all<__nv_bfloat16, G, k8, true, kFlush>
+                : tpmlp_adamw_step_all<__nv_bfloat16, G, k8, false, kFlush>;
+}
+
+template <typename G>
+AdamKernel pick(bool bf16, bool master, bool bits8, bool flush) {
+  if (!bits8) return pick<G, false, false>(bf16, master);
+  return flush ? pick<G, true, true>(bf16, master) : pick<G, true, false>(bf16, master);
 }
 
 // Ends of the tensors' chunks; their number.
@@ -603,8 +624,8 @@ cudaError_t launch_adamw(AdamParams& a, bool bf16, bool grad_bf16, bool bits8, c
   if (chunks < 0) return cudaErrorInvalidConfiguration;
   if (chunks == 0) return cudaSuccess;
   const bool master = a.t[0].master != nullptr;  // of all tensors or none
-  const AdamKernel k = grad_bf16 ? (bits8 ? pick<__nv_bfloat16, true>(bf16, master) : pick<__nv_bfloat16, false>(bf16, master))
-                                 : (bits8 ? pick<float, true>(bf16, master) : pick<float, false>(bf16, master));
+  const bool flush = a.eps >= kFlushEps / std::sqrt(-std::expm1(a.ln_b2));
+  const AdamKernel k = grad_bf16 ? pick<__nv_bfloat16>(bf16, master, bits8, flush) : pick<float>(bf16, master, bits8, flush);
   k<<<chunks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
