@@ -546,7 +546,8 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_desc* desc, const vo
  * 10^-23 all of them.  workspace:
  * tpmlp_grad_norm_workspace_size() bytes, zero-filled or used by this call before.
  * tpmlp_adamw_step: norm (device, or NULL for no norm) is what that call wrote.
- * A norm that is NaN or an infinity skips the step: nothing is written.
+ * A norm that is NaN or an infinity skips the step: nothing is written.  So does one that
+ * grad_scale takes past the fp32 range, unless max_norm clips it.
  *
  * Moments.  TPMLP_ADAMW_32: n fp32 each.  TPMLP_ADAMW_8: groups of 256 elements,
  * the last one filled up with zeros; M a group's largest magnitude and e =

@@ -1252,8 +1252,8 @@ class ShardedAdamW:
     params: contiguous CUDA tensors of one dtype (bf16 or fp32) and device, updated in place.  bits: of a moment, 32 (fp32
     tensors) or 8 (uint8 buffers in the format of include/tpmlp.h).  master: fp32 copies of bf16 parameters, a list or
     True to make them.  The tensors in params, master, m and v may be replaced between two steps.  weight_decay: a number, or one per tensor.  max_norm: the gradients' global norm is computed and
-    clipped to it (None: no norm; inf: computed, but not clipped); where it is not finite the step changes nothing, but
-    counts.
+    clipped to it (None: no norm; inf: computed, but not clipped); where it is not finite, or, without clipping, not after
+    grad_scale, the step changes nothing, but counts.
     seed: of the 8-bit moments' rounding.  capturable: the step's number and the learning rate are kept on the
     device (step_device, lr_device), so that a captured step goes on counting; without it a capture is refused."""
 

@@ -7,7 +7,7 @@
 //   p = p - lr decay p - lr m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps)
 // p is the fp32 master where there is one (the bf16 weight is then written
 // only), else the weight itself, rounded once.  A norm that is not finite skips
-// the step.
+// the step; so does one that grad_scale takes past the range, unless it is clipped.
 //
 // Moments in 8 bits.  Groups of 256 elements; M a group's largest magnitude, e =
 // floor(log2 M), one more where M > 1.875 2^e, at least -90.  A code is a number
@@ -64,6 +64,7 @@ constexpr int kPer = 8;     // elements of a thread and pass
 constexpr int kPasses = 4;  // of a CTA: a warp's consecutive groups, whose scale bytes are one word
 constexpr int kChunk = kThreads * kPer * kPasses;  // elements of a CTA
 constexpr uint32_t kNanScale = 255;
+constexpr float kMost = 3.402823466e38f;  // of fp32's finite numbers
 static_assert(32 * kPer == kAdamGroup && kPasses == 4, "a warp's pass is a group, its chunk's scales a word");
 
 __device__ __forceinline__ uint32_t hash32(uint32_t x) {
@@ -400,9 +401,10 @@ __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(con
 
   float f = a.grad_scale;
   if (a.norm) {
-    const float norm = *a.norm * a.grad_scale;
-    if (!(norm <= 3.402823466e38f)) return;  // NaN or infinity
-    if (a.max_norm > 0.0f && norm > a.max_norm) f *= a.max_norm * __frcp_rn(norm);
+    const float norm = *a.norm, scaled = norm * a.grad_scale;
+    const bool clip = a.max_norm > 0.0f && scaled > a.max_norm, fits = scaled <= kMost;
+    if (!(norm <= kMost) || !(clip || fits)) return;  // NaN, an infinity, or scaled to one that nothing clips
+    if (clip) f = fits ? f * (a.max_norm * __frcp_rn(scaled)) : __fdiv_rn(a.max_norm, norm);
   }
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   float rate = a.rate, c2 = a.c2;
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kThreads) tpmlp_grad_norm_all(const __grid_con
     }
   }
   double d = static_cast<double>(s);
-  if (s <= 3.402823466e38f) d += static_cast<double>(lost);  // an infinite sum loses infinities
+  if (s <= kMost) d += static_cast<double>(lost);  // an infinite sum loses infinities
   __shared__ double parts[kThreads / 32];
   __shared__ bool last;
 #pragma unroll
