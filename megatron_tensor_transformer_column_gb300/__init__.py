@@ -1249,13 +1249,17 @@ class TokenNorm:
 class ShardedAdamW:
     """AdamW over all of a program's tensors at once: the shards' weights, gains, biases.
 
-    params: contiguous CUDA tensors of one dtype (bf16 or fp32) and device, updated in place.  bits: of a moment, 32 (fp32
-    tensors) or 8 (uint8 buffers in the format of include/tpmlp.h).  master: fp32 copies of bf16 parameters, a list or
-    True to make them.  The tensors in params, master, m and v may be replaced between two steps.  weight_decay: a number, or one per tensor.  max_norm: the gradients' global norm is computed and
-    clipped to it (None: no norm; inf: computed, but not clipped); where it is not finite, or, without clipping, not after
-    grad_scale, the step changes nothing, but counts.
-    seed: of the 8-bit moments' rounding.  capturable: the step's number and the learning rate are kept on the
-    device (step_device, lr_device), so that a captured step goes on counting; without it a capture is refused."""
+    params: contiguous CUDA tensors of one dtype (bf16 or fp32) and device, updated in place; a backward pass of a
+    graph recorded before the step that needs the old ones is an error, as with torch's in-place operations.
+    bits: of a moment, 32 (fp32 tensors) or 8 (uint8 buffers in the format of include/tpmlp.h).
+    master: fp32 copies of bf16 parameters, a list or True to make them.  The tensors in params, master, m and v may be
+    replaced between two steps.
+    weight_decay: a number, or one per tensor.
+    max_norm: the gradients' global norm is computed and clipped to it (None: no norm; inf: computed, but not clipped);
+    where it is not finite, or, without clipping, not after grad_scale, the step changes nothing, but counts.
+    seed: of the 8-bit moments' rounding.
+    capturable: the step's number and the learning rate are kept on the device (step_device, lr_device), so that a
+    captured step goes on counting; without it a capture is refused."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, bits=32, master=None,
                  max_norm=None, seed=0, capturable=False):
@@ -1377,6 +1381,8 @@ class ShardedAdamW:
             if status and self.capturable:  # refused: not a step
                 self.step_device.sub_(1)
             _ok(status, "tpmlp_adamw_step")
+        # autograd learns of the writing: a backward pass of an older graph, which needs the old weights, is an error
+        torch.autograd.graph.increment_version(self.params + self.master if self.master else self.params)
         self._steps += 1
         return norm
 
