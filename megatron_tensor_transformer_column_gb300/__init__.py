@@ -1366,6 +1366,9 @@ class ShardedAdamW:
         desc, h = self._descs[gd], self._hyper
         h.lr, (h.beta1, h.beta2), h.eps, h.grad_scale = self.lr, self.betas, self.eps, grad_scale
         h.step, h.seed, h.max_norm = self._steps + 1, self.seed, self.max_norm or 0.0
+        if self.capturable:
+            h.step_device = _ptr("step_device", self.step_device, (), torch.int64, self.device)
+            h.lr_device = _ptr("lr_device", self.lr_device, (), torch.float32, self.device)
         with _on(self.device, stream):
             st, norm, at = _current(self.device), None, None
             if not self.capturable and torch.cuda.is_current_stream_capturing():
@@ -1376,7 +1379,6 @@ class ShardedAdamW:
                 _ok(_lib.tpmlp_grad_norm(desc, g, at, self.workspace.data_ptr(), st), "tpmlp_grad_norm")
             if self.capturable:
                 self.step_device.add_(1)
-                h.lr_device, h.step_device = self.lr_device.data_ptr(), self.step_device.data_ptr()
             status = _lib.tpmlp_adamw_step(desc, p, g, master, m, v, self._decay, h, at, st)
             if status and self.capturable:  # refused: not a step
                 self.step_device.sub_(1)

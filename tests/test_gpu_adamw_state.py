@@ -93,3 +93,23 @@ def test_moments_of_replaced_tensors_are_read_out(gpu_lib):
         xs[2].zero_()
         xs[2] = new
     assert all(torch.equal(a, b) for xs, ys in zip(want, opt.moments()) for a, b in zip(xs, ys))
+
+
+def test_numbers_on_the_device_that_do_not_fit_are_refused(gpu_lib):
+    opt, g = make(gpu_lib, 32, False, capturable=True)
+    opt.step(g)
+    before = [x.clone() for x in state(opt)]
+    for name, good in (("lr_device", opt.lr_device), ("step_device", opt.step_device)):
+        for bad in (good.cpu(), good.double(), good.int(), good.expand(2), good[None]):
+            setattr(opt, name, bad)
+            with pytest.raises(ValueError, match=name):
+                opt.step(g)
+        setattr(opt, name, good)
+    assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(before, state(opt)))
+    opt.lr_device = torch.full((), 2e-3, device="cuda")  # another one that fits is taken
+    opt.step(g)
+    want, _ = make(gpu_lib, 32, False, capturable=True)
+    want.step(g)
+    want.lr_device.fill_(2e-3)
+    want.step(g)
+    assert all(torch.equal(a, b) for a, b in zip(state(want), state(opt)))
