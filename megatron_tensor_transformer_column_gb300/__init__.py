@@ -1409,6 +1409,12 @@ class ShardedAdamW:
         return parts[:n], parts[n:]
 
 
+def _dense(x):
+    """x, or a copy where the library cannot read it as it lies: rows one after the other, its start on 16 bytes."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 def _make_function():
     import torch
 
@@ -1420,7 +1426,8 @@ def _make_function():
             t = mlp.plan.t
             W1_i, W2_i = list(weights[:t]), list(weights[t:2 * t])
             W3_i = list(weights[2 * t:3 * t]) if mlp.swiglu else None
-            Y, saved, H = mlp.forward(X.contiguous(), W1_i, W2_i, W3_i)
+            X = _dense(X)
+            Y, saved, H = mlp.forward(X, W1_i, W2_i, W3_i)
             ctx.mlp = mlp
             ctx.save_for_backward(X, *weights, *saved, *H)
             return Y
@@ -1438,7 +1445,7 @@ def _make_function():
             H = list(tensors[1 + nw + ns:])
             W1_i, W2_i = weights[:t], weights[t:2 * t]
             W3_i = weights[2 * t:] if mlp.swiglu else None
-            g = mlp.backward(X, W1_i, W2_i, saved, H, dY.contiguous(), W3_i)
+            g = mlp.backward(X, W1_i, W2_i, saved, H, _dense(dY), W3_i)
             grads = g["dW1"] + g["dW2"] + (g["dW3"] if mlp.swiglu else [])
             return (None, g["dX"], *grads)
 
@@ -1464,7 +1471,7 @@ def _make_checkpoint_function():
             if len(weights) != n:  # no biases here: a longer list would be computed without its rest
                 names = "W1_i, W2_i, W3_i" if mlp.swiglu else "W1_i, W2_i"
                 raise ValueError(f"expected {n} weights ({names}), got {len(weights)}")
-            X = X.contiguous()
+            X = _dense(X)
             W3_i = list(weights[2 * t:3 * t]) if mlp.swiglu else None
             Y, ckpt = mlp.forward_ckpt8(X, list(weights[:t]), list(weights[t:2 * t]), W3_i)
             ctx.mlp, ctx.nw = mlp, len(weights)
@@ -1479,7 +1486,7 @@ def _make_checkpoint_function():
             X, *rest = ctx.saved_tensors
             weights, ckpt = rest[:nw], rest[nw:]
             W3_i = weights[2 * t:] if mlp.swiglu else None
-            g = mlp.backward_ckpt8(X, weights[:t], weights[t:2 * t], ckpt, dY.contiguous(), W3_i)
+            g = mlp.backward_ckpt8(X, weights[:t], weights[t:2 * t], ckpt, _dense(dY), W3_i)
             return (None, g["dX"], *g["dW1"], *g["dW2"], *(g["dW3"] if mlp.swiglu else []))
 
     return TPMLPCheckpointFunction
@@ -1500,10 +1507,10 @@ def _make_residual_function():
             if len(weights) != n:
                 names = "W1_i, W2_i, W3_i" if mlp.swiglu else "W1_i, W2_i"
                 raise ValueError(f"expected {n} weights ({names}), got {len(weights)}")
-            X = X.contiguous()
+            X = _dense(X)
             W3_i = list(weights[2 * t:]) if mlp.swiglu else None
             Y, ckpt = mlp.forward_ckpt8(X, list(weights[:t]), list(weights[t:2 * t]), W3_i,
-                                        residual=residual.contiguous())
+                                        residual=_dense(residual))
             ctx.mlp, ctx.nw = mlp, n
             ctx.save_for_backward(X, *weights, *ckpt)
             return Y
@@ -1516,7 +1523,7 @@ def _make_residual_function():
             X, *rest = ctx.saved_tensors
             weights, ckpt = rest[:nw], rest[nw:]
             W3_i = weights[2 * t:] if mlp.swiglu else None
-            g = mlp.backward_ckpt8(X, weights[:t], weights[t:2 * t], ckpt, dY.contiguous(), W3_i)
+            g = mlp.backward_ckpt8(X, weights[:t], weights[t:2 * t], ckpt, _dense(dY), W3_i)
             return (None, g["dX"], dY, *g["dW1"], *g["dW2"], *(g["dW3"] if mlp.swiglu else []))
 
     return TPMLPResidualFunction
@@ -1527,7 +1534,8 @@ def _make_norm_function():
 
     def rows(x):
         apart = x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= x.shape[1]
-        return x if apart and x.stride(0) * x.element_size() % 16 == 0 else x.contiguous()
+        whole = apart and x.stride(0) * x.element_size() % 16 == 0 and x.data_ptr() % 16 == 0
+        return x if whole else _dense(x)
 
     class TPMLPNormFunction(torch.autograd.Function):
         """y = TPMLPNormFunction.apply(norm, x, gain, bias), or (y, x + residual) = TPMLPNormFunction.apply(norm, x,
