@@ -483,10 +483,12 @@ TPMLP_API tpmlp_status tpmlp_forward_ckpt8_residual(const tpmlp_plan* plan, cons
  * residual stream's; NULL: none):
  *   w = dy gain,  dx = r (w - mean(w) - n mean(w n)) + dsum   (RMS: without mean(w))
  *   dgain = sum over tokens of dy n,  dbias = sum over tokens of dy
- * All in fp32, each output rounded once to the storage type.  dx is the gradient
- * of x and of the residual alike.  A token with a NaN or an infinity spoils its
- * own outputs and the gradients of gain and bias only; so does one whose squares
- * pass the fp32 range (elements above about 10^17).
+ * All in fp32, each output rounded once to the storage type.  mu is off by a few fp32
+ * roundings of mean|s|, which count in n by r times that: where a mean is 10^4 times
+ * the spread, n has about three digits.  dx is the gradient of x and of the residual
+ * alike.  A token with a NaN or an infinity spoils its own outputs and the gradients of
+ * gain and bias only; so does one whose squares pass the fp32 range (elements above
+ * about 10^17).
  *
  * Arrays are [rows x cols] with row strides ld* >= cols in elements; cols and
  * every ld a multiple of 8 (bf16) / 4 (fp32), cols at most 16384.  gain, bias,
