@@ -1253,7 +1253,7 @@ class ShardedAdamW:
     graph recorded before the step that needs the old ones is an error, as with torch's in-place operations.
     bits: of a moment, 32 (fp32 tensors) or 8 (uint8 buffers in the format of include/tpmlp.h).
     master: fp32 copies of bf16 parameters, a list or True to make them.  The tensors in params, master, m and v may be
-    replaced between two steps.
+    replaced between two steps (a captured step keeps those that it was captured with).
     weight_decay: a number, or one per tensor.
     max_norm: the gradients' global norm is computed and clipped to it (None: no norm; inf: computed, but not clipped);
     where it is not finite, or, without clipping, not after grad_scale, the step changes nothing, but counts.
@@ -1384,7 +1384,7 @@ class ShardedAdamW:
                 self.step_device.sub_(1)
             _ok(status, "tpmlp_adamw_step")
         # autograd learns of the writing: a backward pass of an older graph, which needs the old weights, is an error
-        torch.autograd.graph.increment_version(self.params + self.master if self.master else self.params)
+        torch.autograd.graph.increment_version([*self.params, *(self.master or ())])
         self._steps += 1
         return norm
 
