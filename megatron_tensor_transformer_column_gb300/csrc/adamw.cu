@@ -30,8 +30,12 @@
 //
 // Bound by HBM with moments in 32 bits (10 to 20 instructions an element of 22 to
 // 30 bytes), by the integer pipe and the issue slots with 8 bits (52 instructions
-// an element of 10 bytes; 74 and 76 % of them taken before that).  Measured on GB300, six
-// tensors of 22.5 M, and share of the copy bandwidth:
+// an element of 10 bytes; 74 and 76 % of them taken before that).  The 72 registers that
+// 7 CTAs an SM leave do not hold all of a pass with 8 bits: 32 bytes a thread are
+// spilled with bf16 weights and gradients, up to 140 with masters and fp32
+// gradients; 6 CTAs take 3 % longer.
+//
+// Measured on GB300, six tensors of 22.5 M, and share of the copy bandwidth:
 //   bf16 weights, fp32 masters, 32 bits 543 us (1.0); without masters 426 (1.0)
 //   8 bits: bf16 weights 222 us (0.90), with masters 316 (1.0), fp32 weights 312
 //     (1.0); read out as bf16 118 (1.0)
@@ -67,6 +71,9 @@ constexpr uint32_t kNanScale = 255;
 constexpr float kMost = 3.402823466e38f;  // of fp32's finite numbers
 static_assert(32 * kPer == kAdamGroup && kPasses == 4, "a warp's pass is a group, its chunk's scales a word");
 
+// Two multiplications with xors of the upper bits; the multipliers are those that
+// C. Wellons published in 2018 from a search for 32-bit mixers of low bias.  The
+// host works out a step's key with the same function (adam_hash).
 __device__ __forceinline__ uint32_t hash32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x7feb352du;
   x = (x ^ (x >> 15)) * 0x846ca68bu;
@@ -372,7 +379,8 @@ constexpr double kFlushEps = 0x1p-38;
 // rounding for each product and sum as the formulas have them, so that what the
 // random bits make of them does not depend on how products and sums are fused:
 // the assembler fuses an fp32x2 product with the sum behind it although both are
-// .rn, so each product is a sum itself, with a -0 that only the host knows.
+// .rn, so each product is a sum itself, with a -0 that only the host knows (8 bits,
+// 135 M bf16 weights: 222 us, fused 217; elsewhere equal).
 template <typename P, typename G, bool k8, bool kMaster, bool kFlush>
 __global__ void __launch_bounds__(kThreads, k8 ? 7 : 4) tpmlp_adamw_step_all(const __grid_constant__ AdamParams a) {
   using M = typename std::conditional<kMaster, float, P>::type;

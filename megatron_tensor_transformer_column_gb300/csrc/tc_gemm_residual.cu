@@ -15,6 +15,10 @@
 //   8192 x 11008 by 4096 (8 shards)    412 against 406 us
 //   8192 x 8192 by 2048, unequal       161.5 against 157 us
 //   8192 x (4 x 768) by 768            37 against 35 us
+//   1 to 64 tokens, 4096 by 4096 (8 shards)    25 against 25 us (weights 5)
+//   1 to 64 tokens, 11008 by 4096 (8 shards)   36 against 34 us (weights 13)
+// With few tokens 16 tiles of 256 columns are 16 of 76 pairs at work, each going
+// through all of K: latency-bound, with or without the residual.
 // Fetching a chunk's block when it is due took 161, 421, 165 and 38 us; a
 // prefetch of R into L2 made no difference.
 #include "tc_gemm_body.cuh"

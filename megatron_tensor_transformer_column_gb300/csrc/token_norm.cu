@@ -28,10 +28,15 @@
 // launch, each in a fixed order.
 //
 // Measured on GB300, bf16, device time and share of the copy bandwidth:
-//   8192 x 16384: forward 84 us (0.94), with the sum 180 (0.87), backward 132
-//     (0.90), with dsum 161 us (0.98)
-//   8192 x 4096:  24 (0.83), 46 (0.86), 34 (0.86), 45 us (0.88); 32768 x 4096:
-//     93 (0.85), 175 (0.90), 129 (0.92), 156 us (1.01)
+//   8192 x 16384: forward 84 to 93 us (0.94 to 0.85), with the sum 173 to 180
+//     (0.89), backward 132 (0.90), with dsum 161 us (0.98)
+//   8192 x 4096:  22 to 24 (0.87), 46 (0.86), 35 (0.84), 45 us (0.88); 32768 x
+//     4096: 93 (0.85), 175 (0.90), 129 (0.92), 156 us (1.01)
+//   65536 x 256 (layer norm with bias): 18 (0.55), 23 (0.88), 25 (0.60), 31 us
+//     (0.64); 16384 x 64: 7 us forward, 10 backward (0.1)
+//   fp32, 8192 x 16384: 175 (0.91), 320 (0.99), 259 (0.91), 329 us (0.96); 8192 x
+//     4096: 50 (0.80), 93 (0.86), 71 (0.83), 90 us (0.87); 8192 x 2048 (layer norm
+//     with bias): 25 (0.80), 50 (0.80), 44 (0.67), 54 us (0.74)
 //   8192 x 768 (layer norm with bias): forward with the sum 8.4, backward with dsum
 //     12.4 us, 3 of them the second launch; one token of 4096 3.6 and 5.8 us
 // A first version, one element an instruction and with a branch around every
@@ -39,7 +44,11 @@
 // an element backward, now 22 and half of the issue slots) and by each token's
 // chain of sum, barrier and store.  What bounds it now is HBM where tokens are
 // many; with the sum, two arrays written for two read; with 8192 x 4096 also the
-// launch's ramp and its last round (13.5 tokens a team).  64 elements a thread
+// launch's ramp and its last round (13.5 tokens a team).  Narrow tokens are a warp's
+// each, and 16 warps an SM do not hide a token's chain of wait, sums over the lanes,
+// root and store; below 256 columns lanes are idle as well.  fp32 backward, 8
+// vectors of x and dy a thread fill shared memory, so that there is one stage and
+// a token's loads wait for the token before.  64 elements a thread
 // forward (175 us on 8192 x 16384 with the sum, 2 to 10 % slower elsewhere),
 // streaming stores and L2 prefetch hints (within 1 %) were measured and not kept.
 #include <cuda_bf16.h>
@@ -68,7 +77,7 @@ constexpr int kMaxStages = 6;
 // Forward, a stage is refilled as soon as it is in registers, and 64 KB on their
 // way to an SM are best: with all of shared memory 8192 x 4096 with the sum takes
 // 48 us instead of 46, 32768 x 4096 180 instead of 174, one token 4.3 instead of
-// 3.6; with less, 65536 x 256 29 instead of 22.  Backward a stage is free only
+// 3.6; with less, 65536 x 256 with the sum 29 instead of 22.  Backward a stage is free only
 // when its token is done: two of them (one: 30 % slower; three: 0 to 3 %).
 constexpr int kFlight = 64 * 1024;
 
